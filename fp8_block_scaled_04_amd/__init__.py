@@ -17,4 +17,7 @@ from .binding import (  # noqa: F401
     fp8_jit_default_config, fp8_jit_gemm_nt, fp8_jit_gemm_workspace_bytes, fp8_jit_get_cache_dir,
     fp8_jit_grouped_gemm_contiguous, fp8_jit_grouped_gemm_masked, fp8_jit_set_cache_dir, fp8_jit_stats,
     fp8_jit_warmup,
+    FP8G_GROUP_MAX, FP8G_GROUP_TOP2, FP8G_SIGMOID, FP8G_SOFTMAX, fp8_moe_combine, fp8_moe_combine_backward,
+    fp8_moe_route, fp8_moe_route_backward,
+    FP8G_E2M1, FP8G_INT4, fp8_w4_matvec, fp8_w4_matvec_experts,
 )

@@ -27,6 +27,9 @@ FP8G_OK, FP8G_EINVAL, FP8G_EUNSUPPORTED, FP8G_ELAUNCH, FP8G_ESCRATCH = 0, -1, -2
 FP8G_F32, FP8G_BF16 = 0, 1
 FP8G_E4M3, FP8G_E5M2 = 0, 1
 FP8G_JIT_DENSE, FP8G_JIT_CONTIGUOUS, FP8G_JIT_MASKED = 0, 1, 2
+FP8G_SOFTMAX, FP8G_SIGMOID = 0, 1
+FP8G_GROUP_MAX, FP8G_GROUP_TOP2 = 0, 1
+FP8G_INT4, FP8G_E2M1 = 0, 1
 
 _lib = None
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -79,6 +82,15 @@ _SIGNATURES = {
     "fp8_moe_layout_masked": ([_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "fp8_moe_scatter_rows": ([_vp, _vp, _i64, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _i64, _vp], _i32),
     "fp8_moe_gather_rows": ([_vp, _i32, _i32, _vp, _i32, _vp, _vp], _i32),
+    "fp8_moe_route": ([_vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
+                       _vp], _i32),
+    "fp8_moe_route_backward": ([_vp, _i32, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _i64,
+                                _vp], _i32),
+    "fp8_moe_combine": ([_vp, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp], _i32),
+    "fp8_moe_combine_backward": ([_vp, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp], _i32),
+    "fp8_w4_matvec": ([_vp, _i64, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp], _i32),
+    "fp8_w4_matvec_experts": ([_vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
+                               _i32, _vp], _i32),
 }
 
 
@@ -646,4 +658,199 @@ def fp8_moe_gather_rows(y, dst_row, out, stream=None):
     _same_device(y=y, dst_row=dst_row, out=out)
     st = lib().fp8_moe_gather_rows(_p(y), n, y_rows, _p(dst_row), dst_row.numel(), _p(out), _stream(stream))
     _check("fp8_moe_gather_rows", st)
+    return out
+
+
+# ---- expert routing and the weighted combine --------------------------------------
+_FLOAT_TYPES = {torch.float32: FP8G_F32, torch.bfloat16: FP8G_BF16}
+
+
+def _float_type(t, name):
+    dt = _FLOAT_TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def _rows(t, name):
+    """A matrix whose rows are dense; their stride may exceed their length."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    _want_dim(t, name, 2)
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
+    return t
+
+
+def _ld(t):
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else t.shape[1]
+
+
+def _new(stream, shape, dtype, device):
+    """An output allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def fp8_moe_route(logits, topk, score_func=FP8G_SOFTMAX, bias=None, expert_groups=1, topk_groups=1,
+                  group_score=FP8G_GROUP_MAX, renormalize=False, scale=1.0, expert_idx=None, weights=None,
+                  stream=None):
+    """The topk experts of every token: logits [T][E] (float32 or bfloat16,
+    rows may be strided) -> (expert_idx [T][topk] int32, weights [T][topk]
+    float32), allocated unless given."""
+    dt = _float_type(logits, "logits")
+    T, E = _rows(logits, "logits").shape
+    topk = int(topk)
+    if bias is not None:
+        _want(_f32(bias, "bias"), "bias", (E,))
+    if expert_idx is None:
+        expert_idx = _new(stream, (T, max(topk, 0)), torch.int32, logits.device)
+    if weights is None:
+        weights = _new(stream, (T, max(topk, 0)), torch.float32, logits.device)
+    _want(_i32t(expert_idx, "expert_idx"), "expert_idx", (T, topk))
+    _want(_f32(weights, "weights"), "weights", (T, topk))
+    _same_device(logits=logits, bias=bias, expert_idx=expert_idx, weights=weights)
+    st = lib().fp8_moe_route(_p(logits), dt, _ld(logits), _p(bias), T, E, score_func, expert_groups, topk_groups,
+                             group_score, topk, bool(renormalize), scale, _p(expert_idx), _p(weights),
+                             _stream(stream))
+    _check("fp8_moe_route", st)
+    return expert_idx, weights
+
+
+def fp8_moe_route_backward(logits, expert_idx, grad_weights, grad_logits=None, score_func=FP8G_SOFTMAX,
+                           renormalize=False, scale=1.0, stream=None):
+    """Gradient of the logits [T][E] from that of the weights [T][topk] that
+    fp8_moe_route gave for expert_idx (same score_func, renormalize, scale)."""
+    dt = _float_type(logits, "logits")
+    T, E = _rows(logits, "logits").shape
+    _want_dim(_i32t(expert_idx, "expert_idx"), "expert_idx", 2)
+    topk = expert_idx.shape[1]
+    _want(expert_idx, "expert_idx", (T, topk))
+    _want(_f32(grad_weights, "grad_weights"), "grad_weights", (T, topk))
+    if grad_logits is None:
+        grad_logits = _new(stream, (T, E), logits.dtype, logits.device)
+    if grad_logits.dtype != logits.dtype:
+        raise TypeError(f"grad_logits must be {logits.dtype}, got {grad_logits.dtype}")
+    _want(_rows(grad_logits, "grad_logits"), "grad_logits", (T, E))
+    _same_device(logits=logits, expert_idx=expert_idx, grad_weights=grad_weights, grad_logits=grad_logits)
+    st = lib().fp8_moe_route_backward(_p(logits), dt, _ld(logits), _p(expert_idx), _p(grad_weights), T, E,
+                                      score_func, topk, bool(renormalize), scale, _p(grad_logits),
+                                      _ld(grad_logits), _stream(stream))
+    _check("fp8_moe_route_backward", st)
+    return grad_logits
+
+
+def _check_combine(y, dst_row, weights, tokens, name):
+    """(T, topk, n, y rows) of a combine whose token-side rows are `tokens`."""
+    _want_dim(tokens, name, 2)
+    T, n = tokens.shape
+    if y is not None and (y.dim() < 1 or y.shape[-1] != n):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected rows of {n}")
+    rows = None if y is None else (y.numel() // n if n else 0)
+    topk = None
+    for t, what in ((dst_row, "dst_row"), (weights, "weights")):
+        if t is not None:
+            _want_dim(t, what, 2)
+            topk = t.shape[1] if topk is None else topk
+            _want(t, what, (T, topk))
+    if topk is None:
+        topk = rows // T if T and rows else 1
+    if dst_row is None and rows is not None and n and rows != T * topk:
+        raise ValueError(f"y has {rows} rows, expected {T * topk} without dst_row")
+    return T, topk, n, rows
+
+
+def fp8_moe_combine(y, dst_row, weights, out, stream=None):
+    """out[t] = sum over j of weights[t][j] * y[dst_row[t][j]].  y holds rows
+    of n bfloat16 (any leading shape); dst_row [T][topk] int32 or None (pair p
+    in row p); weights [T][topk] float32 or None (1); out [T][n]."""
+    y, out = _bf16(y, "y"), _bf16(out, "out")
+    if dst_row is not None:
+        _i32t(dst_row, "dst_row")
+    if weights is not None:
+        _f32(weights, "weights")
+    T, topk, n, rows = _check_combine(y, dst_row, weights, out, "out")
+    _same_device(y=y, dst_row=dst_row, weights=weights, out=out)
+    st = lib().fp8_moe_combine(_p(y), rows, n, _p(dst_row), _p(weights), T, topk, _p(out), _stream(stream))
+    _check("fp8_moe_combine", st)
+    return out
+
+
+def fp8_moe_combine_backward(grad_out, y, dst_row, weights, grad_y, grad_weights=None, stream=None):
+    """Gradients of fp8_moe_combine into grad_y (the shape of y; rows no pair
+    names are left as they are) and grad_weights [T][topk] (None: not
+    computed, and y may be None)."""
+    grad_out, grad_y = _bf16(grad_out, "grad_out"), _bf16(grad_y, "grad_y")
+    if dst_row is not None:
+        _i32t(dst_row, "dst_row")
+    if weights is not None:
+        _f32(weights, "weights")
+    T, topk, n, rows = _check_combine(grad_y, dst_row, weights, grad_out, "grad_out")
+    if grad_weights is not None:
+        if y is None:
+            raise ValueError("grad_weights needs y")
+        _want(_bf16(y, "y"), "y", grad_y.shape)
+        _want(_f32(grad_weights, "grad_weights"), "grad_weights", (T, topk))
+    _same_device(grad_out=grad_out, y=y, dst_row=dst_row, weights=weights, grad_y=grad_y, grad_weights=grad_weights)
+    st = lib().fp8_moe_combine_backward(_p(grad_out), _p(y), rows, n, _p(dst_row), _p(weights), T, topk, _p(grad_y),
+                                        _p(grad_weights), _stream(stream))
+    _check("fp8_moe_combine_backward", st)
+    return grad_y, grad_weights
+
+
+# ---- products with 4-bit weights ---------------------------------------------------
+def _check_w4(x, w, scales, zeros, out, lead, rows):
+    """(n, k, group, dtype codes) of a 4-bit product; `lead` = (E,) or ()."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    k = _rows(x, "x").shape[1]
+    if w.dtype != torch.uint8:
+        raise TypeError(f"w must hold pairs of 4-bit codes (uint8), got {w.dtype}")
+    _want_dim(_dev(w, "w"), "w", len(lead) + 2)
+    n = w.shape[-2]
+    _want(w, "w", (*lead, n, k // 2))
+    sd = _float_type(_dev(scales, "scales"), "scales")
+    _want_dim(scales, "scales", len(lead) + 2)
+    groups = scales.shape[-1]
+    if k % 2 or (k and (groups == 0 or k % groups)):
+        raise ValueError(f"{groups} scales per row do not divide {k} columns")
+    _want(scales, "scales", (*lead, n, groups))
+    if zeros is not None:
+        if zeros.dtype != torch.uint8:
+            raise TypeError(f"zeros must be uint8, got {zeros.dtype}")
+        _want(_dev(zeros, "zeros"), "zeros", (*lead, n, groups))
+    od = _float_type(_dev(out, "out"), "out")
+    _want(out, "out", (rows, n))
+    return n, k, k // groups if k else 128, sd, od
+
+
+def fp8_w4_matvec(x, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None):
+    """out [m][n] (bfloat16 or float32) = x [m][k] (bfloat16, rows may be
+    strided) times the transpose of the 4-bit matrix w [n][k / 2] with scales
+    [n][k / group] (float32 or bfloat16) and zero points (uint8, INT4 only)."""
+    m = x.shape[0] if x.dim() else 0
+    n, k, group, sd, od = _check_w4(x, w, scales, zeros, out, (), m)
+    _same_device(x=x, w=w, scales=scales, zeros=zeros, out=out)
+    st = lib().fp8_w4_matvec(_p(x), _ld(x), _p(w), w_format, _p(scales), sd, _p(zeros), group, _p(out), od, m, n, k,
+                             _stream(stream))
+    _check("fp8_w4_matvec", st)
+    return out
+
+
+def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None):
+    """out [P][n]: row p = x row p // (P // x rows) times the matrix of expert
+    expert_idx.view(-1)[p] of w [E][n][k / 2] (scales, zeros [E][n][k /
+    group]); zeros where that is no expert."""
+    P = _i32t(expert_idx, "expert_idx").numel()
+    rows = x.shape[0] if x.dim() else 0
+    if P and (rows == 0 or P % rows):
+        raise ValueError(f"{P} pairs are no multiple of the {rows} rows of x")
+    E = w.shape[0] if w.dim() else 0
+    n, k, group, sd, od = _check_w4(x, w, scales, zeros, out, (E,), P)
+    _same_device(x=x, expert_idx=expert_idx, w=w, scales=scales, zeros=zeros, out=out)
+    st = lib().fp8_w4_matvec_experts(_p(x), _ld(x), rows, _p(expert_idx), P, _p(w), w_format, _p(scales), sd,
+                                     _p(zeros), group, _p(out), od, E, n, k, _stream(stream))
+    _check("fp8_w4_matvec_experts", st)
     return out

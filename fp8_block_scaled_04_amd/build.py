@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8gemm.so")
-SOURCES = [os.path.join(CSRC, "fp8gemm.hip"), os.path.join(CSRC, "moe.hip"), os.path.join(CSRC, "jit.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8gemm.hip", "moe.hip", "moe_ops.hip", "w4.hip", "jit.hip")]
 DENSE_SOURCE = os.path.join(CSRC, "dense_launch.hip")  # compiled once per operand-format pair
 
 # Device code generation; the runtime specialisation compiles with the same.
@@ -59,8 +59,9 @@ def hipcc() -> str:
 
 def _compile_jobs(gen: str, objdir: str):
     """(command, object) per translation unit: the host/grouped/cast unit, the
-    MoE layout unit, the runtime-specialisation unit, and the dense GEMM
-    instantiations once per operand-format pair."""
+    MoE layout unit, the routing and combine unit, the 4-bit unit, the
+    runtime-specialisation unit, and the dense GEMM instantiations once per
+    operand-format pair."""
     base = [hipcc(), *DEVICE_FLAGS, "--offload-arch=gfx950", "-fPIC", "-c", "-I", INCLUDE, "-I", CSRC, "-I", gen]
     jobs = []
     for src in SOURCES:

@@ -1,0 +1,93 @@
+// Weighted sum of the experts' output rows of every token, for gfx950, and
+// its gradients.
+//
+//   out[t]      = bf16( sum over j with 0 <= d_tj < rows of w_tj * y[d_tj] )
+//   grad_y[d]   = bf16( w_tj * grad_out[t] )            for d = d_tj
+//   grad_w[t,j] = < grad_out[t], y[d_tj] >              (0 for a dropped pair)
+// with d_tj = dst_row[t][j], or t * topk + j without one, and w = 1 without
+// weights.  Sums and products are FP32, in a fixed order (no atomics), with
+// one rounding to BF16 at the end.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace fp8g {
+
+__device__ __forceinline__ void unpack8(const v4i& a, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __int_as_float(a[i] << 16);
+    v[2 * i + 1] = __int_as_float(a[i] & 0xffff0000);
+  }
+}
+__device__ __forceinline__ v4i pack8(const float v[8]) {
+  v4i a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = int(pack_bf16x2(v[2 * i], v[2 * i + 1]));
+  return a;
+}
+
+__device__ __forceinline__ int pair_row(const int32_t* dst, int64_t pair, int rows) {
+  const int64_t d = dst ? int64_t(dst[pair]) : pair;
+  return d >= 0 && d < rows ? int(d) : -1;
+}
+
+// Grid: tokens x column blocks of 2048; a thread holds 8 columns.
+__global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __restrict__ y, int rows, int n,
+                                                          const int32_t* __restrict__ dst,
+                                                          const float* __restrict__ weights, int topk,
+                                                          uint16_t* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= n) return;
+  float acc[8] = {};
+  for (int j = 0; j < topk; ++j) {
+    const int d = pair_row(dst, t * topk + j, rows);
+    if (d < 0) continue;
+    const float w = weights ? weights[t * topk + j] : 1.f;
+    float v[8];
+    unpack8(*reinterpret_cast<const v4i*>(y + int64_t(d) * n + c), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  }
+  *reinterpret_cast<v4i*>(out + t * n + c) = pack8(acc);
+}
+
+// One workgroup per token: one pass over its row of grad_out per pair.
+__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_t* __restrict__ grad_out,
+                                                                   const uint16_t* __restrict__ y, int rows, int n,
+                                                                   const int32_t* __restrict__ dst,
+                                                                   const float* __restrict__ weights, int topk,
+                                                                   uint16_t* __restrict__ grad_y,
+                                                                   float* __restrict__ grad_w) {
+  __shared__ float part[4];
+  const int64_t t = blockIdx.x;
+  for (int j = 0; j < topk; ++j) {
+    const int d = pair_row(dst, t * topk + j, rows);
+    const float w = weights ? weights[t * topk + j] : 1.f;
+    float dot = 0.f;
+    if (d >= 0)
+      for (int c = threadIdx.x * 8; c < n; c += 2048) {
+        float g[8], v[8], o[8];
+        unpack8(*reinterpret_cast<const v4i*>(grad_out + t * n + c), g);
+        if (grad_w) {
+          unpack8(*reinterpret_cast<const v4i*>(y + int64_t(d) * n + c), v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = w * g[i];
+        *reinterpret_cast<v4i*>(grad_y + int64_t(d) * n + c) = pack8(o);
+      }
+    if (grad_w) {
+#pragma unroll
+      for (int s = 32; s; s >>= 1) dot += __shfl_xor(dot, s, kWave);
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) grad_w[t * topk + j] = (part[0] + part[1]) + (part[2] + part[3]);
+      __syncthreads();
+    }
+  }
+}
+
+}  // namespace fp8g

@@ -359,6 +359,113 @@ int fp8_moe_scatter_rows(const uint8_t* q, const float* scales, int64_t scales_l
 int fp8_moe_gather_rows(const uint16_t* y, int n, int y_rows, const int32_t* dst_row,
                         int num_tokens, uint16_t* out, void* stream);
 
+/* ---- Expert routing and the weighted combine -------------------------------
+ * What stands before the layout calls (the expert index of every token) and
+ * after the grouped GEMMs (each token's experts' rows, weighted and summed),
+ * with the gradients a training step needs.  The expert index of pair
+ * p = t * topk + j (token t's j-th expert) is what the layout calls take as
+ * expert_idx[p] (num_tokens * topk pairs), and their dst_row[p] is what the
+ * combine takes.  Arrays of these calls need the alignment of their element
+ * (4 bytes; BF16 logits 2) unless stated otherwise. */
+enum { FP8G_SOFTMAX = 0, FP8G_SIGMOID = 1 };       /* score functions */
+enum { FP8G_GROUP_MAX = 0, FP8G_GROUP_TOP2 = 1 };  /* score of a group of experts */
+
+/* The topk experts of every token and their weights.
+ *   logits   [num_tokens] rows of num_experts FP32 or BF16 values
+ *            (logits_dtype FP8G_F32 / FP8G_BF16), row stride logits_ld
+ *            >= num_experts elements
+ *   bias     [num_experts] FP32 or NULL
+ *   scores   s = softmax over the row's logits, or sigmoid of each logit
+ *   picking  by s + bias.  With expert_groups > 1 the experts form that many
+ *            groups of consecutive experts, scored by their largest s + bias
+ *            (FP8G_GROUP_MAX) or the sum of the two largest
+ *            (FP8G_GROUP_TOP2); only experts of the topk_groups best groups
+ *            are picked.  Ties go to the lowest index.
+ *   weights  scale * s of the picked experts (the bias only picks), divided
+ *            by the sum of the picked s with `renormalize`
+ * An expert whose logit is -infinity or NaN, or whose bias is -infinity or
+ * NaN, is never picked; a logit of -infinity adds nothing to the softmax.
+ *   expert_idx [num_tokens][topk] int32, best first; -1 (which routes a pair
+ *              nowhere) where a token has fewer experts left than topk
+ *   weights    [num_tokens][topk] FP32, 0 where expert_idx is -1
+ * Scores are FP32: of two selection scores closer than their rounding either
+ * may come first.  Limits (FP8G_EUNSUPPORTED): num_experts <= 1024, topk <=
+ * 32, expert_groups <= 64.  FP8G_EINVAL: expert_groups does not divide
+ * num_experts, topk exceeds the experts of topk_groups groups. */
+int fp8_moe_route(const void* logits, int logits_dtype, int64_t logits_ld, const float* bias, int num_tokens,
+                  int num_experts, int score_func, int expert_groups, int topk_groups, int group_score, int topk,
+                  int renormalize, float scale, int32_t* expert_idx, float* weights, void* stream);
+
+/* Gradient of the logits of fp8_moe_route, for the picks it made: the
+ * selection is constant, the weights' dependence on the scores (and, for an
+ * un-renormalised softmax, of those on every logit) is differentiated.
+ *   grad_weights [num_tokens][topk] FP32; ignored where expert_idx is -1
+ *   grad_logits  same type as logits, row stride grad_ld >= num_experts;
+ *                every element of the rows is written
+ * An expert_idx outside [0, num_experts) counts as -1. */
+int fp8_moe_route_backward(const void* logits, int logits_dtype, int64_t logits_ld, const int32_t* expert_idx,
+                           const float* grad_weights, int num_tokens, int num_experts, int score_func, int topk,
+                           int renormalize, float scale, void* grad_logits, int64_t grad_ld, void* stream);
+
+/* out[t] = bf16(sum over j of weights[t][j] * y[dst_row[t][j]]): the experts'
+ * rows back in token order.
+ *   y        [y_rows][n] BF16;  out [num_tokens][n] BF16 (written in full)
+ *   dst_row  [num_tokens][topk] int32 rows of y (a row outside [0, y_rows)
+ *            adds nothing and is not read); NULL: pair p sits in row p
+ *   weights  [num_tokens][topk] FP32; NULL: 1
+ * FP32 sums in the order of j, one rounding.  n % 8 == 0; y and out 16-byte
+ * aligned. */
+int fp8_moe_combine(const uint16_t* y, int y_rows, int n, const int32_t* dst_row, const float* weights,
+                    int num_tokens, int topk, uint16_t* out, void* stream);
+
+/* Gradients of fp8_moe_combine:
+ *   grad_y[dst_row[t][j]] = bf16(weights[t][j] * grad_out[t]); rows of grad_y
+ *     that no pair names are not written (clear them once if they are read).
+ *     A row named by two pairs gets one of the two values.
+ *   grad_weights[t][j] = sum of grad_out[t] * y[dst_row[t][j]] (FP32 sum), 0
+ *     for a pair whose row is outside [0, y_rows).  NULL: not computed, and
+ *     y is not read (may be NULL). */
+int fp8_moe_combine_backward(const uint16_t* grad_out, const uint16_t* y, int y_rows, int n, const int32_t* dst_row,
+                             const float* weights, int num_tokens, int topk, uint16_t* grad_y, float* grad_weights,
+                             void* stream);
+
+/* ---- Products with 4-bit weights --------------------------------------------
+ * For decoding: a few rows of BF16 activations against a weight matrix held
+ * in 4 bits with one scale per row and group of 32, 64 or 128 columns.  The
+ * matrix is read once, as it is stored; values are decoded exactly to BF16
+ * operands of the matrix instructions, and the scales are applied to each
+ * group's FP32 sum. */
+enum {
+  FP8G_INT4 = 0,  /* value (code - zero) * scale, code 0..15, zero 8 unless zero points are given */
+  FP8G_E2M1 = 1   /* OCP E2M1 code (sign, 2 exponent bits, 1 mantissa bit: 0 .5 1 1.5 2 3 4 6) * scale */
+};
+
+/* out[m][n] = x[m][k] times the transpose of the 4-bit matrix [n][k].
+ *   x        BF16, row stride x_ld >= k, x_ld % 8 == 0
+ *   w        [n][k / 2] bytes, the even column of a pair in the low 4 bits
+ *   w_scales [n][k / group], FP32 or BF16 (scales_dtype FP8G_F32 / FP8G_BF16)
+ *   w_zeros  [n][k / group] uint8 (FP8G_INT4 only) or NULL
+ *   out      [m][n], BF16 or FP32 (out_dtype)
+ * group 32, 64 or 128 and k % group == 0 (FP8G_EUNSUPPORTED otherwise); any
+ * m and n.  k = 0 gives zeros.  x, w, w_scales, w_zeros, out 16-byte aligned. */
+int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
+                  int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
+                  void* stream);
+
+/* The products of the experts of a decoding step, straight from the routing
+ * (no layout call): row p of out is x row p / (num_pairs / x_rows) times the
+ * matrix of expert expert_idx[p].  x_rows = num_tokens for a projection of
+ * the tokens (topk pairs share a row), x_rows = num_pairs for one of the
+ * pairs' own rows (num_pairs % x_rows must be 0).
+ *   w [num_experts][n][k / 2]; w_scales, w_zeros [num_experts][n][k / group]
+ *   out [num_pairs][n]; a row of zeros where expert_idx[p] is outside
+ *       [0, num_experts)
+ * An expert's matrix is read once for the pairs that share it. */
+int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int32_t* expert_idx, int num_pairs,
+                          const uint8_t* w, int w_format, const void* w_scales, int scales_dtype,
+                          const uint8_t* w_zeros, int group, void* out, int out_dtype, int num_experts, int n, int k,
+                          void* stream);
+
 /* Workspace bytes that let fp8_gemm_nt choose split-K for this shape
  * (0 = never needed).  An upper bound; depends on the CU limit in force. */
 size_t fp8_gemm_workspace_bytes(int m, int n, int k, int num_groups);

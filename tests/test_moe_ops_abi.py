@@ -1,0 +1,82 @@
+"""CPU-only checks of the C entry points of expert routing, the combine and
+the 4-bit products: arguments are refused on the host, before any launch."""
+import ctypes
+import os
+
+import pytest
+
+from fp8_block_scaled_04_amd import binding, build
+
+OK, EINVAL, EUNSUPPORTED = binding.FP8G_OK, binding.FP8G_EINVAL, binding.FP8G_EUNSUPPORTED
+P = ctypes.c_void_p(0x1000)      # an aligned address that is never read
+ODD = ctypes.c_void_p(0x1001)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(build.LIB):
+        build.build()
+    return binding.lib()
+
+
+def _call(fn, args, **over):
+    return fn(*{**args, **over}.values())
+
+
+def test_route_refusals(lib):
+    a = dict(logits=P, dt=0, ld=64, bias=None, T=4, E=64, score=0, groups=1, topk_groups=1, gscore=0, topk=8, renorm=0,
+             scale=1.0, idx=P, w=P, stream=None)
+    f = lib.fp8_moe_route
+    for over in (dict(logits=None), dict(idx=None), dict(w=None), dict(dt=2), dict(ld=63), dict(T=-1), dict(E=0),
+                 dict(score=2), dict(gscore=3), dict(topk=0), dict(topk=65), dict(groups=0), dict(groups=3),
+                 dict(groups=8, topk_groups=9), dict(groups=16, topk_groups=1), dict(logits=ODD), dict(bias=ODD),
+                 dict(idx=ODD), dict(w=ODD), dict(groups=4, topk_groups=0)):
+        assert _call(f, a, **over) == EINVAL, over
+    for over in (dict(E=1025, ld=1025), dict(topk=33), dict(E=130, ld=130, groups=65, topk_groups=8)):
+        assert _call(f, a, **over) == EUNSUPPORTED, over
+    assert _call(f, a, T=0, logits=None) == OK
+    g = dict(logits=P, dt=0, ld=64, idx=P, gw=P, T=4, E=64, score=0, topk=8, renorm=0, scale=1.0, grad=P, gld=64,
+             stream=None)
+    f = lib.fp8_moe_route_backward
+    for over in (dict(logits=None), dict(idx=None), dict(gw=None), dict(grad=None), dict(gld=63), dict(ld=10),
+                 dict(dt=7), dict(T=-2), dict(topk=0), dict(grad=ODD), dict(gw=ODD), dict(score=-1)):
+        assert _call(f, g, **over) == EINVAL, over
+    assert _call(f, g, topk=33) == EUNSUPPORTED
+    assert _call(f, g, T=0) == OK
+
+
+def test_combine_refusals(lib):
+    a = dict(y=P, rows=32, n=64, dst=P, w=P, T=4, topk=8, out=P, stream=None)
+    f = lib.fp8_moe_combine
+    for over in (dict(y=None), dict(out=None), dict(rows=-1), dict(n=-8), dict(T=-1), dict(topk=0), dict(y=ODD),
+                 dict(out=ctypes.c_void_p(0x1008)), dict(dst=ODD), dict(w=ODD)):
+        assert _call(f, a, **over) == EINVAL, over
+    assert _call(f, a, n=12) == EUNSUPPORTED
+    assert _call(f, a, T=0) == OK and _call(f, a, n=0) == OK
+    g = dict(go=P, y=P, rows=32, n=64, dst=P, w=P, T=4, topk=8, gy=P, gw=P, stream=None)
+    f = lib.fp8_moe_combine_backward
+    for over in (dict(go=None), dict(y=None), dict(gy=None), dict(rows=-1), dict(T=-1), dict(topk=0), dict(gw=ODD),
+                 dict(go=ODD), dict(gy=ctypes.c_void_p(0x1008))):
+        assert _call(f, g, **over) == EINVAL, over
+    assert _call(f, g, n=4) == EUNSUPPORTED
+    assert _call(f, g, T=0) == OK and _call(f, g, n=0, gw=None) == OK
+
+
+def test_w4_refusals(lib):
+    a = dict(x=P, ld=256, w=P, fmt=0, s=P, sdt=0, z=None, group=128, out=P, odt=1, m=2, n=16, k=256, stream=None)
+    f = lib.fp8_w4_matvec
+    for over in (dict(x=None), dict(w=None), dict(s=None), dict(out=None), dict(fmt=2), dict(sdt=2), dict(odt=-1),
+                 dict(ld=128), dict(m=-1), dict(n=-1), dict(k=-128), dict(fmt=1, z=P), dict(x=ODD), dict(w=ODD),
+                 dict(s=ctypes.c_void_p(0x1004)), dict(z=ODD), dict(out=ODD)):
+        assert _call(f, a, **over) == EINVAL, over
+    for over in (dict(group=16), dict(group=0), dict(group=256), dict(k=192), dict(ld=260)):
+        assert _call(f, a, **over) == EUNSUPPORTED, over
+    assert _call(f, a, m=0, x=None) == OK and _call(f, a, n=0, out=None) == OK
+    e = dict(x=P, ld=256, rows=2, idx=P, pairs=8, w=P, fmt=0, s=P, sdt=0, z=None, group=128, out=P, odt=1, E=4, n=16,
+             k=256, stream=None)
+    f = lib.fp8_w4_matvec_experts
+    for over in (dict(idx=None), dict(idx=ODD), dict(rows=0), dict(rows=3), dict(rows=-2), dict(pairs=-8), dict(E=0),
+                 dict(x=None), dict(ld=248)):
+        assert _call(f, e, **over) == EINVAL, over
+    assert _call(f, e, group=48) == EUNSUPPORTED
+    assert _call(f, e, pairs=0, rows=0) == OK
