@@ -5,8 +5,14 @@
 //             where there are no zero points)
 //   v(r, c) = e2m1(code(r, c)) * scale(r, c / g)                (E2M1)
 // Codes are packed two to a byte along the row, the even column in the low
-// four bits.  Routed form: pair p = t * topk + j multiplies its row of x with
-// the matrix of expert expert_idx[p]; a row of zeros where that is none.
+// four bits.  Routed form: pair p multiplies its row of x with the matrix of
+// expert expert_idx[p]; a row of zeros where that is none.
+//
+// Each group's sum is formed by BF16 matrix instructions (16 tokens x 16
+// matrix rows x 32 columns): codes 0..15 and E2M1 values are exact in BF16,
+// and the group's scale and zero point are applied to the FP32 sum,
+//     sum (code - zero) * scale * x = scale * (sum code * x - zero * sum x),
+// with sum x from the same instruction against ones.
 #pragma once
 
 #include "device_common.hpp"
@@ -14,6 +20,9 @@
 namespace fp8g {
 
 constexpr int kW4Int4 = 0, kW4E2M1 = 1;
+constexpr int kW4Waves = 8;     // per workgroup, at most (4 where k is split less: two workgroups fit a CU)
+constexpr int kW4Window = 512;   // pairs searched at a time for an expert's tokens
+constexpr int kW4LdsBytes = 156 * 1024;  // rings of a workgroup, at most (160 KB per CU)
 
 struct W4Args {
   const uint16_t* x;
@@ -22,61 +31,377 @@ struct W4Args {
   const void* scales;
   const uint8_t* zeros;
   void* out;
-  int m, n, k, group;
-  const int32_t* expert_idx;  // routed form
+  int scales_bf16, out_f32;
+  int m, n, k;                // m: tokens, or pairs in the routed form
+  const int32_t* expert_idx;  // routed form, else NULL
   int experts, x_div;         // experts; pairs per row of x
+  int by_pair;                // routed form: a workgroup row per pair (else per expert)
+  // set at the launch
+  int split_log2;             // 2^this waves of a workgroup share rows and split k
 };
 
-__device__ __forceinline__ float scale_at(const float* s, int64_t i) { return s[i]; }
-__device__ __forceinline__ float scale_at(const uint16_t* s, int64_t i) {
-  return __uint_as_float(uint32_t(s[i]) << 16);
+typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ v4f mfma16x16x32(const v4i& a, const v4i& b, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf16, a), __builtin_bit_cast(v8bf16, b), c, 0, 0,
+                                                 0);
 }
 
+// Eight codes -> eight BF16 values, in column order.  INT4: the byte 0000qqqq
+// read as E4M3 is q * 2^-9 for every q (0..7 are that format's subnormals,
+// 8..15 its first binade), so the conversion with scale 2^9 gives q exactly.
 template <int FMT>
-__device__ __forceinline__ float w4_value(uint32_t code) {
-  if constexpr (FMT == kW4Int4) return float(int(code));
-  const uint32_t mag = code & 7, e = mag >> 1, m = mag & 1;
-  const float v = e ? (1.f + 0.5f * float(m)) * float(1u << e) * 0.5f : 0.5f * float(m);
-  return code & 8 ? -v : v;
+__device__ __forceinline__ v4i w4_decode(unsigned q) {
+  v4i f;
+  if constexpr (FMT == kW4Int4) {
+    const unsigned even = q & 0x0f0f0f0fu, odd = (q >> 4) & 0x0f0f0f0fu;
+    const unsigned lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
+    f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
+    f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
+    f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
+  } else {
+    f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.f, 0));
+    f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.f, 1));
+    f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.f, 2));
+    f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.f, 3));
+  }
+  return f;
 }
 
-// One wave per output element, lanes along the row: 8 codes (a dword) each.
-template <int FMT, typename S, typename O>
-__global__ void __launch_bounds__(256) w4_kernel(W4Args a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const unsigned blocks = (unsigned(a.n) + 3) / 4;
-  const int r = int(blockIdx.x % blocks) * 4 + int(threadIdx.x >> 6);
-  const int64_t i = blockIdx.x / blocks;
-  if (r >= a.n) return;
-  int64_t e = 0, xi = i;
-  if (a.expert_idx) {
-    e = a.expert_idx[i];
-    xi = i / a.x_div;
+// Workgroup barrier after this wave's LDS accesses; copies to LDS stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Waits until at most N of the wave's copies are in flight.
+template <int N>
+__device__ __forceinline__ void copies_left() {
+  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Copies to LDS as in copy16_to_lds, of one scale or zero point per lane into
+// lane i's dword, and of 16 bytes per lane from addresses of its own.
+__device__ __forceinline__ void copy4_scale_to_lds(const void* base, unsigned index, uint32_t lds, bool two_bytes) {
+  if (two_bytes)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2"
+                 ::"s"(uniform(int(lds))), "v"(index * 2), "s"(uniform_ptr(base)) : "memory");
+  else
+    copy4_to_lds(base, index * 4, lds);
+}
+__device__ __forceinline__ void copy1_zero_to_lds(const uint8_t* base, unsigned byte, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
+               ::"s"(uniform(int(lds))), "v"(byte), "s"(uniform_ptr(base)) : "memory");
+}
+__device__ __forceinline__ void copy16_scattered_to_lds(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(uniform(int(lds))), "v"(src) : "memory");
+}
+
+__device__ const v4i kW4Zeros = {0, 0, 0, 0};
+
+// A wave works through blocks of U steps of 128 columns by 16 R rows of the
+// matrix and TX tokens.  What a block needs comes to the wave's own part of
+// LDS by direct copies, kBlocks blocks deep, in kCopies instructions:
+template <bool Z, int G, int TX, int R, int U>
+struct W4Ring {
+  static constexpr int kQ = 128 / G;                          // groups per step
+  static constexpr int kCodeCopies = U * R;                   // 1 KB each
+  static constexpr int kXCopies = (TX * U + 3) / 4;           // 1 KB each (TX = 1, U = 2: half)
+  static constexpr int kScaleCopies = (U * kQ + 3) / 4 * R;   // four groups of 16 rows each
+  static constexpr int kCopies = kCodeCopies + kXCopies + kScaleCopies * (Z ? 2 : 1);
+  static constexpr int kX = kCodeCopies * 1024, kS = kX + kXCopies * 1024, kZ = kS + kScaleCopies * 256;
+  static constexpr int kBlock = kZ + (Z ? kScaleCopies * 256 : 0);
+  static constexpr int kDeep = kW4LdsBytes / kW4Waves / kBlock;
+  static constexpr int kBlocks = kDeep >= 5 ? 5 : kDeep >= 2 ? kDeep : 2;
+  static constexpr int kWave = kBlocks * kBlock;
+  static_assert(kW4Waves * kWave <= kW4LdsBytes && kCopies * (kBlocks - 1) < 64, "LDS and vmcnt");
+  static_assert(kWave >= 16 * R * 20 * 4, "the partial sums take the ring's place");
+};
+
+// One workgroup: sets of 2^split_log2 waves, each set 16 R rows, its wave j
+// the blocks j, j + 2^split_log2, ...; the partial sums of a set are added
+// through LDS at the end.  Nothing else is shared, so the waves run without
+// barriers.  Codes lie in LDS as [row][piece of 16 bytes], a row's pieces
+// exchanged by (a part of) the row number, activations as [token][unit of 8
+// columns], a token's units exchanged by the token number, so that operand
+// reads meet no bank twice while every copy reads runs of 128 bytes or more.
+//
+// Groups of 128 columns take a lane's 16 bytes as four operands (dword j of
+// the four quarters is operand j, all of one group); shorter groups read
+// dword `quarter` of piece j, so that operand j holds 32 consecutive columns.
+// Up to four tokens stand in the operand rows 0, 4, 8, 12, so that each
+// lane's result register 0 is all it has to scale.
+//
+// Grid: x row blocks; y token tiles, or in the routed form pairs or experts.
+template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
+__global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
+  using L = W4Ring<Z, G, TX, R, U>;
+  constexpr int Q = L::kQ, JG = 4 / Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  constexpr int kRows = 16 * R, kRedLd = TX == 16 ? 20 : TX;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), waves = blockDim.x >> 6;
+  const int lks = a.split_log2, ks = 1 << lks, kidx = wave & (ks - 1), set = wave >> lks;
+  const int sets = waves >> lks;
+  const int row0 = blockIdx.x * (sets * kRows);
+  const unsigned half = unsigned(a.k) >> 1, groups = unsigned(a.k) / G;
+  const int blocks = ((unsigned(a.k) + 128 * U - 1) / (128 * U) - kidx + ks - 1) >> lks;  // of this wave
+
+  int e = 0;
+  bool nowhere = false;
+  if constexpr (ROUTED) {
+    e = a.by_pair ? a.expert_idx[blockIdx.y] : blockIdx.y;
+    if (e < 0 || e >= a.experts) e = a.experts;  // pairs that are routed nowhere
+    e = uniform(e);
+    nowhere = e == a.experts;
   }
-  float acc = 0.f;
-  if (e >= 0 && (!a.expert_idx || e < a.experts)) {
-    const int groups = a.k / a.group;
-    const int64_t row = e * a.n + r;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(a.w + row * (a.k / 2));
-    for (int c = lane * 8; c < a.k; c += kWave * 8) {
-      const uint32_t q = w[c / 8];
-      const int64_t g = row * groups + c / a.group;
-      const float s = scale_at(static_cast<const S*>(a.scales), g);
-      const float z = FMT == kW4Int4 ? (a.zeros ? float(a.zeros[g]) : 8.f) : 0.f;
-      float part = 0.f;
+  const int64_t first_row = ROUTED ? (nowhere ? 0 : int64_t(e) * a.n) + row0 : row0;
+  const uint8_t* wbase = a.w + first_row * half;
+  const char* sbase = static_cast<const char*>(a.scales) + ((first_row * groups) << (a.scales_bf16 ? 1 : 2));
+  const uint8_t* zbase = Z ? a.zeros + first_row * groups : nullptr;
+  const char* ring = lds + wave * L::kWave;
+  const uint32_t ring_at = lds_addr(lds) + wave * L::kWave;
+
+  // Code pieces past the row's end are its last piece again, scales past it the last one's.
+  const auto row_of = [&](int r) { return unsigned(min(set * kRows + r, a.n - 1 - row0)); };
+  const auto code_swap = [](int r) { return U == 4 ? r & 15 : U == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
+  unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        part = fmaf(w4_value<FMT>((q >> (4 * u)) & 15) - z, __uint_as_float(uint32_t(a.x[xi * a.x_ld + c + u]) << 16),
-                    part);
-      acc = fmaf(s, part, acc);
+  for (int c = 0; c < L::kCodeCopies; ++c) {
+    const int r = (c * 64 + lane) / kPieces;
+    cend[c] = row_of(r) * half + half - 16;
+    cpos[c] = row_of(r) * half + ((lane % kPieces) ^ code_swap(r)) * 16;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) soff[r] = row_of(r * 16 + (lane >> 2)) * groups;
+  auto copy_weights = [&](int b) {
+    const unsigned blk = kidx + (b << lks), at = ring_at + unsigned(b % NB) * L::kBlock;
+#pragma unroll
+    for (int c = 0; c < L::kCodeCopies; ++c)
+      copy16_to_lds(wbase, min(blk * (64 * U) + cpos[c], cend[c]), at + c * 1024);
+#pragma unroll
+    for (int c = 0; c < L::kScaleCopies; ++c) {
+      const int h = c / R, r = c % R;  // groups 4 h .. 4 h + 3 of the block, rows 16 r ..
+      const unsigned g = soff[r] + min(blk * (U * Q) + 4 * h + (lane & 3), groups - 1);
+      copy4_scale_to_lds(sbase, g, at + L::kS + c * 256, a.scales_bf16);
+      if constexpr (Z) copy1_zero_to_lds(zbase, g, at + L::kZ + c * 256);
     }
-  }
+  };
+
+  const int quarter = lane >> 4, col = lane & 15;
+  // One tile: tokens t = 0 .. tt - 1; x_row(t), out_row(t) their rows.  `begun`: the first blocks' weights are on
+  // their way (all of the copies are then waited for before the first block).
+  auto tile = [&](int tt, bool begun, auto x_row, auto out_row) {
+    const uint16_t* xsrc[L::kXCopies];  // this lane's unit of block 0; units past the end come from kW4Zeros
+    int xunit[L::kXCopies];
 #pragma unroll
-  for (int s = 32; s; s >>= 1) acc += __shfl_xor(acc, s, kWave);
-  if (lane == 0) {
-    if constexpr (sizeof(O) == 4) static_cast<float*>(a.out)[i * a.n + r] = acc;
-    else static_cast<uint16_t*>(a.out)[i * a.n + r] = uint16_t(pack_bf16x2(acc, 0.f));
+    for (int c = 0; c < L::kXCopies; ++c) {
+      const int t = (c * 64 + lane) / kUnits % TX;
+      xunit[c] = (lane % kUnits) ^ (t & 15);
+      xsrc[c] = a.x + x_row(min(t, tt - 1)) * a.x_ld + xunit[c] * 8;
+    }
+    auto copy_block = [&](int b, bool weights) {
+      const int unit0 = (kidx + (b << lks)) * kUnits;
+      const uint32_t at = ring_at + unsigned(b % NB) * L::kBlock;
+      if (unit0 + kUnits <= a.k >> 3) {
+#pragma unroll
+        for (int c = 0; c < L::kXCopies; ++c)
+          copy16_scattered_to_lds(xsrc[c] + unit0 * 8, at + L::kX + c * 1024);
+      } else {
+#pragma unroll
+        for (int c = 0; c < L::kXCopies; ++c)
+          copy16_scattered_to_lds(
+              unit0 + xunit[c] < a.k >> 3 ? static_cast<const void*>(xsrc[c] + unit0 * 8) : &kW4Zeros,
+              at + L::kX + c * 1024);
+      }
+      if (weights) copy_weights(b);
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < blocks) copy_block(b, !begun);
+
+    const int tok = TX == 16 ? col : TX == 4 ? col >> 2 : 0;
+    const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+    constexpr int A = TX == 16 ? 4 : 1;
+    float acc[R][A] = {};
+    struct Operands {
+      v4i q[U][R], x[U][4], s[L::kScaleCopies], z[Z ? L::kScaleCopies : 1];
+    };
+    // Waits for block b and starts its LDS reads.
+    auto read = [&](Operands& o, int b) {
+      const int newer = min(blocks - 1 - b, NB - 1);  // blocks in flight after this one
+      if (newer >= NB - 1) copies_left<(NB - 1) * L::kCopies>();
+      else if (NB > 4 && newer == 3) copies_left<(3 * L::kCopies < 64 ? 3 * L::kCopies : 0)>();
+      else if (NB > 3 && newer == 2) copies_left<(2 * L::kCopies < 64 ? 2 * L::kCopies : 0)>();
+      else if (newer == 1) copies_left<L::kCopies>();
+      else copies_left<0>();
+      const char* at = ring + (b % NB) * L::kBlock;
+#pragma unroll
+      for (int c = 0; c < L::kScaleCopies; ++c) {
+        o.s[c] = *reinterpret_cast<const v4i*>(at + L::kS + c * 256 + col * 16);
+        if constexpr (Z) o.z[c] = *reinterpret_cast<const v4i*>(at + L::kZ + c * 256 + col * 16);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int row = r * 16 + col, swap = code_swap(row);
+          if constexpr (G == 128) {
+            o.q[u][r] = *reinterpret_cast<const v4i*>(at + (row * kPieces + ((4 * u + quarter) ^ swap)) * 16);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o.q[u][r][j] = *reinterpret_cast<const int*>(at + (row * kPieces + ((4 * u + j) ^ swap)) * 16 + quarter * 4);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int unit = 16 * u + (G == 128 ? 4 * quarter + j : 4 * j + quarter);
+          o.x[u][j] = *reinterpret_cast<const v4i*>(at + L::kX + (tok * kUnits + (unit ^ tok)) * 16);
+        }
+      }
+    };
+    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
+    auto products = [&](Operands& o, int b) {
+      const unsigned g0 = (kidx + (b << lks)) * (U * Q);
+      if (g0 + U * Q > groups) {  // no scale may meet the empty columns' zero sums
+#pragma unroll
+        for (int f = 0; f < U * Q; ++f)
+#pragma unroll
+          for (int r = 0; r < R; ++r) o.s[f / 4 * R + r][f % 4] = g0 + f < groups ? o.s[f / 4 * R + r][f % 4] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v4f part[R], sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const v4f zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            part[r] = mfma16x16x32(o.x[u][j], w4_decode<FMT>(unsigned(o.q[u][r][j])), j % JG ? part[r] : zero);
+          if constexpr (FMT == kW4Int4) sum = mfma16x16x32(o.x[u][j], ones, j % JG ? sum : zero);
+          if (j % JG == JG - 1) {
+            const int f = u * Q + j / JG;  // the group's place in the block
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float scale = __uint_as_float(unsigned(o.s[f / 4 * R + r][f % 4]) << scale_shift);
+              float zero_point = 8.f;
+              if constexpr (Z) zero_point = float(unsigned(o.z[f / 4 * R + r][f % 4]));
+#pragma unroll
+              for (int v = 0; v < A; ++v) {
+                float p = part[r][v];
+                if constexpr (FMT == kW4Int4) p = fmaf(-zero_point, sum[v], p);
+                acc[r][v] = fmaf(scale, p, acc[r][v]);
+              }
+            }
+          }
+        }
+      }
+    };
+    // Block b's products while block b + 1 is read from LDS; its place is then copied anew.
+    auto turn = [&](Operands& now, Operands& next, int b) {
+      if (b + 1 < blocks) read(next, b + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(now, b);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // block b + 1 has been read
+      if (b + 1 + NB < blocks) copy_block(b + 1 + NB, true);
+    };
+    Operands o0, o1;
+    if (blocks > 0) {
+      if (begun) copies_left<0>();
+      read(o0, 0);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (NB < blocks) copy_block(NB, true);
+    }
+    for (int b = 0; b < blocks; b += 2) {
+      turn(o0, o1, b);
+      if (b + 1 < blocks) turn(o1, o0, b + 1);
+    }
+
+    // ---- the sets' partial sums, added in the order of their waves
+    float* red = reinterpret_cast<float*>(lds);
+    lds_barrier();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float* p = red + (wave * kRows + r * 16 + col) * kRedLd;
+      if constexpr (TX == 16) *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+      else if (quarter < TX) p[quarter] = acc[r][0];
+    }
+    lds_barrier();
+    for (int o = tid; o < sets * kRows * TX; o += waves * kWave) {
+      const int rr = o % (16 * R), t = o / (16 * R) % TX, st = o / (16 * R * TX), row = row0 + st * kRows + rr;
+      const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < kW4Waves; ++j) {  // all reads at once
+        const float u = p[(j & (ks - 1)) * kRows * kRedLd];
+        v += j < ks ? u : 0.f;
+      }
+      if (row >= a.n || t >= tt) continue;
+      const int64_t out = out_row(t) * a.n + row;
+      if (a.out_f32) static_cast<float*>(a.out)[out] = v;
+      else static_cast<uint16_t*>(a.out)[out] = uint16_t(pack_bf16x2(v, 0.f));
+    }
+  };
+
+  if constexpr (!ROUTED) {
+    const int base = blockIdx.y * TX;
+    const auto row = [&](int t) { return int64_t(base + t); };
+    tile(min(TX, a.m - base), false, row, row);
+  } else {
+    const bool alone = a.by_pair && nowhere;
+    bool begun = !nowhere;  // the weights need no list
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (begun && b < blocks) copy_weights(b);
+    for (int win = a.by_pair ? blockIdx.y : 0; win < a.m; win += kW4Window) {
+      if (tid == 0) list_n = earlier = 0;
+      lds_barrier();
+      if (alone) {
+        if (tid == 0) list[list_n++] = win;
+      } else {
+        if (a.by_pair && win == int(blockIdx.y))
+          for (int p = tid; p < win; p += waves * kWave)
+            if (a.expert_idx[p] == e) earlier = 1;
+        for (int p = win + tid; p < min(win + kW4Window, a.m); p += waves * kWave) {
+          const int v = a.expert_idx[p];
+          if (nowhere ? v < 0 || v >= a.experts : v == e) list[atomicAdd(&list_n, 1)] = p;
+        }
+      }
+      lds_barrier();
+      if (earlier) break;  // an earlier pair's workgroup has this expert
+      const int count = list_n;
+      for (int t0 = 0; t0 < count; t0 += TX) {
+        const int tt = min(TX, count - t0);
+        if (!nowhere) {
+          tile(tt, begun, [&](int t) { return int64_t(list[t0 + t] / a.x_div); },
+               [&](int t) { return int64_t(list[t0 + t]); });
+          begun = false;
+          copies_left<0>();  // the stores: the next tile counts its copies alone
+        } else {
+          for (int o = tid; o < sets * kRows * tt; o += waves * kWave) {
+            const int row = row0 + o / tt;
+            if (row >= a.n) continue;
+            const int64_t out = int64_t(list[t0 + o % tt]) * a.n + row;
+            if (a.out_f32) static_cast<float*>(a.out)[out] = 0.f;
+            else static_cast<uint16_t*>(a.out)[out] = 0;
+          }
+        }
+        lds_barrier();  // before the next tile's copies
+      }
+      if (alone) break;
+      lds_barrier();  // every wave has taken its count before it is cleared
+    }
+    copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
+}
+
+// out[m][n] = 0 (an empty reduction).
+__global__ void __launch_bounds__(256) w4_zero_kernel(uint32_t* __restrict__ out, int64_t words, int tail) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i < words) out[i] = 0;
+  if (i == words && tail) *reinterpret_cast<uint16_t*>(out + words) = 0;
 }
 
 }  // namespace fp8g
