@@ -14,6 +14,8 @@ namespace {
 using fp8g::W4Args;
 
 constexpr int kFullWaves = 2048;      // 8 on each of 256 CUs
+constexpr int kStreamBytes = 64 * 1024;  // activations of a streaming workgroup, at most
+constexpr int kStreamWorkgroups = 2048;   // workgroups a long stream is dealt to
 constexpr int kMaxColumns = 1 << 20;  // row offsets within a workgroup's 256 rows fit 32 bits
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -47,8 +49,20 @@ int launch_kernel(W4Args a, hipStream_t s) {
   a.by_pair = ROUTED && a.m <= a.experts;
   const int64_t slots = !ROUTED ? cdiv64(a.m, TX) : a.by_pair ? a.m : int64_t(a.experts) + 1;
   if (slots > 65535) return FP8G_EUNSUPPORTED;
-  // k is split over the waves of a workgroup until there is a wave for each of the CUs' places
   const int64_t sets = cdiv64(a.n, 16 * R) * slots, blocks = cdiv64(a.k, 128 * U);
+  // Rows for every place of the CUs, and a tile's activations fit LDS: whole rows per wave.
+  const int64_t x_bytes = (blocks * (256 * U) + 1023) / 1024 * 1024 * TX;
+  if (sets >= kFullWaves && x_bytes <= kStreamBytes) {
+    using L = fp8g::W4StreamRing<Z, G, TX, R, U>;
+    const int64_t row_sets = cdiv64(a.n, 16 * R);
+    a.reps = int(std::max<int64_t>(1, sets / (fp8g::kW4Waves * kStreamWorkgroups)));
+    const int lds = fp8g::kW4Waves * L::kWave + int(x_bytes);
+    hipLaunchKernelGGL((fp8g::w4_stream_kernel<FMT, Z, G, TX, R, U, ROUTED>),
+                       dim3(unsigned(cdiv64(row_sets, fp8g::kW4Waves * a.reps)), unsigned(slots)),
+                       dim3(fp8g::kW4Waves * fp8g::kWave), lds, s, a);
+    return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH;
+  }
+  // k is split over the waves of a workgroup until there is a wave for each of the CUs' places
   int lks = 0;
   while (lks < 3 && (sets << lks) < kFullWaves && (2 << lks) <= blocks) ++lks;
   const int waves = lks == 3 ? 8 : 4;
@@ -100,7 +114,7 @@ extern "C" {
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream) {
-  const W4Args a{x, x_ld, w, w_scales, w_zeros, out, scales_dtype == FP8G_BF16, out_dtype == FP8G_F32, m, n, k, nullptr, 1, 1, 0, 0};
+  const W4Args a{x, x_ld, w, w_scales, w_zeros, out, scales_dtype == FP8G_BF16, out_dtype == FP8G_F32, m, n, k, nullptr, 1, 1, 0, 0, 0};
   bool empty;
   if (int st = check(a, w_format, scales_dtype, out_dtype, group, &empty)) return st;
   return empty ? FP8G_OK : launch(a, w_format, group, static_cast<hipStream_t>(stream));
@@ -113,7 +127,7 @@ int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int
   if (num_pairs < 0 || x_rows < 0 || num_experts < 1) return FP8G_EINVAL;
   if (num_pairs > 0 && (x_rows == 0 || num_pairs % x_rows != 0)) return FP8G_EINVAL;
   const W4Args a{x, x_ld, w, w_scales, w_zeros, out, scales_dtype == FP8G_BF16, out_dtype == FP8G_F32, num_pairs, n, k, expert_idx, num_experts,
-                 num_pairs > 0 ? num_pairs / x_rows : 1, 0, 0};
+                 num_pairs > 0 ? num_pairs / x_rows : 1, 0, 0, 0};
   bool empty;
   if (int st = check(a, w_format, scales_dtype, out_dtype, group, &empty)) return st;
   if (empty) return FP8G_OK;

@@ -38,6 +38,7 @@ struct W4Args {
   int by_pair;                // routed form: a workgroup row per pair (else per expert)
   // set at the launch
   int split_log2;             // 2^this waves of a workgroup share rows and split k
+  int reps;                   // streaming kernel: row sets a wave takes
 };
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
@@ -389,6 +390,264 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
           }
         }
         lds_barrier();  // before the next tile's copies
+      }
+      if (alone) break;
+      lds_barrier();  // every wave has taken its count before it is cleared
+    }
+    copies_left<0>();  // no copy may outlive the workgroup's LDS
+  }
+}
+
+// Rings of the streaming kernel: codes and scales alone.
+template <bool Z, int G, int TX, int R, int U>
+struct W4StreamRing {
+  static constexpr int kQ = 128 / G;
+  static constexpr int kCodeCopies = U * R, kScaleCopies = (U * kQ + 3) / 4 * R;
+  static constexpr int kCopies = kCodeCopies + kScaleCopies * (Z ? 2 : 1);
+  static constexpr int kS = kCodeCopies * 1024, kZ = kS + kScaleCopies * 256;
+  static constexpr int kBlock = kZ + (Z ? kScaleCopies * 256 : 0);
+  static constexpr int kBlocks = 3;
+  static constexpr int kWave = kBlocks * kBlock;
+};
+
+// The product where rows are plenty: every wave takes whole rows (16 R at a
+// time, no split of k), one after the other without a pause, and the
+// workgroup's waves share the tile's activations, which stay in LDS.
+//
+// Grid: x groups of `reps` row sets per wave; y as in w4_kernel.
+template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
+__global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
+  using L = W4StreamRing<Z, G, TX, R, U>;
+  constexpr int Q = L::kQ, JG = 4 / Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  constexpr int kRows = 16 * R, kThreads = kW4Waves * kWave;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6);
+  const int quarter = lane >> 4, col = lane & 15;
+  const unsigned half = unsigned(a.k) >> 1, groups = unsigned(a.k) / G;
+  const int blocks = (unsigned(a.k) + 128 * U - 1) / (128 * U);
+  const int sets = (a.n + kRows - 1) / kRows;
+  const int set0 = blockIdx.x * (kW4Waves * a.reps) + wave;  // then every kW4Waves-th, `reps` of them
+  const int my_sets = max(0, min(a.reps, (sets - set0 + kW4Waves - 1) / kW4Waves));
+  const int total = my_sets * blocks;
+
+  int e = 0;
+  bool nowhere = false;
+  if constexpr (ROUTED) {
+    e = a.by_pair ? a.expert_idx[blockIdx.y] : blockIdx.y;
+    if (e < 0 || e >= a.experts) e = a.experts;  // pairs that are routed nowhere
+    e = uniform(e);
+    nowhere = e == a.experts;
+  }
+  const int64_t first_row = ROUTED ? (nowhere ? 0 : int64_t(e) * a.n) : 0;
+  const uint32_t ring_at = lds_addr(lds) + wave * L::kWave;
+  const char* ring = lds + wave * L::kWave;
+  char* x_lds = lds + kW4Waves * L::kWave;
+  const uint32_t x_at = lds_addr(lds) + kW4Waves * L::kWave;
+  const int x_row_bytes = (blocks * (kUnits * 16) + 1023) & ~1023;
+
+  const auto code_swap = [](int r) { return U == 4 ? r & 15 : U == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
+  // ---- the copies' side of the stream: the next block to bring
+  int c_block = 0, c_set = set0, c_slot = 0;
+  const uint8_t* wbase;
+  const char* sbase;
+  const uint8_t* zbase;
+  unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
+  auto start_set = [&]() {
+    const int64_t row = first_row + int64_t(c_set) * kRows;
+    wbase = a.w + row * half;
+    sbase = static_cast<const char*>(a.scales) + ((row * groups) << (a.scales_bf16 ? 1 : 2));
+    zbase = Z ? a.zeros + row * groups : nullptr;
+    const int last = a.n - 1 - c_set * kRows;  // rows past the end are the last row again
+#pragma unroll
+    for (int c = 0; c < L::kCodeCopies; ++c) {
+      const int r = (c * 64 + lane) / kPieces;
+      const unsigned at = unsigned(min(r, last)) * half;
+      cend[c] = at + half - 16;
+      cpos[c] = at + ((lane % kPieces) ^ code_swap(r)) * 16;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) soff[r] = unsigned(min(r * 16 + (lane >> 2), last)) * groups;
+  };
+  auto copy_next = [&]() {
+    const unsigned at = ring_at + unsigned(c_slot) * L::kBlock;
+#pragma unroll
+    for (int c = 0; c < L::kCodeCopies; ++c)
+      copy16_to_lds(wbase, min(unsigned(c_block) * (64 * U) + cpos[c], cend[c]), at + c * 1024);
+#pragma unroll
+    for (int c = 0; c < L::kScaleCopies; ++c) {
+      const int h = c / R, r = c % R;
+      const unsigned g = soff[r] + min(unsigned(c_block) * (U * Q) + 4 * h + (lane & 3), groups - 1);
+      copy4_scale_to_lds(sbase, g, at + L::kS + c * 256, a.scales_bf16);
+      if constexpr (Z) copy1_zero_to_lds(zbase, g, at + L::kZ + c * 256);
+    }
+    c_slot = c_slot + 1 == NB ? 0 : c_slot + 1;
+    if (++c_block == blocks) {
+      c_block = 0;
+      c_set += kW4Waves;
+      start_set();
+    }
+  };
+  auto begin = [&]() {
+    c_block = c_slot = 0;
+    c_set = set0;
+    start_set();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < total) copy_next();
+  };
+
+  auto tile = [&](int tt, auto x_row, auto out_row) {
+    // the activations: token t's units, exchanged by t; units past the end are zero
+    for (int c = wave; c < tt * (x_row_bytes >> 10); c += kW4Waves) {
+      const int per = x_row_bytes >> 10, t = c / per, u = (c % per) * 64 + lane, unit = u ^ (t & 15);
+      const void* src = unit < a.k >> 3 ? static_cast<const void*>(a.x + x_row(t) * a.x_ld + unit * 8) : &kW4Zeros;
+      copy16_scattered_to_lds(src, x_at + c * 1024);
+    }
+    copies_left<0>();
+    lds_barrier();
+
+    const int tok = TX == 16 ? col : TX == 4 ? col >> 2 : 0;
+    const char* x_mine = x_lds + tok * x_row_bytes;
+    const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+    constexpr int A = TX == 16 ? 4 : 1;
+    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
+    float acc[R][A] = {};
+    int block = 0, slot = 0, set = set0;
+    for (int b = 0; b < total; ++b) {
+      const int newer = min(total - 1 - b, NB - 1);  // blocks in flight after this one
+      if (newer == 2) copies_left<2 * L::kCopies>();
+      else if (newer == 1) copies_left<L::kCopies>();
+      else copies_left<0>();
+      const char* at = ring + slot * L::kBlock;
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      v4i q[U][R], x[U][4], s[L::kScaleCopies], z[Z ? L::kScaleCopies : 1];
+#pragma unroll
+      for (int c = 0; c < L::kScaleCopies; ++c) {
+        s[c] = *reinterpret_cast<const v4i*>(at + L::kS + c * 256 + col * 16);
+        if constexpr (Z) z[c] = *reinterpret_cast<const v4i*>(at + L::kZ + c * 256 + col * 16);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int row = r * 16 + col, swap = code_swap(row);
+          if constexpr (G == 128) {
+            q[u][r] = *reinterpret_cast<const v4i*>(at + (row * kPieces + ((4 * u + quarter) ^ swap)) * 16);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              q[u][r][j] = *reinterpret_cast<const int*>(at + (row * kPieces + ((4 * u + j) ^ swap)) * 16 + quarter * 4);
+          }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the block has been read
+      if (b + NB < total) copy_next();
+      const char* xb = x_mine + block * (kUnits * 16);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int unit = 16 * u + (G == 128 ? 4 * quarter + j : 4 * j + quarter);
+          x[u][j] = *reinterpret_cast<const v4i*>(xb + (unit ^ tok) * 16);
+        }
+      const unsigned g0 = unsigned(block) * (U * Q);
+      if (g0 + U * Q > groups) {  // no scale may meet the empty columns' zero sums
+#pragma unroll
+        for (int f = 0; f < U * Q; ++f)
+#pragma unroll
+          for (int r = 0; r < R; ++r) s[f / 4 * R + r][f % 4] = g0 + f < groups ? s[f / 4 * R + r][f % 4] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v4f part[R], sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const v4f zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            part[r] = mfma16x16x32(x[u][j], w4_decode<FMT>(unsigned(q[u][r][j])), j % JG ? part[r] : zero);
+          if constexpr (FMT == kW4Int4) sum = mfma16x16x32(x[u][j], ones, j % JG ? sum : zero);
+          if (j % JG == JG - 1) {
+            const int f = u * Q + j / JG;  // the group's place in the block
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float scale = __uint_as_float(unsigned(s[f / 4 * R + r][f % 4]) << scale_shift);
+              float zero_point = 8.f;
+              if constexpr (Z) zero_point = float(unsigned(z[f / 4 * R + r][f % 4]));
+#pragma unroll
+              for (int v = 0; v < A; ++v) {
+                float p = part[r][v];
+                if constexpr (FMT == kW4Int4) p = fmaf(-zero_point, sum[v], p);
+                acc[r][v] = fmaf(scale, p, acc[r][v]);
+              }
+            }
+          }
+        }
+      }
+      if (++block == blocks) {  // the rows are done
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int row = set * kRows + r * 16 + col;
+#pragma unroll
+          for (int v = 0; v < A; ++v) {
+            const int t = TX == 16 ? quarter * 4 + v : quarter;
+            if (row < a.n && t < tt) {
+              const int64_t out = out_row(t) * a.n + row;
+              if (a.out_f32) static_cast<float*>(a.out)[out] = acc[r][v];
+              else static_cast<uint16_t*>(a.out)[out] = uint16_t(pack_bf16x2(acc[r][v], 0.f));
+            }
+            acc[r][v] = 0.f;
+          }
+        }
+        block = 0;
+        set += kW4Waves;
+      }
+    }
+  };
+
+  if constexpr (!ROUTED) {
+    const int base = blockIdx.y * TX;
+    const auto row = [&](int t) { return int64_t(base + t); };
+    begin();
+    tile(min(TX, a.m - base), row, row);
+  } else {
+    const bool alone = a.by_pair && nowhere;
+    bool begun = !nowhere;  // the weights need no list
+    if (begun) begin();
+    for (int win = a.by_pair ? blockIdx.y : 0; win < a.m; win += kW4Window) {
+      if (tid == 0) list_n = earlier = 0;
+      lds_barrier();
+      if (alone) {
+        if (tid == 0) list[list_n++] = win;
+      } else {
+        if (a.by_pair && win == int(blockIdx.y))
+          for (int p = tid; p < win; p += kThreads)
+            if (a.expert_idx[p] == e) earlier = 1;
+        for (int p = win + tid; p < min(win + kW4Window, a.m); p += kThreads) {
+          const int v = a.expert_idx[p];
+          if (nowhere ? v < 0 || v >= a.experts : v == e) list[atomicAdd(&list_n, 1)] = p;
+        }
+      }
+      lds_barrier();
+      if (earlier) break;  // an earlier pair's workgroup has this expert
+      const int count = list_n;
+      for (int t0 = 0; t0 < count; t0 += TX) {
+        const int tt = min(TX, count - t0);
+        if (!nowhere) {
+          if (!begun) begin();
+          begun = false;
+          tile(tt, [&](int t) { return int64_t(list[t0 + t] / a.x_div); },
+               [&](int t) { return int64_t(list[t0 + t]); });
+        } else {
+          const int rows = min(a.n - blockIdx.x * (kW4Waves * a.reps) * kRows, kW4Waves * a.reps * kRows);
+          for (int o = tid; o < rows * tt; o += kThreads) {
+            const int64_t out = int64_t(list[t0 + o / rows]) * a.n + blockIdx.x * (kW4Waves * a.reps) * kRows + o % rows;
+            if (a.out_f32) static_cast<float*>(a.out)[out] = 0.f;
+            else static_cast<uint16_t*>(a.out)[out] = 0;
+          }
+        }
+        lds_barrier();  // before the next tile's activations
       }
       if (alone) break;
       lds_barrier();  // every wave has taken its count before it is cleared
