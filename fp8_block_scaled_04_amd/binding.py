@@ -136,12 +136,7 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 0.1 us; building a Stream object takes 2.8
-
-
 def _stream(stream):
-    if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -666,8 +661,22 @@ def fp8_moe_gather_rows(y, dst_row, out, stream=None):
     return out
 
 
-# ---- expert routing and the weighted combine --------------------------------------
+# ---- expert routing, the weighted combine, products with 4-bit weights --------------
+# A decoding step makes these calls by the hundred, so their checks read each
+# attribute of a tensor once (about 0.1 us apiece) and compare; only a failed
+# comparison goes on to say what is wrong.  3 us of a call are checks and
+# marshalling, 3 us the launch.
 _FLOAT_TYPES = {torch.float32: FP8G_F32, torch.bfloat16: FP8G_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object, which takes 2.8 us
+
+
+def _on(stream, device):
+    """The address of the stream to launch on, for tensors of device `device`."""
+    if stream is not None:
+        return stream.cuda_stream
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is {torch.cuda.current_device()}")
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _float_type(t, name):
@@ -677,18 +686,37 @@ def _float_type(t, name):
     return dt
 
 
-def _rows(t, name):
-    """A matrix whose rows are dense; their stride may exceed their length."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a device tensor")
-    _want_dim(t, name, 2)
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
-    return t
+def _tensor(t, name, dtypes, shape, device):
+    """t's address: dense, of the given type (or one of several), shape and device (None: any)."""
+    if (t.dtype is not dtypes and not (type(dtypes) is tuple and t.dtype in dtypes)) or t.shape != shape \
+            or not t.is_contiguous() or (t.get_device() != device if device is not None else not t.is_cuda):
+        allowed = dtypes if type(dtypes) is tuple else (dtypes,)
+        if t.dtype not in allowed:
+            raise TypeError(f"{name} must be {' or '.join(str(d) for d in allowed)}, got {t.dtype}")
+        _want(_dev(t, name), name, shape)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on device {device}")
+    return t.data_ptr()
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else t.shape[1]
+def _matrix(t, name):
+    """(rows, columns, row stride, device) of a matrix whose rows are dense; their stride may exceed their length."""
+    if t.dim() != 2 or not t.is_cuda:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a device tensor")
+        _want_dim(t, name, 2)
+    rows, cols = t.shape
+    if rows > 1 and cols:
+        ld, one = t.stride()
+        if ld < cols or (one != 1 and cols > 1):
+            raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
+    else:
+        ld = cols
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
+    return rows, cols, ld, t.get_device()
+
+
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _new(stream, shape, dtype, device):
@@ -706,20 +734,17 @@ def fp8_moe_route(logits, topk, score_func=FP8G_SOFTMAX, bias=None, expert_group
     rows may be strided) -> (expert_idx [T][topk] int32, weights [T][topk]
     float32), allocated unless given."""
     dt = _float_type(logits, "logits")
-    T, E = _rows(logits, "logits").shape
-    topk = int(topk)
-    if bias is not None:
-        _want(_f32(bias, "bias"), "bias", (E,))
+    T, E, ld, dev = _matrix(logits, "logits")
+    shape = (T, max(int(topk), 0))
     if expert_idx is None:
-        expert_idx = _new(stream, (T, max(topk, 0)), torch.int32, logits.device)
+        expert_idx = _new(stream, shape, torch.int32, logits.device)
     if weights is None:
-        weights = _new(stream, (T, max(topk, 0)), torch.float32, logits.device)
-    _want(_i32t(expert_idx, "expert_idx"), "expert_idx", (T, topk))
-    _want(_f32(weights, "weights"), "weights", (T, topk))
-    _same_device(logits=logits, bias=bias, expert_idx=expert_idx, weights=weights)
-    st = lib().fp8_moe_route(_p(logits), dt, _ld(logits), _p(bias), T, E, score_func, expert_groups, topk_groups,
-                             group_score, topk, bool(renormalize), scale, _p(expert_idx), _p(weights),
-                             _stream(stream))
+        weights = _new(stream, shape, torch.float32, logits.device)
+    st = lib().fp8_moe_route(logits.data_ptr(), dt, ld,
+                             None if bias is None else _tensor(bias, "bias", torch.float32, (E,), dev), T, E,
+                             score_func, expert_groups, topk_groups, group_score, int(topk), bool(renormalize), scale,
+                             _tensor(expert_idx, "expert_idx", torch.int32, shape, dev),
+                             _tensor(weights, "weights", torch.float32, shape, dev), _on(stream, dev))
     _check("fp8_moe_route", st)
     return expert_idx, weights
 
@@ -729,56 +754,63 @@ def fp8_moe_route_backward(logits, expert_idx, grad_weights, grad_logits=None, s
     """Gradient of the logits [T][E] from that of the weights [T][topk] that
     fp8_moe_route gave for expert_idx (same score_func, renormalize, scale)."""
     dt = _float_type(logits, "logits")
-    T, E = _rows(logits, "logits").shape
-    _want_dim(_i32t(expert_idx, "expert_idx"), "expert_idx", 2)
+    T, E, ld, dev = _matrix(logits, "logits")
+    _want_dim(expert_idx, "expert_idx", 2)
     topk = expert_idx.shape[1]
-    _want(expert_idx, "expert_idx", (T, topk))
-    _want(_f32(grad_weights, "grad_weights"), "grad_weights", (T, topk))
     if grad_logits is None:
         grad_logits = _new(stream, (T, E), logits.dtype, logits.device)
     if grad_logits.dtype != logits.dtype:
         raise TypeError(f"grad_logits must be {logits.dtype}, got {grad_logits.dtype}")
-    _want(_rows(grad_logits, "grad_logits"), "grad_logits", (T, E))
-    _same_device(logits=logits, expert_idx=expert_idx, grad_weights=grad_weights, grad_logits=grad_logits)
-    st = lib().fp8_moe_route_backward(_p(logits), dt, _ld(logits), _p(expert_idx), _p(grad_weights), T, E,
-                                      score_func, topk, bool(renormalize), scale, _p(grad_logits),
-                                      _ld(grad_logits), _stream(stream))
+    g_rows, g_cols, g_ld, g_dev = _matrix(grad_logits, "grad_logits")
+    if (g_rows, g_cols, g_dev) != (T, E, dev):
+        _want(grad_logits, "grad_logits", (T, E))
+        raise ValueError(f"grad_logits is on {grad_logits.device}, logits on {logits.device}")
+    st = lib().fp8_moe_route_backward(logits.data_ptr(), dt, ld,
+                                      _tensor(expert_idx, "expert_idx", torch.int32, (T, topk), dev),
+                                      _tensor(grad_weights, "grad_weights", torch.float32, (T, topk), dev), T, E,
+                                      score_func, topk, bool(renormalize), scale, grad_logits.data_ptr(), g_ld,
+                                      _on(stream, dev))
     _check("fp8_moe_route_backward", st)
     return grad_logits
 
 
-def _check_combine(y, dst_row, weights, tokens, name):
-    """(T, topk, n, y rows) of a combine whose token-side rows are `tokens`."""
+def _check_combine(y, y_name, dst_row, weights, tokens, name):
+    """(T, topk, n, y rows, device, y, dst_row, weights and tokens addresses)
+    of a combine whose token-side rows are `tokens`."""
     _want_dim(tokens, name, 2)
     T, n = tokens.shape
-    if y is not None and (y.dim() < 1 or y.shape[-1] != n):
-        raise ValueError(f"y has shape {tuple(y.shape)}, expected rows of {n}")
-    rows = None if y is None else (y.numel() // n if n else 0)
-    topk = None
-    for t, what in ((dst_row, "dst_row"), (weights, "weights")):
-        if t is not None:
-            _want_dim(t, what, 2)
-            topk = t.shape[1] if topk is None else topk
-            _want(t, what, (T, topk))
+    dev = tokens.get_device()
+    at = _tensor(tokens, name, _BF16_BITS, (T, n), dev)
+    ys = y.shape
+    if len(ys) < 1 or ys[-1] != n:
+        raise ValueError(f"{y_name} has shape {tuple(ys)}, expected rows of {n}")
+    y_at = _tensor(y, y_name, _BF16_BITS, ys, dev)
+    rows = y.numel() // n if n else 0
+    if dev < 0:
+        raise TypeError(f"{name} must be a device tensor")
+    topk, d_at, w_at = None, None, None
+    if dst_row is not None:
+        _want_dim(dst_row, "dst_row", 2)
+        topk = dst_row.shape[1]
+        d_at = _tensor(dst_row, "dst_row", torch.int32, (T, topk), dev)
+    if weights is not None:
+        if topk is None:
+            _want_dim(weights, "weights", 2)
+            topk = weights.shape[1]
+        w_at = _tensor(weights, "weights", torch.float32, (T, topk), dev)
     if topk is None:
         topk = rows // T if T and rows else 1
-    if dst_row is None and rows is not None and n and rows != T * topk:
-        raise ValueError(f"y has {rows} rows, expected {T * topk} without dst_row")
-    return T, topk, n, rows
+    if dst_row is None and n and rows != T * topk:
+        raise ValueError(f"{y_name} has {rows} rows, expected {T * topk} without dst_row")
+    return T, topk, n, rows, dev, y_at, d_at, w_at, at
 
 
 def fp8_moe_combine(y, dst_row, weights, out, stream=None):
     """out[t] = sum over j of weights[t][j] * y[dst_row[t][j]].  y holds rows
     of n bfloat16 (any leading shape); dst_row [T][topk] int32 or None (pair p
     in row p); weights [T][topk] float32 or None (1); out [T][n]."""
-    y, out = _bf16(y, "y"), _bf16(out, "out")
-    if dst_row is not None:
-        _i32t(dst_row, "dst_row")
-    if weights is not None:
-        _f32(weights, "weights")
-    T, topk, n, rows = _check_combine(y, dst_row, weights, out, "out")
-    _same_device(y=y, dst_row=dst_row, weights=weights, out=out)
-    st = lib().fp8_moe_combine(_p(y), rows, n, _p(dst_row), _p(weights), T, topk, _p(out), _stream(stream))
+    T, topk, n, rows, dev, y_at, d_at, w_at, out_at = _check_combine(y, "y", dst_row, weights, out, "out")
+    st = lib().fp8_moe_combine(y_at, rows, n, d_at, w_at, T, topk, out_at, _on(stream, dev))
     _check("fp8_moe_combine", st)
     return out
 
@@ -787,48 +819,36 @@ def fp8_moe_combine_backward(grad_out, y, dst_row, weights, grad_y, grad_weights
     """Gradients of fp8_moe_combine into grad_y (the shape of y; rows no pair
     names are left as they are) and grad_weights [T][topk] (None: not
     computed, and y may be None)."""
-    grad_out, grad_y = _bf16(grad_out, "grad_out"), _bf16(grad_y, "grad_y")
-    if dst_row is not None:
-        _i32t(dst_row, "dst_row")
-    if weights is not None:
-        _f32(weights, "weights")
-    T, topk, n, rows = _check_combine(grad_y, dst_row, weights, grad_out, "grad_out")
+    T, topk, n, rows, dev, gy_at, d_at, w_at, go_at = _check_combine(grad_y, "grad_y", dst_row, weights, grad_out,
+                                                                     "grad_out")
+    y_at = gw_at = None
     if grad_weights is not None:
         if y is None:
             raise ValueError("grad_weights needs y")
-        _want(_bf16(y, "y"), "y", grad_y.shape)
-        _want(_f32(grad_weights, "grad_weights"), "grad_weights", (T, topk))
-    _same_device(grad_out=grad_out, y=y, dst_row=dst_row, weights=weights, grad_y=grad_y, grad_weights=grad_weights)
-    st = lib().fp8_moe_combine_backward(_p(grad_out), _p(y), rows, n, _p(dst_row), _p(weights), T, topk, _p(grad_y),
-                                        _p(grad_weights), _stream(stream))
+        y_at = _tensor(y, "y", _BF16_BITS, grad_y.shape, dev)
+        gw_at = _tensor(grad_weights, "grad_weights", torch.float32, (T, topk), dev)
+    st = lib().fp8_moe_combine_backward(go_at, y_at, rows, n, d_at, w_at, T, topk, gy_at, gw_at, _on(stream, dev))
     _check("fp8_moe_combine_backward", st)
     return grad_y, grad_weights
 
 
-# ---- products with 4-bit weights ---------------------------------------------------
 def _check_w4(x, w, scales, zeros, out, lead, rows):
-    """(n, k, group, dtype codes) of a 4-bit product; `lead` = (E,) or ()."""
-    if x.dtype != torch.bfloat16:
+    """(x stride, n, k, group, scale and out types, device, and the addresses
+    of w, scales, zeros and out) of a 4-bit product; lead = (E,) or ()."""
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"x must be bfloat16, got {x.dtype}")
-    k = _rows(x, "x").shape[1]
-    if w.dtype != torch.uint8:
-        raise TypeError(f"w must hold pairs of 4-bit codes (uint8), got {w.dtype}")
-    _want_dim(_dev(w, "w"), "w", len(lead) + 2)
-    n = w.shape[-2]
-    _want(w, "w", (*lead, n, k // 2))
-    sd = _float_type(_dev(scales, "scales"), "scales")
+    _, k, ld, dev = _matrix(x, "x")
+    _want_dim(w, "w", len(lead) + 2)
     _want_dim(scales, "scales", len(lead) + 2)
-    groups = scales.shape[-1]
+    n, groups = scales.shape[-2:]
     if k % 2 or (k and (groups == 0 or k % groups)):
         raise ValueError(f"{groups} scales per row do not divide {k} columns")
-    _want(scales, "scales", (*lead, n, groups))
-    if zeros is not None:
-        if zeros.dtype != torch.uint8:
-            raise TypeError(f"zeros must be uint8, got {zeros.dtype}")
-        _want(_dev(zeros, "zeros"), "zeros", (*lead, n, groups))
-    od = _float_type(_dev(out, "out"), "out")
-    _want(out, "out", (rows, n))
-    return n, k, k // groups if k else 128, sd, od
+    sd, od = _float_type(scales, "scales"), _float_type(out, "out")
+    shape = (*lead, n, groups)
+    return (ld, n, k, k // groups if k else 128, sd, od, dev, _tensor(w, "w", torch.uint8, (*lead, n, k // 2), dev),
+            _tensor(scales, "scales", scales.dtype, shape, dev),
+            None if zeros is None else _tensor(zeros, "zeros", torch.uint8, shape, dev),
+            _tensor(out, "out", out.dtype, (rows, n), dev))
 
 
 def fp8_w4_matvec(x, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None):
@@ -836,10 +856,9 @@ def fp8_w4_matvec(x, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None
     strided) times the transpose of the 4-bit matrix w [n][k / 2] with scales
     [n][k / group] (float32 or bfloat16) and zero points (uint8, INT4 only)."""
     m = x.shape[0] if x.dim() else 0
-    n, k, group, sd, od = _check_w4(x, w, scales, zeros, out, (), m)
-    _same_device(x=x, w=w, scales=scales, zeros=zeros, out=out)
-    st = lib().fp8_w4_matvec(_p(x), _ld(x), _p(w), w_format, _p(scales), sd, _p(zeros), group, _p(out), od, m, n, k,
-                             _stream(stream))
+    ld, n, k, group, sd, od, dev, w_at, s_at, z_at, out_at = _check_w4(x, w, scales, zeros, out, (), m)
+    st = lib().fp8_w4_matvec(x.data_ptr(), ld, w_at, w_format, s_at, sd, z_at, group, out_at, od, m, n, k,
+                             _on(stream, dev))
     _check("fp8_w4_matvec", st)
     return out
 
@@ -848,14 +867,14 @@ def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zer
     """out [P][n]: row p = x row p // (P // x rows) times the matrix of expert
     expert_idx.view(-1)[p] of w [E][n][k / 2] (scales, zeros [E][n][k /
     group]); zeros where that is no expert."""
-    P = _i32t(expert_idx, "expert_idx").numel()
+    P = expert_idx.numel()
     rows = x.shape[0] if x.dim() else 0
     if P and (rows == 0 or P % rows):
         raise ValueError(f"{P} pairs are no multiple of the {rows} rows of x")
     E = w.shape[0] if w.dim() else 0
-    n, k, group, sd, od = _check_w4(x, w, scales, zeros, out, (E,), P)
-    _same_device(x=x, expert_idx=expert_idx, w=w, scales=scales, zeros=zeros, out=out)
-    st = lib().fp8_w4_matvec_experts(_p(x), _ld(x), rows, _p(expert_idx), P, _p(w), w_format, _p(scales), sd,
-                                     _p(zeros), group, _p(out), od, E, n, k, _stream(stream))
+    ld, n, k, group, sd, od, dev, w_at, s_at, z_at, out_at = _check_w4(x, w, scales, zeros, out, (E,), P)
+    st = lib().fp8_w4_matvec_experts(x.data_ptr(), ld, rows,
+                                     _tensor(expert_idx, "expert_idx", torch.int32, expert_idx.shape, dev), P, w_at,
+                                     w_format, s_at, sd, z_at, group, out_at, od, E, n, k, _on(stream, dev))
     _check("fp8_w4_matvec_experts", st)
     return out
