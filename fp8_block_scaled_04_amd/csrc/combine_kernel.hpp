@@ -53,7 +53,12 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __rest
   *reinterpret_cast<v4i*>(out + t * n + c) = pack8(acc);
 }
 
-// One workgroup per token: one pass over its row of grad_out per pair.
+// PAIRS = false: a workgroup per token, which takes its pairs one after the
+// other (its row of grad_out then comes from the cache after the first).
+// PAIRS = true: a workgroup per pair.  A thread holds up to kBwdChunks pieces
+// of 8 columns at a time, all loaded before any is used.
+constexpr int kBwdChunks = 4;
+template <bool PAIRS>
 __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_t* __restrict__ grad_out,
                                                                    const uint16_t* __restrict__ y, int rows, int n,
                                                                    const int32_t* __restrict__ dst,
@@ -61,23 +66,37 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_
                                                                    uint16_t* __restrict__ grad_y,
                                                                    float* __restrict__ grad_w) {
   __shared__ float part[4];
-  const int64_t t = blockIdx.x;
-  for (int j = 0; j < topk; ++j) {
+  const int64_t t = PAIRS ? int64_t(blockIdx.x) / topk : blockIdx.x;
+  const int j0 = PAIRS ? int(blockIdx.x - t * topk) : 0, j1 = PAIRS ? j0 + 1 : topk;
+  for (int j = j0; j < j1; ++j) {
     const int d = pair_row(dst, t * topk + j, rows);
     const float w = weights ? weights[t * topk + j] : 1.f;
+    const uint16_t* go = grad_out + t * n;
     float dot = 0.f;
     if (d >= 0)
-      for (int c = threadIdx.x * 8; c < n; c += 2048) {
-        float g[8], v[8], o[8];
-        unpack8(*reinterpret_cast<const v4i*>(grad_out + t * n + c), g);
-        if (grad_w) {
-          unpack8(*reinterpret_cast<const v4i*>(y + int64_t(d) * n + c), v);
+      for (int c0 = threadIdx.x * 8; c0 < n; c0 += 2048 * kBwdChunks) {
+        v4i gv[kBwdChunks], yv[kBwdChunks];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+        for (int u = 0; u < kBwdChunks; ++u) {
+          const int c = min(c0 + u * 2048, n - 8);
+          gv[u] = *reinterpret_cast<const v4i*>(go + c);
+          if (grad_w) yv[u] = *reinterpret_cast<const v4i*>(y + int64_t(d) * n + c);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = w * g[i];
-        *reinterpret_cast<v4i*>(grad_y + int64_t(d) * n + c) = pack8(o);
+        for (int u = 0; u < kBwdChunks; ++u) {
+          const int c = c0 + u * 2048;
+          if (c >= n) break;
+          float g[8], v[8], o[8];
+          unpack8(gv[u], g);
+          if (grad_w) {
+            unpack8(yv[u], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = w * g[i];
+          *reinterpret_cast<v4i*>(grad_y + int64_t(d) * n + c) = pack8(o);
+        }
       }
     if (grad_w) {
 #pragma unroll

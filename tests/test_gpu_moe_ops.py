@@ -103,6 +103,55 @@ def test_route(T, E, topk, groups, topk_groups, top2, dtype, sigmoid, with_bias,
     check_route(strided(t, pad), l, topk, sigmoid, bias, groups, topk_groups, top2, renormalize, 2.5)
 
 
+@pytest.mark.parametrize("T,E,topk,groups,topk_groups", [
+    (3, 1000, 8, 5, 2), (2, 990, 17, 33, 9),  # groups whose padded places outnumber the lanes: 32 experts a lane
+    (40000, 8, 2, 1, 1), (9000, 64, 6, 8, 3), (33000, 16, 4, 4, 2), (70001, 4, 3, 1, 1)])  # few lanes a token
+def test_route_lane_counts(T, E, topk, groups, topk_groups):
+    """Every share of lanes a token can have, against the oracle on a sample of
+    rows, and all rows against each other (the rows repeat)."""
+    require_gpu()
+    rng = np.random.default_rng(T)
+    base = 64 if T > 64 else T
+    _, l = spread_logits(rng, base, E, "f32")
+    reps = -(-T // base)
+    full = np.tile(l, (reps, 1))[:T]
+    for sigmoid, renormalize in ((False, False), (True, True)):
+        idx, w = Out((T, topk), torch.int32, 55), Out((T, topk), torch.float32, 55)
+        b.fp8_moe_route(dev(full), topk, b.FP8G_SIGMOID if sigmoid else b.FP8G_SOFTMAX, None, groups, topk_groups,
+                        b.FP8G_GROUP_TOP2, renormalize, 1.0, idx.view, w.view)
+        gi, gw = idx.numpy(), w.numpy()
+        want_i, want_w, gap = moe_ops.route(l, topk, sigmoid, None, groups, topk_groups, True, renormalize)
+        ok = gap > 2.0 ** -19
+        assert ok.mean() > 0.5 and np.array_equal(gi[:base][ok], want_i[ok])
+        assert not (np.abs(gw[:base] - want_w) > route_bound(l, want_w))[ok].any()
+        assert np.array_equal(gi, np.tile(gi[:base], (reps, 1))[:T])
+        assert np.array_equal(gw, np.tile(gw[:base], (reps, 1))[:T])
+        g = rng.normal(size=(base, topk)).astype(np.float32)
+        grad = b.fp8_moe_route_backward(dev(full), idx.view, dev(np.tile(g, (reps, 1))[:T]), None,
+                                        b.FP8G_SIGMOID if sigmoid else b.FP8G_SOFTMAX, renormalize).cpu().numpy()
+        want, mag = moe_ops.route_backward(l, gi[:base], g, sigmoid, renormalize)
+        assert np.all(np.abs(grad[:base] - want) <= mag * (8 * 6 + E + 3 * topk + 48) * U + 2.0 ** -126)
+        assert np.array_equal(grad, np.tile(grad[:base], (reps, 1))[:T])
+
+
+def test_combine_backward_of_many_tokens():
+    """The form for many tokens, with the weights' gradient and without."""
+    require_gpu()
+    rng = np.random.default_rng(21)
+    T, k, n, rows = 300, 3, 2120, 1000
+    dst = pairs(rng, T, k, rows)
+    ty, y = bf16(rng.normal(size=(rows, n)))
+    tg, go = bf16(rng.normal(size=(T, n)))
+    w = rng.normal(size=(T, k)).astype(np.float32)
+    for with_gw in (True, False):
+        gy, gw = Out((rows, n), torch.bfloat16, 3), Out((T, k), torch.float32, 3)
+        b.fp8_moe_combine_backward(tg, ty if with_gw else None, dev(dst), dev(w), gy.view,
+                                   gw.view if with_gw else None)
+        want_y, want_w, mag = moe_ops.combine_backward(go, y, dst, w, np.full((rows, n), 3.0))
+        assert np.all(np.abs(gy.numpy() - want_y) <= np.abs(want_y) * (2.0 ** -8 * (1 + 2.0 ** -8) + 2 * U))
+        assert np.all(np.abs(gw.numpy() - want_w) <= (n + 1) * U * mag) if with_gw else np.all(gw.numpy() == 3)
+
+
 def test_route_ties_go_to_the_lowest_index():
     require_gpu()
     for E, groups, topk in ((8, 1, 3), (256, 8, 8), (100, 5, 5), (1024, 1, 32)):

@@ -138,6 +138,68 @@ def test_experts(T, topk, E, n, k, per_pair, group, fmt, sdt, with_zeros, odt):
     assert np.all(got[(e.reshape(-1) < 0) | (e.reshape(-1) >= E)] == 0)
 
 
+STREAMS = [  # m, n, k: enough rows that no wave splits k
+    (1, 32768, 128), (1, 40001, 320), (3, 33000, 256), (4, 32769, 1024), (5, 65536, 128), (16, 70007, 384),
+    (19, 66000, 160), (1, 300000, 64)]
+
+
+@pytest.mark.parametrize("m,n,k", STREAMS)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES)
+def test_matvec_of_many_rows(m, n, k, group, fmt, sdt, with_zeros, odt):
+    require_gpu()
+    k = k // group * group or group
+    rng = np.random.default_rng(m + n + k)
+    tw, w, ts, s, tz, z = matrix(rng, (), n, k, group, sdt, with_zeros)
+    tx, x = bf16(rng.normal(size=(m, k)))
+    out = Out((m, n), DT[odt], 5)
+    b.fp8_w4_matvec(strided(tx, 8 * (m % 2)), tw, ts, out.view, FMT[fmt], tz)
+    want, mag = moe_ops.w4_matvec(x, w, s, z, fmt == "e2m1")
+    check(out.numpy(), want, mag, k, odt)
+
+
+@pytest.mark.parametrize("T,topk,E,n,k,per_pair", [
+    (1, 8, 64, 4100, 128, False), (2, 5, 40, 3500, 256, True), (40, 8, 300, 130, 384, False), (64, 8, 128, 270, 512, True),
+    (30, 4, 500, 80, 1024, False), (900, 2, 9, 4000, 64, False), (7, 3, 60, 8200, 96, True)])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES)
+def test_experts_of_many_rows(T, topk, E, n, k, per_pair, group, fmt, sdt, with_zeros, odt):
+    require_gpu()
+    k = k // group * group
+    rng = np.random.default_rng(T + E + n)
+    e = rng.integers(0, E, (T, topk)).astype(np.int32)
+    if T > 2:
+        e[rng.random((T, topk)) < 0.1] = rng.choice([-1, E, E + 9])
+        e[1] = -1
+    tw, w, ts, s, tz, z = matrix(rng, (E,), n, k, group, sdt, with_zeros)
+    tx, x = bf16(rng.normal(size=(T * topk if per_pair else T, k)))
+    out = Out((T * topk, n), DT[odt], 5)
+    b.fp8_w4_matvec_experts(tx, dev(e), tw, ts, out.view, FMT[fmt], tz)
+    want, mag = moe_ops.w4_matvec_experts(x, e, w, s, z, fmt == "e2m1")
+    got = out.numpy()
+    check(got, want, mag, k, odt)
+    assert np.all(got[(e.reshape(-1) < 0) | (e.reshape(-1) >= E)] == 0)
+
+
+def test_streamed_matrices_past_32_bits():
+    """Experts past 2^32 bytes, with enough pairs for whole rows per wave."""
+    require_gpu()
+    rng = np.random.default_rng(7)
+    E, n, k = 140, 16384, 4096
+    w = torch.empty(E, n, k // 2, dtype=torch.uint8, device="cuda")
+    s = torch.empty(E, n, k // 64, device="cuda")
+    for g in (0, 139):
+        w[g] = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda")
+        s[g] = 0.01
+    tx, x = bf16(rng.normal(size=(2, k)))
+    out = torch.empty(4, n, device="cuda")
+    b.fp8_w4_matvec_experts(tx, dev(np.int32([[139, 0], [0, 139]])), w, s, out)
+    for p, g in enumerate((139, 0, 0, 139)):
+        rows = [0, 17, 4095, n - 1]
+        want, mag = moe_ops.w4_matvec(x[p // 2:p // 2 + 1], w[g][rows].cpu().numpy(), s[g][rows].cpu().numpy())
+        check(out[p][rows].cpu().numpy()[None], want, mag, k, "f32")
+
+
 def test_matrices_past_32_bits():
     """Experts whose codes start past 2^32 bytes."""
     require_gpu()
