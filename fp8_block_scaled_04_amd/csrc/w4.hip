@@ -76,9 +76,10 @@ int launch_kernel(W4Args a, hipStream_t s) {
 
 template <int FMT, bool Z, int G, bool ROUTED>
 int launch_tiles(const W4Args& a, hipStream_t s) {
+  constexpr int kSteps = G == 32 ? 1 : 2;  // 128-column steps of a block: four groups or fewer
   // tokens per expert: hardly ever above 1, 4 with 1/8, 1 on average
-  if (ROUTED ? a.m <= a.experts / 8 : a.m == 1) return launch_kernel<FMT, Z, G, 1, 1, 2, ROUTED>(a, s);
-  if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, 2, ROUTED>(a, s);
+  if (ROUTED ? a.m <= a.experts / 8 : a.m == 1) return launch_kernel<FMT, Z, G, 1, 1, kSteps, ROUTED>(a, s);
+  if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, kSteps, ROUTED>(a, s);
   const int64_t sets = cdiv64(a.n, 32) * (ROUTED ? a.experts : cdiv64(a.m, 16));
   if (sets * fp8g::kW4Waves < kFullWaves / 2) return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
   return launch_kernel<FMT, Z, G, 16, 2, 1, ROUTED>(a, s);

@@ -101,6 +101,38 @@ __device__ __forceinline__ void copy16_scattered_to_lds(const void* src, uint32_
 
 __device__ const v4i kW4Zeros = {0, 0, 0, 0};
 
+// Scales (or zero points) of 16 R rows, F = U * 128 / G groups a block.  A
+// copy brings four groups of 16 rows, a dword per lane, four lanes per row
+// (a lane per row, as one group would have it, takes the memory pipe four
+// times as long): parts of a block where it has four groups or more, else a
+// period of 4 / F blocks at once.
+template <int R, int F>
+struct W4Scales {
+  static constexpr int kParts = F >= 4 ? F / 4 : 1, kPeriod = F >= 4 ? 1 : 4 / F;
+  static constexpr int kCopies = kParts * R, kBytes = kCopies * 256;  // of a period
+  unsigned v[R][F];
+  // What a lane (column `col` of the matrix operand) needs for a block, the i-th of its period.
+  __device__ __forceinline__ void read(const char* at, int col, int i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if constexpr (F >= 4) {
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          const v4i t = *reinterpret_cast<const v4i*>(at + (h * R + r) * 256 + col * 16);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) v[r][4 * h + f] = unsigned(t[f]);
+        }
+      } else if constexpr (F == 2) {
+        const v2u t = *reinterpret_cast<const v2u*>(at + r * 256 + col * 16 + i * 8);
+        v[r][0] = t.x;
+        v[r][1] = t.y;
+      } else {
+        v[r][0] = *reinterpret_cast<const unsigned*>(at + r * 256 + col * 16 + i * 4);
+      }
+    }
+  }
+};
+
 // A wave works through blocks of U steps of 128 columns by 16 R rows of the
 // matrix and TX tokens.  What a block needs comes to the wave's own part of
 // LDS by direct copies, kBlocks blocks deep, in kCopies instructions:
@@ -109,13 +141,16 @@ struct W4Ring {
   static constexpr int kQ = 128 / G;                          // groups per step
   static constexpr int kCodeCopies = U * R;                   // 1 KB each
   static constexpr int kXCopies = (TX * U + 3) / 4;           // 1 KB each (TX = 1, U = 2: half)
-  static constexpr int kScaleCopies = (U * kQ + 3) / 4 * R;   // four groups of 16 rows each
-  static constexpr int kCopies = kCodeCopies + kXCopies + kScaleCopies * (Z ? 2 : 1);
-  static constexpr int kX = kCodeCopies * 1024, kS = kX + kXCopies * 1024, kZ = kS + kScaleCopies * 256;
-  static constexpr int kBlock = kZ + (Z ? kScaleCopies * 256 : 0);
-  static constexpr int kDeep = kW4LdsBytes / kW4Waves / kBlock;
-  static constexpr int kBlocks = kDeep >= 5 ? 5 : kDeep >= 2 ? kDeep : 2;
-  static constexpr int kWave = kBlocks * kBlock;
+  using Scales = W4Scales<R, U * kQ>;
+  // Counted per block; those of a period of several blocks are not (the waits are then a little stricter).
+  static constexpr int kCopies = kCodeCopies + kXCopies + (Scales::kPeriod == 1 ? Scales::kCopies * (Z ? 2 : 1) : 0);
+  static constexpr int kX = kCodeCopies * 1024, kBlock = kX + kXCopies * 1024;
+  static constexpr int kScaleSlot = Scales::kBytes * (Z ? 2 : 1);
+  static constexpr int slots(int blocks) { return (blocks + Scales::kPeriod - 1) / Scales::kPeriod + (Scales::kPeriod > 1); }
+  static constexpr int bytes(int blocks) { return blocks * kBlock + slots(blocks) * kScaleSlot; }
+  static constexpr int deep(int blocks) { return bytes(blocks) * kW4Waves <= kW4LdsBytes || blocks == 2 ? blocks : deep(blocks - 1); }
+  static constexpr int kBlocks = deep(5), kSlots = slots(kBlocks), kScales = kBlocks * kBlock;
+  static constexpr int kWave = bytes(kBlocks);
   static_assert(kW4Waves * kWave <= kW4LdsBytes && kCopies * (kBlocks - 1) < 64, "LDS and vmcnt");
   static_assert(kWave >= 16 * R * 20 * 4, "the partial sums take the ring's place");
 };
@@ -138,7 +173,7 @@ struct W4Ring {
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   using L = W4Ring<Z, G, TX, R, U>;
-  constexpr int Q = L::kQ, JG = 4 / Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  constexpr int Q = L::kQ, JG = 4 / Q, F = U * Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
   constexpr int kRows = 16 * R, kRedLd = TX == 16 ? 20 : TX;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
@@ -167,6 +202,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   // Code pieces past the row's end are its last piece again, scales past it the last one's.
   const auto row_of = [&](int r) { return unsigned(min(set * kRows + r, a.n - 1 - row0)); };
   const auto code_swap = [](int r) { return U == 4 ? r & 15 : U == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
+  using Scales = typename L::Scales;
   unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
 #pragma unroll
   for (int c = 0; c < L::kCodeCopies; ++c) {
@@ -178,16 +214,20 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   for (int r = 0; r < R; ++r) soff[r] = row_of(r * 16 + (lane >> 2)) * groups;
   auto copy_weights = [&](int b) {
     const unsigned blk = kidx + (b << lks), at = ring_at + unsigned(b % NB) * L::kBlock;
+    if (b % Scales::kPeriod == 0) {
+      const unsigned to = ring_at + L::kScales + unsigned(b / Scales::kPeriod % L::kSlots) * L::kScaleSlot;
+#pragma unroll
+      for (int c = 0; c < Scales::kCopies; ++c) {
+        const int h = c / R, r = c % R, i = lane & 3;  // part h, rows 16 r ..; the lane's i-th group
+        const unsigned g = F >= 4 ? blk * F + 4 * h + i : (blk + ((i / F) << lks)) * F + i % F;
+        const unsigned at_g = soff[r] + min(g, groups - 1);
+        copy4_scale_to_lds(sbase, at_g, to + c * 256, a.scales_bf16);
+        if constexpr (Z) copy1_zero_to_lds(zbase, at_g, to + Scales::kBytes + c * 256);
+      }
+    }
 #pragma unroll
     for (int c = 0; c < L::kCodeCopies; ++c)
       copy16_to_lds(wbase, min(blk * (64 * U) + cpos[c], cend[c]), at + c * 1024);
-#pragma unroll
-    for (int c = 0; c < L::kScaleCopies; ++c) {
-      const int h = c / R, r = c % R;  // groups 4 h .. 4 h + 3 of the block, rows 16 r ..
-      const unsigned g = soff[r] + min(blk * (U * Q) + 4 * h + (lane & 3), groups - 1);
-      copy4_scale_to_lds(sbase, g, at + L::kS + c * 256, a.scales_bf16);
-      if constexpr (Z) copy1_zero_to_lds(zbase, g, at + L::kZ + c * 256);
-    }
   };
 
   const int quarter = lane >> 4, col = lane & 15;
@@ -227,22 +267,21 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     constexpr int A = TX == 16 ? 4 : 1;
     float acc[R][A] = {};
     struct Operands {
-      v4i q[U][R], x[U][4], s[L::kScaleCopies], z[Z ? L::kScaleCopies : 1];
+      v4i q[U][R], x[U][4];
+      Scales s, z;
     };
     // Waits for block b and starts its LDS reads.
     auto read = [&](Operands& o, int b) {
       const int newer = min(blocks - 1 - b, NB - 1);  // blocks in flight after this one
       if (newer >= NB - 1) copies_left<(NB - 1) * L::kCopies>();
-      else if (NB > 4 && newer == 3) copies_left<(3 * L::kCopies < 64 ? 3 * L::kCopies : 0)>();
-      else if (NB > 3 && newer == 2) copies_left<(2 * L::kCopies < 64 ? 2 * L::kCopies : 0)>();
+      else if (NB > 4 && newer == 3) copies_left<(NB > 4 ? 3 : 0) * L::kCopies>();
+      else if (NB > 3 && newer == 2) copies_left<(NB > 3 ? 2 : 0) * L::kCopies>();
       else if (newer == 1) copies_left<L::kCopies>();
       else copies_left<0>();
       const char* at = ring + (b % NB) * L::kBlock;
-#pragma unroll
-      for (int c = 0; c < L::kScaleCopies; ++c) {
-        o.s[c] = *reinterpret_cast<const v4i*>(at + L::kS + c * 256 + col * 16);
-        if constexpr (Z) o.z[c] = *reinterpret_cast<const v4i*>(at + L::kZ + c * 256 + col * 16);
-      }
+      const char* scales_at = ring + L::kScales + b / Scales::kPeriod % L::kSlots * L::kScaleSlot;
+      o.s.read(scales_at, col, b % Scales::kPeriod);
+      if constexpr (Z) o.z.read(scales_at + Scales::kBytes, col, b % Scales::kPeriod);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -270,7 +309,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
 #pragma unroll
         for (int f = 0; f < U * Q; ++f)
 #pragma unroll
-          for (int r = 0; r < R; ++r) o.s[f / 4 * R + r][f % 4] = g0 + f < groups ? o.s[f / 4 * R + r][f % 4] : 0;
+          for (int r = 0; r < R; ++r) o.s.v[r][f] = g0 + f < groups ? o.s.v[r][f] : 0;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -286,9 +325,9 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
             const int f = u * Q + j / JG;  // the group's place in the block
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              const float scale = __uint_as_float(unsigned(o.s[f / 4 * R + r][f % 4]) << scale_shift);
+              const float scale = __uint_as_float(o.s.v[r][f] << scale_shift);
               float zero_point = 8.f;
-              if constexpr (Z) zero_point = float(unsigned(o.z[f / 4 * R + r][f % 4]));
+              if constexpr (Z) zero_point = float(o.z.v[r][f]);
 #pragma unroll
               for (int v = 0; v < A; ++v) {
                 float p = part[r][v];
@@ -402,12 +441,13 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
 template <bool Z, int G, int TX, int R, int U>
 struct W4StreamRing {
   static constexpr int kQ = 128 / G;
-  static constexpr int kCodeCopies = U * R, kScaleCopies = (U * kQ + 3) / 4 * R;
-  static constexpr int kCopies = kCodeCopies + kScaleCopies * (Z ? 2 : 1);
-  static constexpr int kS = kCodeCopies * 1024, kZ = kS + kScaleCopies * 256;
-  static constexpr int kBlock = kZ + (Z ? kScaleCopies * 256 : 0);
-  static constexpr int kBlocks = 3;
-  static constexpr int kWave = kBlocks * kBlock;
+  using Scales = W4Scales<R, U * kQ>;
+  static constexpr int kCodeCopies = U * R;
+  static constexpr int kCopies = kCodeCopies + (Scales::kPeriod == 1 ? Scales::kCopies * (Z ? 2 : 1) : 0);
+  static constexpr int kBlock = kCodeCopies * 1024, kBlocks = 3;
+  static constexpr int kScaleSlot = Scales::kBytes * (Z ? 2 : 1);
+  static constexpr int kSlots = kBlocks + (Scales::kPeriod > 1);  // a short row begins a period with every block
+  static constexpr int kScales = kBlocks * kBlock, kWave = kScales + kSlots * kScaleSlot;
 };
 
 // The product where rows are plenty: every wave takes whole rows (16 R at a
@@ -418,7 +458,7 @@ struct W4StreamRing {
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
   using L = W4StreamRing<Z, G, TX, R, U>;
-  constexpr int Q = L::kQ, JG = 4 / Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  constexpr int Q = L::kQ, JG = 4 / Q, F = U * Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
   constexpr int kRows = 16 * R, kThreads = kW4Waves * kWave;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
@@ -452,7 +492,9 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
   const uint8_t* wbase;
   const char* sbase;
   const uint8_t* zbase;
+  using Scales = typename L::Scales;
   unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
+  int c_scale_slot = 0;
   auto start_set = [&]() {
     const int64_t row = first_row + int64_t(c_set) * kRows;
     wbase = a.w + row * half;
@@ -470,17 +512,21 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     for (int r = 0; r < R; ++r) soff[r] = unsigned(min(r * 16 + (lane >> 2), last)) * groups;
   };
   auto copy_next = [&]() {
-    const unsigned at = ring_at + unsigned(c_slot) * L::kBlock;
+    const unsigned at = ring_at + unsigned(c_slot) * L::kBlock, blk = c_block;
+    if (c_block % Scales::kPeriod == 0) {
+      const unsigned to = ring_at + L::kScales + unsigned(c_scale_slot) * L::kScaleSlot;
+      c_scale_slot = c_scale_slot + 1 == L::kSlots ? 0 : c_scale_slot + 1;
+#pragma unroll
+      for (int c = 0; c < Scales::kCopies; ++c) {
+        const int h = c / R, r = c % R;
+        const unsigned g = soff[r] + min(blk * F + 4 * h + (lane & 3), groups - 1);
+        copy4_scale_to_lds(sbase, g, to + c * 256, a.scales_bf16);
+        if constexpr (Z) copy1_zero_to_lds(zbase, g, to + Scales::kBytes + c * 256);
+      }
+    }
 #pragma unroll
     for (int c = 0; c < L::kCodeCopies; ++c)
-      copy16_to_lds(wbase, min(unsigned(c_block) * (64 * U) + cpos[c], cend[c]), at + c * 1024);
-#pragma unroll
-    for (int c = 0; c < L::kScaleCopies; ++c) {
-      const int h = c / R, r = c % R;
-      const unsigned g = soff[r] + min(unsigned(c_block) * (U * Q) + 4 * h + (lane & 3), groups - 1);
-      copy4_scale_to_lds(sbase, g, at + L::kS + c * 256, a.scales_bf16);
-      if constexpr (Z) copy1_zero_to_lds(zbase, g, at + L::kZ + c * 256);
-    }
+      copy16_to_lds(wbase, min(blk * (64 * U) + cpos[c], cend[c]), at + c * 1024);
     c_slot = c_slot + 1 == NB ? 0 : c_slot + 1;
     if (++c_block == blocks) {
       c_block = 0;
@@ -489,7 +535,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     }
   };
   auto begin = [&]() {
-    c_block = c_slot = 0;
+    c_block = c_slot = c_scale_slot = 0;
     c_set = set0;
     start_set();
 #pragma unroll
@@ -513,7 +559,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     constexpr int A = TX == 16 ? 4 : 1;
     const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
     float acc[R][A] = {};
-    int block = 0, slot = 0, set = set0;
+    int block = 0, slot = 0, scale_slot = L::kSlots - 1, set = set0;
     for (int b = 0; b < total; ++b) {
       const int newer = min(total - 1 - b, NB - 1);  // blocks in flight after this one
       if (newer == 2) copies_left<2 * L::kCopies>();
@@ -521,12 +567,12 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
       else copies_left<0>();
       const char* at = ring + slot * L::kBlock;
       slot = slot + 1 == NB ? 0 : slot + 1;
-      v4i q[U][R], x[U][4], s[L::kScaleCopies], z[Z ? L::kScaleCopies : 1];
-#pragma unroll
-      for (int c = 0; c < L::kScaleCopies; ++c) {
-        s[c] = *reinterpret_cast<const v4i*>(at + L::kS + c * 256 + col * 16);
-        if constexpr (Z) z[c] = *reinterpret_cast<const v4i*>(at + L::kZ + c * 256 + col * 16);
-      }
+      v4i q[U][R], x[U][4];
+      Scales s, z;
+      if (block % Scales::kPeriod == 0) scale_slot = scale_slot + 1 == L::kSlots ? 0 : scale_slot + 1;
+      const char* scales_at = ring + L::kScales + scale_slot * L::kScaleSlot;
+      s.read(scales_at, col, block % Scales::kPeriod);
+      if constexpr (Z) z.read(scales_at + Scales::kBytes, col, block % Scales::kPeriod);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -556,7 +602,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
 #pragma unroll
         for (int f = 0; f < U * Q; ++f)
 #pragma unroll
-          for (int r = 0; r < R; ++r) s[f / 4 * R + r][f % 4] = g0 + f < groups ? s[f / 4 * R + r][f % 4] : 0;
+          for (int r = 0; r < R; ++r) s.v[r][f] = g0 + f < groups ? s.v[r][f] : 0;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -572,9 +618,9 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
             const int f = u * Q + j / JG;  // the group's place in the block
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              const float scale = __uint_as_float(unsigned(s[f / 4 * R + r][f % 4]) << scale_shift);
+              const float scale = __uint_as_float(s.v[r][f] << scale_shift);
               float zero_point = 8.f;
-              if constexpr (Z) zero_point = float(unsigned(z[f / 4 * R + r][f % 4]));
+              if constexpr (Z) zero_point = float(z.v[r][f]);
 #pragma unroll
               for (int v = 0; v < A; ++v) {
                 float p = part[r][v];
