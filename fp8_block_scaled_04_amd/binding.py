@@ -667,16 +667,19 @@ def fp8_moe_gather_rows(y, dst_row, out, stream=None):
 # comparison goes on to say what is wrong.  3 us of a call are checks and
 # marshalling, 3 us the launch.
 _FLOAT_TYPES = {torch.float32: FP8G_F32, torch.bfloat16: FP8G_BF16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object, which takes 2.8 us
+# The current stream's address and the current device without the objects that torch.cuda builds (2.8 and 0.3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(stream, device):
     """The address of the stream to launch on, for tensors of device `device`."""
     if stream is not None:
         return stream.cuda_stream
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"the tensors are on device {device}, the current device is {torch.cuda.current_device()}")
-    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return _raw_stream(device)
 
 
 def _float_type(t, name):
@@ -700,20 +703,18 @@ def _tensor(t, name, dtypes, shape, device):
 
 def _matrix(t, name):
     """(rows, columns, row stride, device) of a matrix whose rows are dense; their stride may exceed their length."""
-    if t.dim() != 2 or not t.is_cuda:
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a device tensor")
+    shape, device = t.shape, t.get_device()
+    if device < 0:
+        raise TypeError(f"{name} must be a device tensor")
+    if len(shape) != 2:
         _want_dim(t, name, 2)
-    rows, cols = t.shape
-    if rows > 1 and cols:
-        ld, one = t.stride()
-        if ld < cols or (one != 1 and cols > 1):
-            raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
-    else:
+    rows, cols = shape
+    ld, one = t.stride()
+    if rows < 2 or not cols:
         ld = cols
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(t.shape)}")
-    return rows, cols, ld, t.get_device()
+    if ld < cols or (one != 1 and cols > 1):
+        raise ValueError(f"{name} must have dense rows, got strides {t.stride()} for shape {tuple(shape)}")
+    return rows, cols, ld, device
 
 
 _BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
@@ -832,31 +833,34 @@ def fp8_moe_combine_backward(grad_out, y, dst_row, weights, grad_y, grad_weights
     return grad_y, grad_weights
 
 
-def _check_w4(x, w, scales, zeros, out, lead, rows):
-    """(x stride, n, k, group, scale and out types, device, and the addresses
-    of w, scales, zeros and out) of a 4-bit product; lead = (E,) or ()."""
+def _check_w4(x, k, dev, w, scales, zeros, out, lead, rows):
+    """(n, group, scale and out types, and the addresses of w, scales, zeros
+    and out) of a 4-bit product; lead = (E,) or ()."""
     if x.dtype is not torch.bfloat16:
         raise TypeError(f"x must be bfloat16, got {x.dtype}")
-    _, k, ld, dev = _matrix(x, "x")
-    _want_dim(w, "w", len(lead) + 2)
-    _want_dim(scales, "scales", len(lead) + 2)
-    n, groups = scales.shape[-2:]
+    shape = scales.shape
+    if len(shape) != len(lead) + 2:
+        _want_dim(scales, "scales", len(lead) + 2)
+    n, groups = shape[-2], shape[-1]
     if k % 2 or (k and (groups == 0 or k % groups)):
         raise ValueError(f"{groups} scales per row do not divide {k} columns")
-    sd, od = _float_type(scales, "scales"), _float_type(out, "out")
     shape = (*lead, n, groups)
-    return (ld, n, k, k // groups if k else 128, sd, od, dev, _tensor(w, "w", torch.uint8, (*lead, n, k // 2), dev),
-            _tensor(scales, "scales", scales.dtype, shape, dev),
+    s_type, o_type = scales.dtype, out.dtype
+    sd, od = _FLOAT_TYPES.get(s_type), _FLOAT_TYPES.get(o_type)
+    if sd is None or od is None:
+        _float_type(scales, "scales"), _float_type(out, "out")
+    return (n, k // groups if k else 128, sd, od, _tensor(w, "w", torch.uint8, (*lead, n, k // 2), dev),
+            _tensor(scales, "scales", s_type, shape, dev),
             None if zeros is None else _tensor(zeros, "zeros", torch.uint8, shape, dev),
-            _tensor(out, "out", out.dtype, (rows, n), dev))
+            _tensor(out, "out", o_type, (rows, n), dev))
 
 
 def fp8_w4_matvec(x, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None):
     """out [m][n] (bfloat16 or float32) = x [m][k] (bfloat16, rows may be
     strided) times the transpose of the 4-bit matrix w [n][k / 2] with scales
     [n][k / group] (float32 or bfloat16) and zero points (uint8, INT4 only)."""
-    m = x.shape[0] if x.dim() else 0
-    ld, n, k, group, sd, od, dev, w_at, s_at, z_at, out_at = _check_w4(x, w, scales, zeros, out, (), m)
+    m, k, ld, dev = _matrix(x, "x")
+    n, group, sd, od, w_at, s_at, z_at, out_at = _check_w4(x, k, dev, w, scales, zeros, out, (), m)
     st = lib().fp8_w4_matvec(x.data_ptr(), ld, w_at, w_format, s_at, sd, z_at, group, out_at, od, m, n, k,
                              _on(stream, dev))
     _check("fp8_w4_matvec", st)
@@ -867,12 +871,12 @@ def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zer
     """out [P][n]: row p = x row p // (P // x rows) times the matrix of expert
     expert_idx.view(-1)[p] of w [E][n][k / 2] (scales, zeros [E][n][k /
     group]); zeros where that is no expert."""
+    rows, k, ld, dev = _matrix(x, "x")
     P = expert_idx.numel()
-    rows = x.shape[0] if x.dim() else 0
     if P and (rows == 0 or P % rows):
         raise ValueError(f"{P} pairs are no multiple of the {rows} rows of x")
     E = w.shape[0] if w.dim() else 0
-    ld, n, k, group, sd, od, dev, w_at, s_at, z_at, out_at = _check_w4(x, w, scales, zeros, out, (E,), P)
+    n, group, sd, od, w_at, s_at, z_at, out_at = _check_w4(x, k, dev, w, scales, zeros, out, (E,), P)
     st = lib().fp8_w4_matvec_experts(x.data_ptr(), ld, rows,
                                      _tensor(expert_idx, "expert_idx", torch.int32, expert_idx.shape, dev), P, w_at,
                                      w_format, s_at, sd, z_at, group, out_at, od, E, n, k, _on(stream, dev))
