@@ -17,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8gemm.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fp8gemm.hip", "moe.hip", "moe_ops.hip", "w4.hip", "jit.hip")]
 DENSE_SOURCE = os.path.join(CSRC, "dense_launch.hip")  # compiled once per operand-format pair
+W4_SOURCE = os.path.join(CSRC, "w4_launch.hip")  # compiled once per kind of 4-bit matrix
 
 # Device code generation; the runtime specialisation compiles with the same.
 DEVICE_FLAGS = [
@@ -60,8 +61,8 @@ def hipcc() -> str:
 def _compile_jobs(gen: str, objdir: str):
     """(command, object) per translation unit: the host/grouped/cast unit, the
     MoE layout unit, the routing and combine unit, the 4-bit unit, the
-    runtime-specialisation unit, and the dense GEMM instantiations once per
-    operand-format pair."""
+    runtime-specialisation unit, the dense GEMM instantiations once per
+    operand-format pair and the 4-bit kernels once per kind of matrix."""
     base = [hipcc(), *DEVICE_FLAGS, "--offload-arch=gfx950", "-fPIC", "-c", "-I", INCLUDE, "-I", CSRC, "-I", gen]
     jobs = []
     for src in SOURCES:
@@ -70,6 +71,9 @@ def _compile_jobs(gen: str, objdir: str):
     for fmt in range(4):
         obj = os.path.join(objdir, f"dense_launch_fmt{fmt}.o")
         jobs.append(([*base, f"-DFP8G_DENSE_FMT={fmt}", DENSE_SOURCE, "-o", obj], obj))
+    for kind in range(3):
+        obj = os.path.join(objdir, f"w4_launch_kind{kind}.o")
+        jobs.append(([*base, f"-DFP8G_W4_KIND={kind}", W4_SOURCE, "-o", obj], obj))
     return jobs
 
 

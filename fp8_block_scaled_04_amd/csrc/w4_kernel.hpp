@@ -13,9 +13,25 @@
 // and the group's scale and zero point are applied to the FP32 sum,
 //     sum (code - zero) * scale * x = scale * (sum code * x - zero * sum x),
 // with sum x from the same instruction against ones.
+//
+// What bounds it: the codes are read once, 0.5 byte a weight, and a CU has to
+// decode what it reads.  A lane's 16 bytes take 36 (INT4) or 16 (E2M1) vector
+// instructions of 4 cycles to decode and more again around that, so the
+// codes' way from memory to LDS runs by direct copies (no registers, several
+// blocks ahead) and the waves carry as little else as they can.  Measured on
+// gfx950: a direct copy of 1 KB takes the CU's memory pipe 17 cycles when
+// four consecutive lanes read 64 bytes, 64 cycles when every lane reads a row
+// of its own, as the operand layout has it; so rows are copied by four or
+// eight lanes and turned in LDS.
+//   one token       4096 x 7168 INT4, groups of 128       6.3 us (2.4 TB/s; an empty launch takes 1.7)
+//   5 tokens        2111 x 7168 E2M1, groups of 32        6.9 us
+//   16 tokens       7168 x 16384 INT4 with zero points   20.5 us (3.0 TB/s)
+//   8 experts       4096 x 2048, one token               11.8 us (3.2 TB/s)
+//   128 experts     7168 x 2048, 64 tokens, 8 each        220 us (4.5 TB/s)
 #pragma once
 
 #include "device_common.hpp"
+#include "w4_launch.hpp"
 
 namespace fp8g {
 
@@ -23,23 +39,6 @@ constexpr int kW4Int4 = 0, kW4E2M1 = 1;
 constexpr int kW4Waves = 8;     // per workgroup, at most (4 where k is split less: two workgroups fit a CU)
 constexpr int kW4Window = 512;   // pairs searched at a time for an expert's tokens
 constexpr int kW4LdsBytes = 156 * 1024;  // rings of a workgroup, at most (160 KB per CU)
-
-struct W4Args {
-  const uint16_t* x;
-  int64_t x_ld;
-  const uint8_t* w;
-  const void* scales;
-  const uint8_t* zeros;
-  void* out;
-  int scales_bf16, out_f32;
-  int m, n, k;                // m: tokens, or pairs in the routed form
-  const int32_t* expert_idx;  // routed form, else NULL
-  int experts, x_div;         // experts; pairs per row of x
-  int by_pair;                // routed form: a workgroup row per pair (else per expert)
-  // set at the launch
-  int split_log2;             // 2^this waves of a workgroup share rows and split k
-  int reps;                   // streaming kernel: row sets a wave takes
-};
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
@@ -57,7 +56,8 @@ __device__ __forceinline__ v4i w4_decode(unsigned q) {
   v4i f;
   if constexpr (FMT == kW4Int4) {
     const unsigned even = q & 0x0f0f0f0fu, odd = (q >> 4) & 0x0f0f0f0fu;
-    const unsigned lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    const unsigned lo = __builtin_amdgcn_perm(odd, even, 0x05010400u);
+    const unsigned hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
     f[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
     f[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
     f[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
@@ -133,82 +133,217 @@ struct W4Scales {
   }
 };
 
-// A wave works through blocks of U steps of 128 columns by 16 R rows of the
-// matrix and TX tokens.  What a block needs comes to the wave's own part of
-// LDS by direct copies, kBlocks blocks deep, in kCopies instructions:
+// Where a row's 16-byte pieces lie in a block's codes [row][4 U pieces]: piece
+// p at p ^ w4_swap(row), so that the 16 rows of an operand read meet no bank
+// twice while the copies read 64 U bytes of a row in one run.
+template <int U>
+__device__ __forceinline__ constexpr int w4_swap(int row) {
+  static_assert(U == 1 || U == 2, "four or eight pieces per row");
+  return U == 2 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// The token in a lane's operand row (its `col`).  Up to four tokens stand in
+// the rows 0, 4, 8, 12, so that result register 0 is all a lane has to scale.
+template <int TX>
+__device__ __forceinline__ int w4_token(int col) { return TX == 16 ? col : TX == 4 ? col >> 2 : 0; }
+
+// A block: U steps of 128 columns by 16 R rows of the matrix and TX tokens,
+// as a lane (operand row `col`, columns' `quarter`) holds it.  Groups of 128
+// columns take a lane's 16 bytes of codes as four operands (dword j of the
+// four quarters is operand j, all of one group); shorter groups read dword
+// `quarter` of piece j, so that operand j holds 32 consecutive columns.
+template <int FMT, bool Z, int G, int TX, int R, int U>
+struct W4Block {
+  static constexpr int Q = 128 / G, F = U * Q, JG = 4 / Q;  // groups per step and block; instructions per group
+  static constexpr int A = TX == 16 ? 4 : 1;                // result registers in use
+  using Scales = W4Scales<R, F>;
+  v4i q[U][R], x[U][4];
+  Scales s, z;
+
+  __device__ __forceinline__ void read_codes(const char* at, int quarter, int col) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int row = r * 16 + col, swap = w4_swap<U>(row);
+        const char* p = at + row * (64 * U);
+        if constexpr (G == 128) {
+          q[u][r] = *reinterpret_cast<const v4i*>(p + ((4 * u + quarter) ^ swap) * 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[u][r][j] = *reinterpret_cast<const int*>(p + ((4 * u + j) ^ swap) * 16 + quarter * 4);
+        }
+      }
+  }
+  // `at`: the block's units of the lane's token, [16 U units of 8 columns], unit i at i ^ token.
+  __device__ __forceinline__ void read_x(const char* at, int quarter, int token) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int unit = 16 * u + (G == 128 ? 4 * quarter + j : 4 * j + quarter);
+        x[u][j] = *reinterpret_cast<const v4i*>(at + (unit ^ token) * 16);
+      }
+  }
+  // acc[r][i] += the block's products; g0 its first group, of `groups` per row.
+  __device__ __forceinline__ void products(float (&acc)[R][A], unsigned g0, unsigned groups, unsigned scale_shift) {
+    if (g0 + F > groups) {  // no scale may meet the empty columns' zero sums
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int r = 0; r < R; ++r) s.v[r][f] = g0 + f < groups ? s.v[r][f] : 0;
+    }
+    const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v4f part[R], sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          part[r] = mfma16x16x32(x[u][j], w4_decode<FMT>(unsigned(q[u][r][j])), j % JG ? part[r] : zero);
+        if constexpr (FMT == kW4Int4) sum = mfma16x16x32(x[u][j], ones, j % JG ? sum : zero);
+        if (j % JG != JG - 1) continue;
+        const int f = u * Q + j / JG;  // the group's place in the block
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float scale = __uint_as_float(s.v[r][f] << scale_shift);
+          float zero_point = 8.f;
+          if constexpr (Z) zero_point = float(z.v[r][f]);
+#pragma unroll
+          for (int v = 0; v < A; ++v) {
+            float p = part[r][v];
+            if constexpr (FMT == kW4Int4) p = fmaf(-zero_point, sum[v], p);
+            acc[r][v] = fmaf(scale, p, acc[r][v]);
+          }
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
+  if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+  else static_cast<uint16_t*>(a.out)[at] = uint16_t(pack_bf16x2(v, 0.f));
+}
+
+// ---- routed form -------------------------------------------------------------
+// The workgroups of grid row y take pair y's expert (by_pair: fewer pairs
+// than experts; an expert's first pair takes them all) or expert y; row
+// a.experts is the pairs that are routed nowhere.
+__device__ __forceinline__ int w4_expert(const W4Args& a) {
+  const int e = a.by_pair ? a.expert_idx[blockIdx.y] : int(blockIdx.y);
+  return uniform(e < 0 || e >= a.experts ? a.experts : e);
+}
+
+struct W4List {
+  int pair[kW4Window], count, earlier;
+};
+
+// tile(pairs, tokens) for the expert's pairs, at most `most` at a time, or
+// for those routed nowhere zeros(pairs, tokens).  The order within the list
+// is any; a pair's result does not depend on it.
+template <typename Tile, typename Zeros>
+__device__ __forceinline__ void w4_for_pairs(const W4Args& a, int e, int most, W4List& list, Tile&& tile,
+                                             Zeros&& zeros) {
+  const int tid = threadIdx.x, threads = blockDim.x, y = blockIdx.y;
+  const bool nowhere = e == a.experts, alone = a.by_pair && nowhere;
+  for (int win = a.by_pair ? y : 0; win < a.m; win += kW4Window) {
+    if (tid == 0) {
+      list.count = alone;
+      list.earlier = 0;
+      if (alone) list.pair[0] = y;
+    }
+    lds_barrier();
+    if (!alone) {
+      if (a.by_pair && win == y)
+        for (int p = tid; p < y; p += threads)
+          if (a.expert_idx[p] == e) list.earlier = 1;
+      for (int p = win + tid; p < min(win + kW4Window, a.m); p += threads) {
+        const int v = a.expert_idx[p];
+        if (nowhere ? v < 0 || v >= a.experts : v == e) list.pair[atomicAdd(&list.count, 1)] = p;
+      }
+    }
+    lds_barrier();
+    if (list.earlier) break;  // an earlier pair's workgroups have this expert
+    const int count = list.count;
+    for (int t0 = 0; t0 < count; t0 += most) {
+      if (nowhere) zeros(list.pair + t0, min(most, count - t0));
+      else tile(list.pair + t0, min(most, count - t0));
+      lds_barrier();  // before the next tile's activations
+    }
+    if (alone) break;
+    lds_barrier();  // every wave has taken its count before it is cleared
+  }
+}
+
+// ---- k split over the waves --------------------------------------------------
+// What a block needs comes to the wave's own part of LDS by direct copies,
+// kBlocks blocks deep, in kCopies instructions.
 template <bool Z, int G, int TX, int R, int U>
 struct W4Ring {
-  static constexpr int kQ = 128 / G;                          // groups per step
-  static constexpr int kCodeCopies = U * R;                   // 1 KB each
-  static constexpr int kXCopies = (TX * U + 3) / 4;           // 1 KB each (TX = 1, U = 2: half)
-  using Scales = W4Scales<R, U * kQ>;
+  using Scales = W4Scales<R, U * (128 / G)>;
+  static constexpr int kCodeCopies = U * R, kXCopies = (TX * U + 3) / 4;  // 1 KB each
   // Counted per block; those of a period of several blocks are not (the waits are then a little stricter).
   static constexpr int kCopies = kCodeCopies + kXCopies + (Scales::kPeriod == 1 ? Scales::kCopies * (Z ? 2 : 1) : 0);
   static constexpr int kX = kCodeCopies * 1024, kBlock = kX + kXCopies * 1024;
   static constexpr int kScaleSlot = Scales::kBytes * (Z ? 2 : 1);
-  static constexpr int slots(int blocks) { return (blocks + Scales::kPeriod - 1) / Scales::kPeriod + (Scales::kPeriod > 1); }
+  // Blocks in flight reach into this many periods.
+  static constexpr int slots(int blocks) {
+    return (blocks + Scales::kPeriod - 1) / Scales::kPeriod + (Scales::kPeriod > 1);
+  }
   static constexpr int bytes(int blocks) { return blocks * kBlock + slots(blocks) * kScaleSlot; }
-  static constexpr int deep(int blocks) { return bytes(blocks) * kW4Waves <= kW4LdsBytes || blocks == 2 ? blocks : deep(blocks - 1); }
+  static constexpr int deep(int blocks) {
+    return bytes(blocks) * kW4Waves <= kW4LdsBytes || blocks == 2 ? blocks : deep(blocks - 1);
+  }
   static constexpr int kBlocks = deep(5), kSlots = slots(kBlocks), kScales = kBlocks * kBlock;
   static constexpr int kWave = bytes(kBlocks);
   static_assert(kW4Waves * kWave <= kW4LdsBytes && kCopies * (kBlocks - 1) < 64, "LDS and vmcnt");
   static_assert(kWave >= 16 * R * 20 * 4, "the partial sums take the ring's place");
 };
 
-// One workgroup: sets of 2^split_log2 waves, each set 16 R rows, its wave j
-// the blocks j, j + 2^split_log2, ...; the partial sums of a set are added
-// through LDS at the end.  Nothing else is shared, so the waves run without
-// barriers.  Codes lie in LDS as [row][piece of 16 bytes], a row's pieces
-// exchanged by (a part of) the row number, activations as [token][unit of 8
-// columns], a token's units exchanged by the token number, so that operand
-// reads meet no bank twice while every copy reads runs of 128 bytes or more.
-//
-// Groups of 128 columns take a lane's 16 bytes as four operands (dword j of
-// the four quarters is operand j, all of one group); shorter groups read
-// dword `quarter` of piece j, so that operand j holds 32 consecutive columns.
-// Up to four tokens stand in the operand rows 0, 4, 8, 12, so that each
-// lane's result register 0 is all it has to scale.
+// For few rows.  Sets of 2^split_log2 waves of a workgroup take 16 R rows
+// each, wave j of a set the blocks j, j + 2^split_log2, ...; the partial sums
+// of a set are added through LDS at the end.  Nothing else is shared, so the
+// waves run without barriers, each with its own copies of the activations it
+// needs.
 //
 // Grid: x row blocks; y token tiles, or in the routed form pairs or experts.
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   using L = W4Ring<Z, G, TX, R, U>;
-  constexpr int Q = L::kQ, JG = 4 / Q, F = U * Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  using Block = W4Block<FMT, Z, G, TX, R, U>;
+  using Scales = typename Block::Scales;
+  constexpr int F = Block::F, A = Block::A, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
   constexpr int kRows = 16 * R, kRedLd = TX == 16 ? 20 : TX;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), waves = blockDim.x >> 6;
+  const int quarter = lane >> 4, col = lane & 15;
   const int lks = a.split_log2, ks = 1 << lks, kidx = wave & (ks - 1), set = wave >> lks;
-  const int sets = waves >> lks;
-  const int row0 = blockIdx.x * (sets * kRows);
+  const int sets = waves >> lks, row0 = blockIdx.x * (sets * kRows);
   const unsigned half = unsigned(a.k) >> 1, groups = unsigned(a.k) / G;
   const int blocks = ((unsigned(a.k) + 128 * U - 1) / (128 * U) - kidx + ks - 1) >> lks;  // of this wave
 
-  int e = 0;
-  bool nowhere = false;
-  if constexpr (ROUTED) {
-    e = a.by_pair ? a.expert_idx[blockIdx.y] : blockIdx.y;
-    if (e < 0 || e >= a.experts) e = a.experts;  // pairs that are routed nowhere
-    e = uniform(e);
-    nowhere = e == a.experts;
-  }
-  const int64_t first_row = ROUTED ? (nowhere ? 0 : int64_t(e) * a.n) + row0 : row0;
+  const int e = ROUTED ? w4_expert(a) : 0;
+  const bool nowhere = ROUTED && e == a.experts;
+  const int64_t first_row = ROUTED && !nowhere ? int64_t(e) * a.n + row0 : row0;
   const uint8_t* wbase = a.w + first_row * half;
   const char* sbase = static_cast<const char*>(a.scales) + ((first_row * groups) << (a.scales_bf16 ? 1 : 2));
   const uint8_t* zbase = Z ? a.zeros + first_row * groups : nullptr;
   const char* ring = lds + wave * L::kWave;
   const uint32_t ring_at = lds_addr(lds) + wave * L::kWave;
 
-  // Code pieces past the row's end are its last piece again, scales past it the last one's.
+  // Code pieces past the row's end are its last piece again, scales past it the last one's; rows past the matrix its
+  // last row.
   const auto row_of = [&](int r) { return unsigned(min(set * kRows + r, a.n - 1 - row0)); };
-  const auto code_swap = [](int r) { return U == 4 ? r & 15 : U == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
-  using Scales = typename L::Scales;
   unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
 #pragma unroll
   for (int c = 0; c < L::kCodeCopies; ++c) {
     const int r = (c * 64 + lane) / kPieces;
     cend[c] = row_of(r) * half + half - 16;
-    cpos[c] = row_of(r) * half + ((lane % kPieces) ^ code_swap(r)) * 16;
+    cpos[c] = row_of(r) * half + ((lane % kPieces) ^ w4_swap<U>(r)) * 16;
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) soff[r] = row_of(r * 16 + (lane >> 2)) * groups;
@@ -230,7 +365,6 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       copy16_to_lds(wbase, min(blk * (64 * U) + cpos[c], cend[c]), at + c * 1024);
   };
 
-  const int quarter = lane >> 4, col = lane & 15;
   // One tile: tokens t = 0 .. tt - 1; x_row(t), out_row(t) their rows.  `begun`: the first blocks' weights are on
   // their way (all of the copies are then waited for before the first block).
   auto tile = [&](int tt, bool begun, auto x_row, auto out_row) {
@@ -262,16 +396,11 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     for (int b = 0; b < NB; ++b)
       if (b < blocks) copy_block(b, !begun);
 
-    const int tok = TX == 16 ? col : TX == 4 ? col >> 2 : 0;
-    const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
-    constexpr int A = TX == 16 ? 4 : 1;
+    const int token = w4_token<TX>(col);
+    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
     float acc[R][A] = {};
-    struct Operands {
-      v4i q[U][R], x[U][4];
-      Scales s, z;
-    };
     // Waits for block b and starts its LDS reads.
-    auto read = [&](Operands& o, int b) {
+    auto read = [&](Block& o, int b) {
       const int newer = min(blocks - 1 - b, NB - 1);  // blocks in flight after this one
       if (newer >= NB - 1) copies_left<(NB - 1) * L::kCopies>();
       else if (NB > 4 && newer == 3) copies_left<(NB > 4 ? 3 : 0) * L::kCopies>();
@@ -279,75 +408,21 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       else if (newer == 1) copies_left<L::kCopies>();
       else copies_left<0>();
       const char* at = ring + (b % NB) * L::kBlock;
-      const char* scales_at = ring + L::kScales + b / Scales::kPeriod % L::kSlots * L::kScaleSlot;
-      o.s.read(scales_at, col, b % Scales::kPeriod);
-      if constexpr (Z) o.z.read(scales_at + Scales::kBytes, col, b % Scales::kPeriod);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = r * 16 + col, swap = code_swap(row);
-          if constexpr (G == 128) {
-            o.q[u][r] = *reinterpret_cast<const v4i*>(at + (row * kPieces + ((4 * u + quarter) ^ swap)) * 16);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o.q[u][r][j] = *reinterpret_cast<const int*>(at + (row * kPieces + ((4 * u + j) ^ swap)) * 16 + quarter * 4);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int unit = 16 * u + (G == 128 ? 4 * quarter + j : 4 * j + quarter);
-          o.x[u][j] = *reinterpret_cast<const v4i*>(at + L::kX + (tok * kUnits + (unit ^ tok)) * 16);
-        }
-      }
-    };
-    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
-    auto products = [&](Operands& o, int b) {
-      const unsigned g0 = (kidx + (b << lks)) * (U * Q);
-      if (g0 + U * Q > groups) {  // no scale may meet the empty columns' zero sums
-#pragma unroll
-        for (int f = 0; f < U * Q; ++f)
-#pragma unroll
-          for (int r = 0; r < R; ++r) o.s.v[r][f] = g0 + f < groups ? o.s.v[r][f] : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v4f part[R], sum;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v4f zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            part[r] = mfma16x16x32(o.x[u][j], w4_decode<FMT>(unsigned(o.q[u][r][j])), j % JG ? part[r] : zero);
-          if constexpr (FMT == kW4Int4) sum = mfma16x16x32(o.x[u][j], ones, j % JG ? sum : zero);
-          if (j % JG == JG - 1) {
-            const int f = u * Q + j / JG;  // the group's place in the block
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const float scale = __uint_as_float(o.s.v[r][f] << scale_shift);
-              float zero_point = 8.f;
-              if constexpr (Z) zero_point = float(o.z.v[r][f]);
-#pragma unroll
-              for (int v = 0; v < A; ++v) {
-                float p = part[r][v];
-                if constexpr (FMT == kW4Int4) p = fmaf(-zero_point, sum[v], p);
-                acc[r][v] = fmaf(scale, p, acc[r][v]);
-              }
-            }
-          }
-        }
-      }
+      const char* scales = ring + L::kScales + b / Scales::kPeriod % L::kSlots * L::kScaleSlot;
+      o.s.read(scales, col, b % Scales::kPeriod);
+      if constexpr (Z) o.z.read(scales + Scales::kBytes, col, b % Scales::kPeriod);
+      o.read_codes(at, quarter, col);
+      o.read_x(at + L::kX + token * (kUnits * 16), quarter, token);
     };
     // Block b's products while block b + 1 is read from LDS; its place is then copied anew.
-    auto turn = [&](Operands& now, Operands& next, int b) {
+    auto turn = [&](Block& now, Block& next, int b) {
       if (b + 1 < blocks) read(next, b + 1);
       __builtin_amdgcn_sched_barrier(0);
-      products(now, b);
+      now.products(acc, (kidx + (b << lks)) * F, groups, scale_shift);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // block b + 1 has been read
       if (b + 1 + NB < blocks) copy_block(b + 1 + NB, true);
     };
-    Operands o0, o1;
+    Block o0, o1;
     if (blocks > 0) {
       if (begun) copies_left<0>();
       read(o0, 0);
@@ -365,12 +440,13 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float* p = red + (wave * kRows + r * 16 + col) * kRedLd;
-      if constexpr (TX == 16) *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+      if constexpr (TX == 16)
+        *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
       else if (quarter < TX) p[quarter] = acc[r][0];
     }
     lds_barrier();
     for (int o = tid; o < sets * kRows * TX; o += waves * kWave) {
-      const int rr = o % (16 * R), t = o / (16 * R) % TX, st = o / (16 * R * TX), row = row0 + st * kRows + rr;
+      const int rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
       const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
       float v = 0.f;
 #pragma unroll
@@ -378,10 +454,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
         const float u = p[(j & (ks - 1)) * kRows * kRedLd];
         v += j < ks ? u : 0.f;
       }
-      if (row >= a.n || t >= tt) continue;
-      const int64_t out = out_row(t) * a.n + row;
-      if (a.out_f32) static_cast<float*>(a.out)[out] = v;
-      else static_cast<uint16_t*>(a.out)[out] = uint16_t(pack_bf16x2(v, 0.f));
+      if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, v);
     }
   };
 
@@ -390,58 +463,31 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     const auto row = [&](int t) { return int64_t(base + t); };
     tile(min(TX, a.m - base), false, row, row);
   } else {
-    const bool alone = a.by_pair && nowhere;
+    __shared__ W4List list;
     bool begun = !nowhere;  // the weights need no list
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       if (begun && b < blocks) copy_weights(b);
-    for (int win = a.by_pair ? blockIdx.y : 0; win < a.m; win += kW4Window) {
-      if (tid == 0) list_n = earlier = 0;
-      lds_barrier();
-      if (alone) {
-        if (tid == 0) list[list_n++] = win;
-      } else {
-        if (a.by_pair && win == int(blockIdx.y))
-          for (int p = tid; p < win; p += waves * kWave)
-            if (a.expert_idx[p] == e) earlier = 1;
-        for (int p = win + tid; p < min(win + kW4Window, a.m); p += waves * kWave) {
-          const int v = a.expert_idx[p];
-          if (nowhere ? v < 0 || v >= a.experts : v == e) list[atomicAdd(&list_n, 1)] = p;
-        }
-      }
-      lds_barrier();
-      if (earlier) break;  // an earlier pair's workgroup has this expert
-      const int count = list_n;
-      for (int t0 = 0; t0 < count; t0 += TX) {
-        const int tt = min(TX, count - t0);
-        if (!nowhere) {
-          tile(tt, begun, [&](int t) { return int64_t(list[t0 + t] / a.x_div); },
-               [&](int t) { return int64_t(list[t0 + t]); });
+    w4_for_pairs(
+        a, e, TX, list,
+        [&](const int* pairs, int tt) {
+          tile(tt, begun, [&](int t) { return int64_t(pairs[t] / a.x_div); }, [&](int t) { return int64_t(pairs[t]); });
           begun = false;
           copies_left<0>();  // the stores: the next tile counts its copies alone
-        } else {
-          for (int o = tid; o < sets * kRows * tt; o += waves * kWave) {
-            const int row = row0 + o / tt;
-            if (row >= a.n) continue;
-            const int64_t out = int64_t(list[t0 + o % tt]) * a.n + row;
-            if (a.out_f32) static_cast<float*>(a.out)[out] = 0.f;
-            else static_cast<uint16_t*>(a.out)[out] = 0;
-          }
-        }
-        lds_barrier();  // before the next tile's copies
-      }
-      if (alone) break;
-      lds_barrier();  // every wave has taken its count before it is cleared
-    }
+        },
+        [&](const int* pairs, int tt) {
+          for (int o = tid; o < sets * kRows * tt; o += waves * kWave)
+            if (row0 + o / tt < a.n) w4_store(a, int64_t(pairs[o % tt]) * a.n + row0 + o / tt, 0.f);
+        });
     copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
 }
 
-// Rings of the streaming kernel: codes and scales alone.
-template <bool Z, int G, int TX, int R, int U>
+// ---- whole rows per wave -----------------------------------------------------
+// Rings of codes and scales alone.
+template <bool Z, int G, int R, int U>
 struct W4StreamRing {
-  static constexpr int kQ = 128 / G;
-  using Scales = W4Scales<R, U * kQ>;
+  using Scales = W4Scales<R, U * (128 / G)>;
   static constexpr int kCodeCopies = U * R;
   static constexpr int kCopies = kCodeCopies + (Scales::kPeriod == 1 ? Scales::kCopies * (Z ? 2 : 1) : 0);
   static constexpr int kBlock = kCodeCopies * 1024, kBlocks = 3;
@@ -450,51 +496,41 @@ struct W4StreamRing {
   static constexpr int kScales = kBlocks * kBlock, kWave = kScales + kSlots * kScaleSlot;
 };
 
-// The product where rows are plenty: every wave takes whole rows (16 R at a
-// time, no split of k), one after the other without a pause, and the
-// workgroup's waves share the tile's activations, which stay in LDS.
+// Where rows are plenty: every wave takes whole rows (16 R at a time, no split
+// of k), one set after the other without a pause, and the workgroup's waves
+// share the tile's activations, which stay in LDS.
 //
 // Grid: x groups of `reps` row sets per wave; y as in w4_kernel.
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
-  using L = W4StreamRing<Z, G, TX, R, U>;
-  constexpr int Q = L::kQ, JG = 4 / Q, F = U * Q, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
-  constexpr int kRows = 16 * R, kThreads = kW4Waves * kWave;
+  using L = W4StreamRing<Z, G, R, U>;
+  using Block = W4Block<FMT, Z, G, TX, R, U>;
+  using Scales = typename Block::Scales;
+  constexpr int F = Block::F, A = Block::A, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
+  constexpr int kRows = 16 * R;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  __shared__ int list[ROUTED ? kW4Window : 1], list_n, earlier;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6);
   const int quarter = lane >> 4, col = lane & 15;
   const unsigned half = unsigned(a.k) >> 1, groups = unsigned(a.k) / G;
   const int blocks = (unsigned(a.k) + 128 * U - 1) / (128 * U);
   const int sets = (a.n + kRows - 1) / kRows;
-  const int set0 = blockIdx.x * (kW4Waves * a.reps) + wave;  // then every kW4Waves-th, `reps` of them
-  const int my_sets = max(0, min(a.reps, (sets - set0 + kW4Waves - 1) / kW4Waves));
-  const int total = my_sets * blocks;
+  const int first_set = blockIdx.x * (kW4Waves * a.reps), set0 = first_set + wave;  // then every kW4Waves-th
+  const int total = max(0, min(a.reps, (sets - set0 + kW4Waves - 1) / kW4Waves)) * blocks;
 
-  int e = 0;
-  bool nowhere = false;
-  if constexpr (ROUTED) {
-    e = a.by_pair ? a.expert_idx[blockIdx.y] : blockIdx.y;
-    if (e < 0 || e >= a.experts) e = a.experts;  // pairs that are routed nowhere
-    e = uniform(e);
-    nowhere = e == a.experts;
-  }
-  const int64_t first_row = ROUTED ? (nowhere ? 0 : int64_t(e) * a.n) : 0;
-  const uint32_t ring_at = lds_addr(lds) + wave * L::kWave;
+  const int e = ROUTED ? w4_expert(a) : 0;
+  const bool nowhere = ROUTED && e == a.experts;
+  const int64_t first_row = ROUTED && !nowhere ? int64_t(e) * a.n : 0;
+  const uint32_t ring_at = lds_addr(lds) + wave * L::kWave, x_at = lds_addr(lds) + kW4Waves * L::kWave;
   const char* ring = lds + wave * L::kWave;
-  char* x_lds = lds + kW4Waves * L::kWave;
-  const uint32_t x_at = lds_addr(lds) + kW4Waves * L::kWave;
+  const char* x_lds = lds + kW4Waves * L::kWave;
   const int x_row_bytes = (blocks * (kUnits * 16) + 1023) & ~1023;
 
-  const auto code_swap = [](int r) { return U == 4 ? r & 15 : U == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
   // ---- the copies' side of the stream: the next block to bring
-  int c_block = 0, c_set = set0, c_slot = 0;
+  int c_block = 0, c_set = set0, c_slot = 0, c_scale_slot = 0;
   const uint8_t* wbase;
   const char* sbase;
   const uint8_t* zbase;
-  using Scales = typename L::Scales;
   unsigned cpos[L::kCodeCopies], cend[L::kCodeCopies], soff[R];
-  int c_scale_slot = 0;
   auto start_set = [&]() {
     const int64_t row = first_row + int64_t(c_set) * kRows;
     wbase = a.w + row * half;
@@ -506,7 +542,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
       const int r = (c * 64 + lane) / kPieces;
       const unsigned at = unsigned(min(r, last)) * half;
       cend[c] = at + half - 16;
-      cpos[c] = at + ((lane % kPieces) ^ code_swap(r)) * 16;
+      cpos[c] = at + ((lane % kPieces) ^ w4_swap<U>(r)) * 16;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) soff[r] = unsigned(min(r * 16 + (lane >> 2), last)) * groups;
@@ -545,18 +581,17 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
 
   auto tile = [&](int tt, auto x_row, auto out_row) {
     // the activations: token t's units, exchanged by t; units past the end are zero
-    for (int c = wave; c < tt * (x_row_bytes >> 10); c += kW4Waves) {
-      const int per = x_row_bytes >> 10, t = c / per, u = (c % per) * 64 + lane, unit = u ^ (t & 15);
+    const int per = x_row_bytes >> 10;
+    for (int c = wave; c < tt * per; c += kW4Waves) {
+      const int t = c / per, unit = ((c % per) * 64 + lane) ^ (t & 15);
       const void* src = unit < a.k >> 3 ? static_cast<const void*>(a.x + x_row(t) * a.x_ld + unit * 8) : &kW4Zeros;
       copy16_scattered_to_lds(src, x_at + c * 1024);
     }
     copies_left<0>();
     lds_barrier();
 
-    const int tok = TX == 16 ? col : TX == 4 ? col >> 2 : 0;
-    const char* x_mine = x_lds + tok * x_row_bytes;
-    const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
-    constexpr int A = TX == 16 ? 4 : 1;
+    const int token = w4_token<TX>(col);
+    const char* x_mine = x_lds + token * x_row_bytes;
     const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
     float acc[R][A] = {};
     int block = 0, slot = 0, scale_slot = L::kSlots - 1, set = set0;
@@ -567,70 +602,16 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
       else copies_left<0>();
       const char* at = ring + slot * L::kBlock;
       slot = slot + 1 == NB ? 0 : slot + 1;
-      v4i q[U][R], x[U][4];
-      Scales s, z;
       if (block % Scales::kPeriod == 0) scale_slot = scale_slot + 1 == L::kSlots ? 0 : scale_slot + 1;
-      const char* scales_at = ring + L::kScales + scale_slot * L::kScaleSlot;
-      s.read(scales_at, col, block % Scales::kPeriod);
-      if constexpr (Z) z.read(scales_at + Scales::kBytes, col, block % Scales::kPeriod);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = r * 16 + col, swap = code_swap(row);
-          if constexpr (G == 128) {
-            q[u][r] = *reinterpret_cast<const v4i*>(at + (row * kPieces + ((4 * u + quarter) ^ swap)) * 16);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              q[u][r][j] = *reinterpret_cast<const int*>(at + (row * kPieces + ((4 * u + j) ^ swap)) * 16 + quarter * 4);
-          }
-        }
-      }
+      const char* scales = ring + L::kScales + scale_slot * L::kScaleSlot;
+      Block o;
+      o.s.read(scales, col, block % Scales::kPeriod);
+      if constexpr (Z) o.z.read(scales + Scales::kBytes, col, block % Scales::kPeriod);
+      o.read_codes(at, quarter, col);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the block has been read
       if (b + NB < total) copy_next();
-      const char* xb = x_mine + block * (kUnits * 16);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int unit = 16 * u + (G == 128 ? 4 * quarter + j : 4 * j + quarter);
-          x[u][j] = *reinterpret_cast<const v4i*>(xb + (unit ^ tok) * 16);
-        }
-      const unsigned g0 = unsigned(block) * (U * Q);
-      if (g0 + U * Q > groups) {  // no scale may meet the empty columns' zero sums
-#pragma unroll
-        for (int f = 0; f < U * Q; ++f)
-#pragma unroll
-          for (int r = 0; r < R; ++r) s.v[r][f] = g0 + f < groups ? s.v[r][f] : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v4f part[R], sum;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v4f zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            part[r] = mfma16x16x32(x[u][j], w4_decode<FMT>(unsigned(q[u][r][j])), j % JG ? part[r] : zero);
-          if constexpr (FMT == kW4Int4) sum = mfma16x16x32(x[u][j], ones, j % JG ? sum : zero);
-          if (j % JG == JG - 1) {
-            const int f = u * Q + j / JG;  // the group's place in the block
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const float scale = __uint_as_float(s.v[r][f] << scale_shift);
-              float zero_point = 8.f;
-              if constexpr (Z) zero_point = float(z.v[r][f]);
-#pragma unroll
-              for (int v = 0; v < A; ++v) {
-                float p = part[r][v];
-                if constexpr (FMT == kW4Int4) p = fmaf(-zero_point, sum[v], p);
-                acc[r][v] = fmaf(scale, p, acc[r][v]);
-              }
-            }
-          }
-        }
-      }
+      o.read_x(x_mine + block * (kUnits * 16), quarter, token);
+      o.products(acc, unsigned(block) * F, groups, scale_shift);
       if (++block == blocks) {  // the rows are done
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -638,11 +619,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
 #pragma unroll
           for (int v = 0; v < A; ++v) {
             const int t = TX == 16 ? quarter * 4 + v : quarter;
-            if (row < a.n && t < tt) {
-              const int64_t out = out_row(t) * a.n + row;
-              if (a.out_f32) static_cast<float*>(a.out)[out] = acc[r][v];
-              else static_cast<uint16_t*>(a.out)[out] = uint16_t(pack_bf16x2(acc[r][v], 0.f));
-            }
+            if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, acc[r][v]);
             acc[r][v] = 0.f;
           }
         }
@@ -658,55 +635,23 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     begin();
     tile(min(TX, a.m - base), row, row);
   } else {
-    const bool alone = a.by_pair && nowhere;
+    __shared__ W4List list;
     bool begun = !nowhere;  // the weights need no list
     if (begun) begin();
-    for (int win = a.by_pair ? blockIdx.y : 0; win < a.m; win += kW4Window) {
-      if (tid == 0) list_n = earlier = 0;
-      lds_barrier();
-      if (alone) {
-        if (tid == 0) list[list_n++] = win;
-      } else {
-        if (a.by_pair && win == int(blockIdx.y))
-          for (int p = tid; p < win; p += kThreads)
-            if (a.expert_idx[p] == e) earlier = 1;
-        for (int p = win + tid; p < min(win + kW4Window, a.m); p += kThreads) {
-          const int v = a.expert_idx[p];
-          if (nowhere ? v < 0 || v >= a.experts : v == e) list[atomicAdd(&list_n, 1)] = p;
-        }
-      }
-      lds_barrier();
-      if (earlier) break;  // an earlier pair's workgroup has this expert
-      const int count = list_n;
-      for (int t0 = 0; t0 < count; t0 += TX) {
-        const int tt = min(TX, count - t0);
-        if (!nowhere) {
+    w4_for_pairs(
+        a, e, TX, list,
+        [&](const int* pairs, int tt) {
           if (!begun) begin();
           begun = false;
-          tile(tt, [&](int t) { return int64_t(list[t0 + t] / a.x_div); },
-               [&](int t) { return int64_t(list[t0 + t]); });
-        } else {
-          const int rows = min(a.n - blockIdx.x * (kW4Waves * a.reps) * kRows, kW4Waves * a.reps * kRows);
-          for (int o = tid; o < rows * tt; o += kThreads) {
-            const int64_t out = int64_t(list[t0 + o / rows]) * a.n + blockIdx.x * (kW4Waves * a.reps) * kRows + o % rows;
-            if (a.out_f32) static_cast<float*>(a.out)[out] = 0.f;
-            else static_cast<uint16_t*>(a.out)[out] = 0;
-          }
-        }
-        lds_barrier();  // before the next tile's activations
-      }
-      if (alone) break;
-      lds_barrier();  // every wave has taken its count before it is cleared
-    }
+          tile(tt, [&](int t) { return int64_t(pairs[t] / a.x_div); }, [&](int t) { return int64_t(pairs[t]); });
+        },
+        [&](const int* pairs, int tt) {
+          const int row0 = first_set * kRows, rows = min(a.n - row0, kW4Waves * a.reps * kRows);
+          for (int o = tid; o < rows * tt; o += blockDim.x)
+            w4_store(a, int64_t(pairs[o / rows]) * a.n + row0 + o % rows, 0.f);
+        });
     copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
-}
-
-// out[m][n] = 0 (an empty reduction).
-__global__ void __launch_bounds__(256) w4_zero_kernel(uint32_t* __restrict__ out, int64_t words, int tail) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i < words) out[i] = 0;
-  if (i == words && tail) *reinterpret_cast<uint16_t*>(out + words) = 0;
 }
 
 }  // namespace fp8g

@@ -446,8 +446,11 @@ enum {
  *   w_scales [n][k / group], FP32 or BF16 (scales_dtype FP8G_F32 / FP8G_BF16)
  *   w_zeros  [n][k / group] uint8 (FP8G_INT4 only) or NULL
  *   out      [m][n], BF16 or FP32 (out_dtype)
- * group 32, 64 or 128 and k % group == 0 (FP8G_EUNSUPPORTED otherwise); any
- * m and n.  k = 0 gives zeros.  x, w, w_scales, w_zeros, out 16-byte aligned. */
+ * group 32, 64 or 128 and k % group == 0, k <= 2^20, n <= 2^30, m <= 65535 *
+ * 16 (FP8G_EUNSUPPORTED otherwise); any other m and n.  k = 0 gives zeros.
+ * x, w, w_scales, w_zeros, out 16-byte aligned.
+ * Meant for up to a few tens of rows: every 16 rows decode the matrix anew
+ * (the FP8 GEMMs serve longer batches). */
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream);
@@ -460,7 +463,8 @@ int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_forma
  *   w [num_experts][n][k / 2]; w_scales, w_zeros [num_experts][n][k / group]
  *   out [num_pairs][n]; a row of zeros where expert_idx[p] is outside
  *       [0, num_experts)
- * An expert's matrix is read once for the pairs that share it. */
+ * An expert's matrix is read once for the pairs that share it, 16 at a time
+ * (4 where there are no more pairs than experts).  num_experts <= 65534. */
 int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int32_t* expert_idx, int num_pairs,
                           const uint8_t* w, int w_format, const void* w_scales, int scales_dtype,
                           const uint8_t* w_zeros, int group, void* out, int out_dtype, int num_experts, int n, int k,
