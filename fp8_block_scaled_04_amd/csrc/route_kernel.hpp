@@ -49,8 +49,7 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = uint16_
 __device__ __forceinline__ float below(float l, float m) { return l == m ? 0.f : l - m; }
 
 // exp(x) for -104 <= x <= 88 (0 from the bottom of the range on): exp2 of the product with log2(e), whose rounding
-// error
-// is put back (without that, |x| * 2^-24 of relative error).
+// error is put back (without that, |x| * 2^-24 of relative error).
 __device__ __forceinline__ float exp_near(float x) {
   const float t = x * 1.44269502f;
   const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));

@@ -11,18 +11,26 @@ namespace fp8g {
 namespace host {
 namespace {
 
-// 8 waves on each of 256 CUs.  k is split only as far as that needs: 8 ways,
-// 4096 x 7168 (256 sets) takes 6.5 us, 4 ways 8.5, 2 ways 13, not split 22;
-// the waves that split a row set also exchange its sums, so no wider split is
-// made where the sets alone fill the CUs.
-constexpr int kFullWaves = 2048;
+// k is split over the waves of a workgroup, 8 ways up to kSplit8 row sets, 4
+// ways up to kSplit4, else 2 ways.  A workgroup of 8 waves fills a CU's LDS, one
+// of 4 half of it, so kSplit8 workgroups run at once, or twice as many small
+// ones, and a few more sets would cost a second round.  Measured with one token
+// (16 for those marked *), 8, 4 and 2 ways: 256 sets (4096 x 7168) 6.5, 8.5 and
+// 13 us; 320 (5120 x 5120) 7.6 and 7.0; 448 (7168 x 16384) 18.6 and 16.0.  4 and
+// 2 ways: 640 sets (10240 x 4096) 8.6 and 9.7; 768* (24576 x 1536) 8.7 and 9.6;
+// 896 (14336 x 4096) 10.7 and 10.1.
+constexpr int kSplit8 = 256, kSplit4 = 768;
 // Row sets from which on a wave takes whole rows.  Measured for one token,
 // whole rows against k split: 1024 sets (16384 x 4096) 13.8 and 10.4 us, 1536
 // (24576 x 1536) 7.6 and 8.2, 2048 (32768 x 2048) 9.5 and 10.5, 4096 (65536 x
 // 1024) 9.9 and 10.7; eight experts of 4096 x 2048 (2048) 11.6 and 13.5.
 constexpr int kStreamSets = 2048;
-constexpr int kStreamBytes = 64 * 1024;   // activations of a streaming workgroup, at most
-constexpr int kStreamWorkgroups = 2048;   // workgroups a long stream is dealt to
+constexpr int kStreamBytes = 64 * 1024;  // activations of a streaming workgroup, at most
+// Workgroups that a long stream is dealt to: a wave then takes several sets one
+// after another and the copies never pause between them (256 experts of 4096 x
+// 1024: 139 us, 152 with a workgroup for every 8 sets; one token, 1048576 x
+// 256: 38 and 49; no difference from k = 2048 on).
+constexpr int kStreamWorkgroups = 2048;
 
 int64_t cdiv64(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
@@ -44,9 +52,8 @@ int launch_kernel(W4Args a, hipStream_t s) {
                        dim3(kW4Waves * kWave), lds, s, a);
     return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH;
   }
-  // k is split over the waves of a workgroup until there is a wave for each of the CUs' places
-  int lks = 0;
-  while (lks < 3 && (sets << lks) < kFullWaves && (2 << lks) <= blocks) ++lks;
+  int lks = sets <= kSplit8 ? 3 : sets <= kSplit4 ? 2 : sets < kStreamSets ? 1 : 0;
+  while ((1 << lks) > std::max<int64_t>(1, blocks)) --lks;
   const int waves = lks == 3 ? 8 : 4;
   a.split_log2 = lks;
   const int lds = waves * W4Ring<Z, G, TX, R, U>::kWave;
@@ -58,15 +65,19 @@ int launch_kernel(W4Args a, hipStream_t s) {
 
 template <int FMT, bool Z, int G, bool ROUTED>
 int launch_tiles(const W4Args& a, hipStream_t s) {
-  constexpr int kSteps = G == 32 ? 1 : 2;  // 128-column steps of a block: four groups or fewer
-  // Tokens per expert: hardly ever above 1, 4 with 1/8, 1 on average (a second tile reads the matrix again: 128
-  // experts with 4 tokens each on average took 451 us by tiles of 4, 293 by tiles of 16).
+  // 128-column steps of a block: two hide more of a wave's latency (one token, 4096 x 7168: 6.4 us, 6.7 with one; 8
+  // experts of 4096 x 2048: 11.5 and 13.2), but groups of 32 and tiles of 16 tokens have their registers full with one.
+  constexpr int kSteps = G == 32 ? 1 : 2;
+  // Tokens a tile.  One, with more than one per expert unlikely (one token, 65536 x 1024: 9.1 us, 9.5 by tiles of 4;
+  // 8 experts of 4096 x 2048: 11.5 and 12.0).  Four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64 pairs with 64
+  // experts of 4096 x 2048: 53.7 and 60.9).  Else 16: a second tile decodes the matrix again (128 experts with 4 tokens
+  // each on average 451 us by tiles of 4, 293 by tiles of 16).
   if (ROUTED ? a.m <= a.experts / 8 : a.m == 1) return launch_kernel<FMT, Z, G, 1, 1, kSteps, ROUTED>(a, s);
   if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, kSteps, ROUTED>(a, s);
-  const int64_t sets = cdiv64(a.n, 32) * (ROUTED ? a.experts : cdiv64(a.m, 16));
-  // 32 rows a wave where there are enough (16 tokens, 7168 x 16384: 21 us, 26 with 16 rows), else 16 (5 tokens,
-  // 2111 x 7168: 6.8 us, 8.5 with 32)
-  if (sets * kW4Waves < kFullWaves / 2) return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
+  // 16 rows a wave as long as one workgroup each takes them all (16 tokens, 4096 x 7168: 7.9 us, 9.5 with 32 rows),
+  // 32 from there on (16 tokens, 4608 x 7168: 9.6 us, 12.9 with 16; 7168 x 16384: 18.2, 25.8 with 16).
+  const int64_t sets = cdiv64(a.n, 16) * (ROUTED ? a.experts : cdiv64(a.m, 16));
+  if (sets <= kSplit8) return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
   return launch_kernel<FMT, Z, G, 16, 2, 1, ROUTED>(a, s);
 }
 
