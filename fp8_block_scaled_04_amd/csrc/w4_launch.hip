@@ -22,9 +22,10 @@ namespace {
 constexpr int kSplit8 = 256, kSplit4 = 768;
 // Row sets from which on a wave takes whole rows.  Measured for one token,
 // whole rows against k split: 1024 sets (16384 x 4096) 13.8 and 10.4 us, 1536
-// (24576 x 1536) 7.6 and 8.2, 2048 (32768 x 2048) 9.5 and 10.5, 4096 (65536 x
-// 1024) 9.9 and 10.7; eight experts of 4096 x 2048 (2048) 11.6 and 13.5.
-constexpr int kStreamSets = 2048;
+// (24576 x 1536) 7.7 and 8.1, (24576 x 7168) 23.9 and 21.6, 1792 (28672 x 2048)
+// 9.3 and 10.8, 4096 (65536 x 1024) 9.9 and 10.7; six experts of 4096 x 2048
+// (1536) 10.2 and 14.2, eight (2048) 11.6 and 13.5.
+constexpr int kStreamSets = 1536;
 constexpr int kStreamBytes = 64 * 1024;  // activations of a streaming workgroup, at most
 // Workgroups that a long stream is dealt to: a wave then takes several sets one
 // after another and the copies never pause between them (256 experts of 4096 x
@@ -65,9 +66,9 @@ int launch_kernel(W4Args a, hipStream_t s) {
 
 template <int FMT, bool Z, int G, bool ROUTED>
 int launch_tiles(const W4Args& a, hipStream_t s) {
-  // 128-column steps of a block: two hide more of a wave's latency (one token, 4096 x 7168: 6.4 us, 6.7 with one; 8
-  // experts of 4096 x 2048: 11.5 and 13.2), but groups of 32 and tiles of 16 tokens have their registers full with one.
-  constexpr int kSteps = G == 32 ? 1 : 2;
+  // 128-column steps of a block: two hide more of a wave's latency (one token, 4096 x 7168: 6.4 us, 6.7 with one; with
+  // groups of 32 6.3 and 6.8; 8 experts of 4096 x 2048: 11.5 and 13.2).  For 16 tokens the rings would not fit LDS.
+  constexpr int kSteps = 2;
   // Tokens a tile.  One, with more than one per expert unlikely (one token, 65536 x 1024: 9.1 us, 9.5 by tiles of 4;
   // 8 experts of 4096 x 2048: 11.5 and 12.0).  Four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64 pairs with 64
   // experts of 4096 x 2048: 53.7 and 60.9).  Else 16: a second tile decodes the matrix again (128 experts with 4 tokens
