@@ -18,7 +18,7 @@
 // What bounds it: long batches the vector instructions of ranking (about 170
 // a token of 256 experts; the logits alone would take 7 us at the rate of a
 // large copy), short ones the chain of loads and exchanges.  32768 tokens of
-// 256 experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 16.2 us, 92 with
+// 256 experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 16.1 us, 92 with
 // one wave per token that picks one expert at a time; 8 tokens 4.4 us (13.5).
 #pragma once
 
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
 // 2^log2_lanes (at least topk) lanes per token, V consecutive experts per
 // lane; lane j computes v_j, which then goes round the lanes.  Bound by its
 // writes where the batch is long: 16384 tokens of 128 experts (BF16, softmax
-// over all) take 6.3 us, against 3.6 for the bytes at the rate of a large copy
+// over all) take 6.2 us, against 3.6 for the bytes at the rate of a large copy
 // and the launch.
 template <typename L, int V>
 __global__ void __launch_bounds__(256) moe_route_backward_kernel(const L* __restrict__ logits, int64_t ld,

@@ -23,11 +23,11 @@
 // four consecutive lanes read 64 bytes, 64 cycles when every lane reads a row
 // of its own, as the operand layout has it; so rows are copied by four or
 // eight lanes and turned in LDS.
-//   one token       4096 x 7168 INT4, groups of 128       6.3 us (2.4 TB/s; an empty launch takes 1.7)
-//   5 tokens        2111 x 7168 E2M1, groups of 32        6.9 us
-//   16 tokens       7168 x 16384 INT4 with zero points   20.5 us (3.0 TB/s)
-//   8 experts       4096 x 2048, one token               11.8 us (3.2 TB/s)
-//   128 experts     7168 x 2048, 64 tokens, 8 each        220 us (4.5 TB/s)
+//   one token       4096 x 7168 INT4, groups of 128       6.4 us (2.4 TB/s; an empty launch takes 1.7)
+//   5 tokens        2111 x 7168 E2M1, groups of 32        6.8 us (1.3 TB/s)
+//   16 tokens       7168 x 16384 INT4 with zero points   20.3 us (3.2 TB/s)
+//   8 experts       4096 x 2048, one token               11.7 us (3.1 TB/s)
+//   128 experts     7168 x 2048, 64 tokens, 8 each        214 us (4.6 TB/s)
 #pragma once
 
 #include "device_common.hpp"

@@ -450,7 +450,9 @@ enum {
  * 16 (FP8G_EUNSUPPORTED otherwise); any other m and n.  k = 0 gives zeros.
  * x, w, w_scales, w_zeros, out 16-byte aligned.
  * Meant for up to a few tens of rows: every 16 rows decode the matrix anew
- * (the FP8 GEMMs serve longer batches). */
+ * (the FP8 GEMMs serve longer batches).  The zero point is applied to a
+ * group's sums, so with FP8G_INT4 an infinity or a NaN in a row of x makes
+ * that row's outputs NaN; other rows do not see it. */
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream);

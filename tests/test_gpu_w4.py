@@ -181,6 +181,44 @@ def test_experts_of_many_rows(T, topk, E, n, k, per_pair, group, fmt, sdt, with_
     assert np.all(got[(e.reshape(-1) < 0) | (e.reshape(-1) >= E)] == 0)
 
 
+@pytest.mark.parametrize("m,n,k", [
+    (1, 4096, 1152), (4, 4097, 1152), (1, 12288, 1056), (3, 12289, 1152), (1, 24560, 1056), (2, 24561, 1152),
+    (16, 4096, 1152), (9, 4097, 1152), (17, 2048, 2176), (33, 1400, 2176), (16, 8192, 1056), (7, 8193, 1152),
+    (16, 24576, 640), (8, 24577, 640), (12, 49120, 320), (16, 49121, 320), (1, 560000, 64), (16, 1050000, 32)])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES[1:3] + TYPES[4:])
+def test_matvec_around_each_split(m, n, k, group, fmt, sdt, with_zeros, odt):
+    """Numbers of rows on both sides of where fewer waves share them, and where a wave takes several sets of them."""
+    require_gpu()
+    k = k // group * group or group
+    n = min(n, (1 << 25) // k)
+    rng = np.random.default_rng(m + n + k)
+    tw, w, ts, s, tz, z = matrix(rng, (), n, k, group, sdt, with_zeros)
+    tx, x = bf16(rng.normal(size=(m, k)))
+    out = Out((m, n), DT[odt], 5)
+    b.fp8_w4_matvec(strided(tx, 8 * (m % 2)), tw, ts, out.view, FMT[fmt], tz)
+    want, mag = moe_ops.w4_matvec(x, w, s, z, fmt == "e2m1")
+    check(out.numpy(), want, mag, k, odt)
+
+
+@pytest.mark.parametrize("T,topk,E,n,k,per_pair", [
+    (500, 1, 500, 1040, 64, False), (400, 1, 300, 3700, 64, True), (4, 2, 9, 1000, 1056, False), (5, 2, 8, 456, 1152, True),
+    (1, 3, 40, 4096, 640, False), (2, 3, 6, 4097, 640, True)])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES[1:3] + TYPES[4:])
+def test_experts_around_each_split(T, topk, E, n, k, per_pair, group, fmt, sdt, with_zeros, odt):
+    require_gpu()
+    k = k // group * group
+    rng = np.random.default_rng(T + E + n)
+    e = rng.integers(0, E, (T, topk)).astype(np.int32)
+    tw, w, ts, s, tz, z = matrix(rng, (E,), n, k, group, sdt, with_zeros)
+    tx, x = bf16(rng.normal(size=(T * topk if per_pair else T, k)))
+    out = Out((T * topk, n), DT[odt], 5)
+    b.fp8_w4_matvec_experts(tx, dev(e), tw, ts, out.view, FMT[fmt], tz)
+    want, mag = moe_ops.w4_matvec_experts(x, e, w, s, z, fmt == "e2m1")
+    check(out.numpy(), want, mag, k, odt)
+
+
 def test_streamed_matrices_past_32_bits():
     """Experts past 2^32 bytes, with enough pairs for whole rows per wave."""
     require_gpu()
