@@ -37,8 +37,9 @@ namespace fp8g {
 
 constexpr int kW4Int4 = 0, kW4E2M1 = 1;
 constexpr int kW4Waves = 8;     // per workgroup, at most (4 where k is split less: two workgroups fit a CU)
-constexpr int kW4Window = 512;   // pairs searched at a time for an expert's tokens
-constexpr int kW4LdsBytes = 156 * 1024;  // rings of a workgroup, at most (160 KB per CU)
+constexpr int kW4Window = 512;  // pairs searched at a time for an expert's tokens
+// Rings of a workgroup of 8 waves, at most: with a list of pairs each, two workgroups of 4 fit a CU's 160 KB.
+constexpr int kW4LdsBytes = 156 * 1024;
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
@@ -239,11 +240,12 @@ __device__ __forceinline__ int w4_expert(const W4Args& a) {
 }
 
 struct W4List {
-  int pair[kW4Window], count, earlier;
+  uint16_t pair[kW4Window];  // from the window's start
+  int count, earlier;
 };
 
-// tile(pairs, tokens) for the expert's pairs, at most `most` at a time, or
-// for those routed nowhere zeros(pairs, tokens).  The order within the list
+// tile(pair_of, tokens) for the expert's pairs, at most `most` at a time, or
+// for those routed nowhere zeros(pair_of, tokens).  The order within the list
 // is any; a pair's result does not depend on it.
 template <typename Tile, typename Zeros>
 __device__ __forceinline__ void w4_for_pairs(const W4Args& a, int e, int most, W4List& list, Tile&& tile,
@@ -254,7 +256,7 @@ __device__ __forceinline__ void w4_for_pairs(const W4Args& a, int e, int most, W
     if (tid == 0) {
       list.count = alone;
       list.earlier = 0;
-      if (alone) list.pair[0] = y;
+      if (alone) list.pair[0] = 0;  // win == y
     }
     lds_barrier();
     if (!alone) {
@@ -263,15 +265,16 @@ __device__ __forceinline__ void w4_for_pairs(const W4Args& a, int e, int most, W
           if (a.expert_idx[p] == e) list.earlier = 1;
       for (int p = win + tid; p < min(win + kW4Window, a.m); p += threads) {
         const int v = a.expert_idx[p];
-        if (nowhere ? v < 0 || v >= a.experts : v == e) list.pair[atomicAdd(&list.count, 1)] = p;
+        if (nowhere ? v < 0 || v >= a.experts : v == e) list.pair[atomicAdd(&list.count, 1)] = uint16_t(p - win);
       }
     }
     lds_barrier();
     if (list.earlier) break;  // an earlier pair's workgroups have this expert
     const int count = list.count;
     for (int t0 = 0; t0 < count; t0 += most) {
-      if (nowhere) zeros(list.pair + t0, min(most, count - t0));
-      else tile(list.pair + t0, min(most, count - t0));
+      const auto pair_of = [&](int t) { return win + list.pair[t0 + t]; };
+      if (nowhere) zeros(pair_of, min(most, count - t0));
+      else tile(pair_of, min(most, count - t0));
       lds_barrier();  // before the next tile's activations
     }
     if (alone) break;
@@ -470,14 +473,14 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       if (begun && b < blocks) copy_weights(b);
     w4_for_pairs(
         a, e, TX, list,
-        [&](const int* pairs, int tt) {
-          tile(tt, begun, [&](int t) { return int64_t(pairs[t] / a.x_div); }, [&](int t) { return int64_t(pairs[t]); });
+        [&](auto pair_of, int tt) {
+          tile(tt, begun, [&](int t) { return int64_t(pair_of(t) / a.x_div); }, [&](int t) { return int64_t(pair_of(t)); });
           begun = false;
           copies_left<0>();  // the stores: the next tile counts its copies alone
         },
-        [&](const int* pairs, int tt) {
+        [&](auto pair_of, int tt) {
           for (int o = tid; o < sets * kRows * tt; o += waves * kWave)
-            if (row0 + o / tt < a.n) w4_store(a, int64_t(pairs[o % tt]) * a.n + row0 + o / tt, 0.f);
+            if (row0 + o / tt < a.n) w4_store(a, int64_t(pair_of(o % tt)) * a.n + row0 + o / tt, 0.f);
         });
     copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
@@ -640,15 +643,15 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     if (begun) begin();
     w4_for_pairs(
         a, e, TX, list,
-        [&](const int* pairs, int tt) {
+        [&](auto pair_of, int tt) {
           if (!begun) begin();
           begun = false;
-          tile(tt, [&](int t) { return int64_t(pairs[t] / a.x_div); }, [&](int t) { return int64_t(pairs[t]); });
+          tile(tt, [&](int t) { return int64_t(pair_of(t) / a.x_div); }, [&](int t) { return int64_t(pair_of(t)); });
         },
-        [&](const int* pairs, int tt) {
+        [&](auto pair_of, int tt) {
           const int row0 = first_set * kRows, rows = min(a.n - row0, kW4Waves * a.reps * kRows);
           for (int o = tid; o < rows * tt; o += blockDim.x)
-            w4_store(a, int64_t(pairs[o / rows]) * a.n + row0 + o % rows, 0.f);
+            w4_store(a, int64_t(pair_of(o / rows)) * a.n + row0 + o % rows, 0.f);
         });
     copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
