@@ -67,7 +67,7 @@ int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_forma
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream) {
   const W4Args a{x, x_ld, w, w_scales, w_zeros, out, scales_dtype == FP8G_BF16, out_dtype == FP8G_F32, m, n, k,
-                 nullptr, 1, 1, 0, 0, 0};
+                 nullptr, 1, 1, 0, 0};
   bool empty;
   if (int st = check(a, w_format, scales_dtype, out_dtype, group, &empty)) return st;
   return empty ? FP8G_OK : launch(a, w_format, group, static_cast<hipStream_t>(stream));
@@ -80,7 +80,7 @@ int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int
   if (num_pairs < 0 || x_rows < 0 || num_experts < 1) return FP8G_EINVAL;
   if (num_pairs > 0 && (x_rows == 0 || num_pairs % x_rows != 0)) return FP8G_EINVAL;
   const W4Args a{x, x_ld, w, w_scales, w_zeros, out, scales_dtype == FP8G_BF16, out_dtype == FP8G_F32, num_pairs, n, k,
-                 expert_idx, num_experts, num_pairs > 0 ? num_pairs / x_rows : 1, 0, 0, 0};
+                 expert_idx, num_experts, num_pairs > 0 ? num_pairs / x_rows : 1, 0, 0};
   bool empty;
   if (int st = check(a, w_format, scales_dtype, out_dtype, group, &empty)) return st;
   if (empty) return FP8G_OK;

@@ -37,9 +37,11 @@ namespace fp8g {
 
 constexpr int kW4Int4 = 0, kW4E2M1 = 1;
 constexpr int kW4Waves = 8;     // per workgroup, at most (4 where k is split less: two workgroups fit a CU)
-constexpr int kW4Window = 512;  // pairs searched at a time for an expert's tokens
-// Rings of a workgroup of 8 waves, at most: with a list of pairs each, two workgroups of 4 fit a CU's 160 KB.
+// Rings of a workgroup of 8 waves, at most: with a tile's pairs each, two workgroups of 4 fit a CU's 160 KB.
 constexpr int kW4LdsBytes = 156 * 1024;
+constexpr int kW4MaxExperts = 4096;  // their counts take the rings' place in LDS
+// Routed form, tiles of up to 4 pairs: a workgroup row per pair; of 16: per expert.
+constexpr bool w4_by_pair(int tx) { return tx < 16; }
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
@@ -231,55 +233,127 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
 }
 
 // ---- routed form -------------------------------------------------------------
-// The workgroups of grid row y take pair y's expert (by_pair: fewer pairs
-// than experts; an expert's first pair takes them all) or expert y; row
-// a.experts is the pairs that are routed nowhere.
-__device__ __forceinline__ int w4_expert(const W4Args& a) {
-  const int e = a.by_pair ? a.expert_idx[blockIdx.y] : int(blockIdx.y);
-  return uniform(e < 0 || e >= a.experts ? a.experts : e);
-}
-
-struct W4List {
-  uint16_t pair[kW4Window];  // from the window's start
-  int count, earlier;
+// A tile is TX pairs of one expert that follow one another, the t-th tile the
+// pairs of rank t * TX .. in the order of their indices.  Grid row y takes
+//   tiles of up to 4 (no more pairs than experts): the tile that pair y
+//   begins, if any;
+//   tiles of 16: y < experts the first tile of expert y, y = experts the pairs
+//   that are routed nowhere, further rows the experts' further tiles in order
+//   (a.m / 17 at most), which a count of every expert's pairs finds.
+// So an expert that many tokens chose has a workgroup for each of its tiles,
+// not one that works through them.
+template <int TX>
+struct W4Tile {
+  int pair[TX];
+  int counts[kW4Waves];  // of the waves' pairs in a window of blockDim pairs
 };
 
-// tile(pair_of, tokens) for the expert's pairs, at most `most` at a time, or
-// for those routed nowhere zeros(pair_of, tokens).  The order within the list
-// is any; a pair's result does not depend on it.
-template <typename Tile, typename Zeros>
-__device__ __forceinline__ void w4_for_pairs(const W4Args& a, int e, int most, W4List& list, Tile&& tile,
-                                             Zeros&& zeros) {
-  const int tid = threadIdx.x, threads = blockDim.x, y = blockIdx.y;
-  const bool nowhere = e == a.experts, alone = a.by_pair && nowhere;
-  for (int win = a.by_pair ? y : 0; win < a.m; win += kW4Window) {
-    if (tid == 0) {
-      list.count = alone;
-      list.earlier = 0;
-      if (alone) list.pair[0] = 0;  // win == y
-    }
+// Of the pairs p in [from, to) with expert_idx[p] = e, those of rank first ..
+// first + TX - 1 are entered in the tile, where the first found has rank
+// `rank`; returns the rank after the last.
+template <int TX>
+__device__ __forceinline__ int w4_find_pairs(const W4Args& a, int e, int from, int to, int rank, int first,
+                                             W4Tile<TX>& tile) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), waves = blockDim.x >> 6;
+  for (int win = from; win < to && rank < first + TX; win += blockDim.x) {
+    const bool found = win + tid < to && a.expert_idx[win + tid] == e;
+    const uint64_t mask = __ballot(found);
+    if (lane == 0) tile.counts[wave] = __popcll(mask);
     lds_barrier();
-    if (!alone) {
-      if (a.by_pair && win == y)
-        for (int p = tid; p < y; p += threads)
-          if (a.expert_idx[p] == e) list.earlier = 1;
-      for (int p = win + tid; p < min(win + kW4Window, a.m); p += threads) {
-        const int v = a.expert_idx[p];
-        if (nowhere ? v < 0 || v >= a.experts : v == e) list.pair[atomicAdd(&list.count, 1)] = uint16_t(p - win);
-      }
+    int mine = rank;
+    for (int w = 0; w < waves; ++w) {
+      const int c = tile.counts[w];
+      mine += w < wave ? c : 0;
+      rank += c;
     }
+    rank = uniform(rank);
+    mine += __popcll(mask & ((uint64_t(1) << lane) - 1));
+    if (found && mine >= first && mine < first + TX) tile.pair[mine - first] = win + tid;
     lds_barrier();
-    if (list.earlier) break;  // an earlier pair's workgroups have this expert
-    const int count = list.count;
-    for (int t0 = 0; t0 < count; t0 += most) {
-      const auto pair_of = [&](int t) { return win + list.pair[t0 + t]; };
-      if (nowhere) zeros(pair_of, min(most, count - t0));
-      else tile(pair_of, min(most, count - t0));
-      lds_barrier();  // before the next tile's activations
-    }
-    if (alone) break;
-    lds_barrier();  // every wave has taken its count before it is cleared
   }
+  return rank;
+}
+
+// The j-th of the experts' tiles after their first ones: its expert (-1: there are fewer) and the rank it starts at.
+template <int TX>
+__device__ __forceinline__ int w4_further_tile(const W4Args& a, int j, int* hist, int& first) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  for (int e = tid; e < a.experts; e += blockDim.x) hist[e] = 0;
+  lds_barrier();
+  for (int p = tid; p < a.m; p += blockDim.x) {
+    const int v = a.expert_idx[p];
+    if (v >= 0 && v < a.experts) atomicAdd(&hist[v], 1);
+  }
+  lds_barrier();
+  int expert = -1;
+  for (int c = 0; c < a.experts; c += kWave) {
+    const int more = c + lane < a.experts ? max(0, (hist[c + lane] + TX - 1) / TX - 1) : 0;
+    int upto = more;  // with the lanes before
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const int v = __shfl_up(upto, d, kWave);
+      upto += lane >= d ? v : 0;
+    }
+    const uint64_t past = __ballot(upto > j);
+    if (past) {
+      const int at = __ffsll(static_cast<unsigned long long>(past)) - 1;
+      expert = uniform(c + at);
+      first = uniform((j - __shfl(upto - more, at, kWave) + 1) * TX);
+      break;
+    }
+    j -= uniform(__shfl(upto, kWave - 1, kWave));
+  }
+  lds_barrier();  // hist is free again
+  return expert;
+}
+
+// This workgroup's tile: its expert (a.experts: pairs routed nowhere, -1:
+// nothing to do) and its number of pairs.  `scratch`: a.experts ints of LDS.
+template <int TX>
+__device__ __forceinline__ int w4_routed_tile(const W4Args& a, W4Tile<TX>& tile, int* scratch, int& count) {
+  const int y = blockIdx.y;
+  if constexpr (w4_by_pair(TX)) {
+    const int e = uniform(a.expert_idx[y]);
+    if (e < 0 || e >= a.experts) return a.experts;
+    count = 1;
+    if constexpr (TX > 1) {
+      const int rank = w4_find_pairs<TX>(a, e, 0, y, 0, a.m, tile);
+      if (rank % TX) return -1;  // in an earlier pair's tile
+      count = min(TX, w4_find_pairs<TX>(a, e, y, a.m, rank, rank, tile) - rank);
+    }
+    return e;
+  } else {
+    if (y == a.experts) return y;
+    int e = y, first = 0;
+    if (y > a.experts) e = w4_further_tile<TX>(a, y - a.experts - 1, scratch, first);
+    count = e < 0 ? 0 : min(TX, w4_find_pairs<TX>(a, e, 0, a.m, 0, first, tile) - first);
+    return count > 0 ? e : -1;
+  }
+}
+
+// out = 0 in rows row0 .. row0 + rows - 1 of the matrix for the pairs that are routed nowhere.
+template <int TX>
+__device__ __forceinline__ void w4_store_zeros(const W4Args& a, int row0, int rows) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), threads = blockDim.x;
+  if constexpr (w4_by_pair(TX)) {
+    for (int o = tid; o < rows; o += threads) w4_store(a, int64_t(blockIdx.y) * a.n + row0 + o, 0.f);
+    return;
+  }
+  for (int win = 0; win < a.m; win += threads) {
+    const int v = win + tid < a.m ? a.expert_idx[win + tid] : 0;
+    for (uint64_t left = __ballot(v < 0 || v >= a.experts); left; left &= left - 1) {
+      const int p = win + wave * kWave + __ffsll(static_cast<unsigned long long>(left)) - 1;
+      for (int o = lane; o < rows; o += kWave) w4_store(a, int64_t(p) * a.n + row0 + o, 0.f);
+    }
+  }
+}
+
+// The pair (routed form) or row that token t of the workgroup's tile is.
+template <bool ROUTED, int TX>
+__device__ __forceinline__ int w4_row(const W4Tile<TX>& tile, int t) {
+  if constexpr (!ROUTED) return int(blockIdx.y) * TX + t;
+  else if constexpr (TX == 1) return blockIdx.y;
+  else return tile.pair[t];
 }
 
 // ---- k split over the waves --------------------------------------------------
@@ -313,7 +387,7 @@ struct W4Ring {
 // waves run without barriers, each with its own copies of the activations it
 // needs.
 //
-// Grid: x row blocks; y token tiles, or in the routed form pairs or experts.
+// Grid: x row blocks; y tiles of tokens, or the routed form's.
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   using L = W4Ring<Z, G, TX, R, U>;
@@ -329,9 +403,17 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   const unsigned half = unsigned(a.k) >> 1, groups = unsigned(a.k) / G;
   const int blocks = ((unsigned(a.k) + 128 * U - 1) / (128 * U) - kidx + ks - 1) >> lks;  // of this wave
 
-  const int e = ROUTED ? w4_expert(a) : 0;
-  const bool nowhere = ROUTED && e == a.experts;
-  const int64_t first_row = ROUTED && !nowhere ? int64_t(e) * a.n + row0 : row0;
+  int e = 0, tt = min(TX, a.m - int(blockIdx.y) * TX);
+  __shared__ W4Tile<TX> pairs;
+  if constexpr (ROUTED) {
+    e = w4_routed_tile<TX>(a, pairs, reinterpret_cast<int*>(lds), tt);
+    if (e == a.experts) w4_store_zeros<TX>(a, row0, min(sets * kRows, a.n - row0));
+    if (e < 0 || e == a.experts) return;
+  }
+  // the pair of the tile's token t, and its row of x
+  const auto out_row = [&](int t) { return int64_t(w4_row<ROUTED, TX>(pairs, t)); };
+  const auto x_row = [&](int t) { return int64_t(w4_row<ROUTED, TX>(pairs, t) / (ROUTED ? a.x_div : 1)); };
+  const int64_t first_row = int64_t(e) * a.n + row0;
   const uint8_t* wbase = a.w + first_row * half;
   const char* sbase = static_cast<const char*>(a.scales) + ((first_row * groups) << (a.scales_bf16 ? 1 : 2));
   const uint8_t* zbase = Z ? a.zeros + first_row * groups : nullptr;
@@ -368,121 +450,92 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       copy16_to_lds(wbase, min(blk * (64 * U) + cpos[c], cend[c]), at + c * 1024);
   };
 
-  // One tile: tokens t = 0 .. tt - 1; x_row(t), out_row(t) their rows.  `begun`: the first blocks' weights are on
-  // their way (all of the copies are then waited for before the first block).
-  auto tile = [&](int tt, bool begun, auto x_row, auto out_row) {
-    const uint16_t* xsrc[L::kXCopies];  // this lane's unit of block 0; units past the end come from kW4Zeros
-    int xunit[L::kXCopies];
+  const uint16_t* xsrc[L::kXCopies];  // this lane's unit of block 0; units past the end come from kW4Zeros
+  int xunit[L::kXCopies];
 #pragma unroll
-    for (int c = 0; c < L::kXCopies; ++c) {
-      const int t = (c * 64 + lane) / kUnits % TX;
-      xunit[c] = (lane % kUnits) ^ (t & 15);
-      xsrc[c] = a.x + x_row(min(t, tt - 1)) * a.x_ld + xunit[c] * 8;
+  for (int c = 0; c < L::kXCopies; ++c) {
+    const int t = (c * 64 + lane) / kUnits % TX;
+    xunit[c] = (lane % kUnits) ^ (t & 15);
+    xsrc[c] = a.x + x_row(min(t, tt - 1)) * a.x_ld + xunit[c] * 8;
+  }
+  auto copy_block = [&](int b) {
+    const int unit0 = (kidx + (b << lks)) * kUnits;
+    const uint32_t at = ring_at + unsigned(b % NB) * L::kBlock;
+    if (unit0 + kUnits <= a.k >> 3) {
+#pragma unroll
+      for (int c = 0; c < L::kXCopies; ++c)
+        copy16_scattered_to_lds(xsrc[c] + unit0 * 8, at + L::kX + c * 1024);
+    } else {
+#pragma unroll
+      for (int c = 0; c < L::kXCopies; ++c)
+        copy16_scattered_to_lds(
+            unit0 + xunit[c] < a.k >> 3 ? static_cast<const void*>(xsrc[c] + unit0 * 8) : &kW4Zeros,
+            at + L::kX + c * 1024);
     }
-    auto copy_block = [&](int b, bool weights) {
-      const int unit0 = (kidx + (b << lks)) * kUnits;
-      const uint32_t at = ring_at + unsigned(b % NB) * L::kBlock;
-      if (unit0 + kUnits <= a.k >> 3) {
-#pragma unroll
-        for (int c = 0; c < L::kXCopies; ++c)
-          copy16_scattered_to_lds(xsrc[c] + unit0 * 8, at + L::kX + c * 1024);
-      } else {
-#pragma unroll
-        for (int c = 0; c < L::kXCopies; ++c)
-          copy16_scattered_to_lds(
-              unit0 + xunit[c] < a.k >> 3 ? static_cast<const void*>(xsrc[c] + unit0 * 8) : &kW4Zeros,
-              at + L::kX + c * 1024);
-      }
-      if (weights) copy_weights(b);
-    };
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (b < blocks) copy_block(b, !begun);
-
-    const int token = w4_token<TX>(col);
-    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
-    float acc[R][A] = {};
-    // Waits for block b and starts its LDS reads.
-    auto read = [&](Block& o, int b) {
-      const int newer = min(blocks - 1 - b, NB - 1);  // blocks in flight after this one
-      if (newer >= NB - 1) copies_left<(NB - 1) * L::kCopies>();
-      else if (NB > 4 && newer == 3) copies_left<(NB > 4 ? 3 : 0) * L::kCopies>();
-      else if (NB > 3 && newer == 2) copies_left<(NB > 3 ? 2 : 0) * L::kCopies>();
-      else if (newer == 1) copies_left<L::kCopies>();
-      else copies_left<0>();
-      const char* at = ring + (b % NB) * L::kBlock;
-      const char* scales = ring + L::kScales + b / Scales::kPeriod % L::kSlots * L::kScaleSlot;
-      o.s.read(scales, col, b % Scales::kPeriod);
-      if constexpr (Z) o.z.read(scales + Scales::kBytes, col, b % Scales::kPeriod);
-      o.read_codes(at, quarter, col);
-      o.read_x(at + L::kX + token * (kUnits * 16), quarter, token);
-    };
-    // Block b's products while block b + 1 is read from LDS; its place is then copied anew.
-    auto turn = [&](Block& now, Block& next, int b) {
-      if (b + 1 < blocks) read(next, b + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      now.products(acc, (kidx + (b << lks)) * F, groups, scale_shift);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // block b + 1 has been read
-      if (b + 1 + NB < blocks) copy_block(b + 1 + NB, true);
-    };
-    Block o0, o1;
-    if (blocks > 0) {
-      if (begun) copies_left<0>();
-      read(o0, 0);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (NB < blocks) copy_block(NB, true);
-    }
-    for (int b = 0; b < blocks; b += 2) {
-      turn(o0, o1, b);
-      if (b + 1 < blocks) turn(o1, o0, b + 1);
-    }
-
-    // ---- the sets' partial sums, added in the order of their waves
-    float* red = reinterpret_cast<float*>(lds);
-    lds_barrier();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float* p = red + (wave * kRows + r * 16 + col) * kRedLd;
-      if constexpr (TX == 16)
-        *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
-      else if (quarter < TX) p[quarter] = acc[r][0];
-    }
-    lds_barrier();
-    for (int o = tid; o < sets * kRows * TX; o += waves * kWave) {
-      const int rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
-      const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
-      float v = 0.f;
-#pragma unroll
-      for (int j = 0; j < kW4Waves; ++j) {  // all reads at once
-        const float u = p[(j & (ks - 1)) * kRows * kRedLd];
-        v += j < ks ? u : 0.f;
-      }
-      if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, v);
-    }
+    copy_weights(b);
   };
-
-  if constexpr (!ROUTED) {
-    const int base = blockIdx.y * TX;
-    const auto row = [&](int t) { return int64_t(base + t); };
-    tile(min(TX, a.m - base), false, row, row);
-  } else {
-    __shared__ W4List list;
-    bool begun = !nowhere;  // the weights need no list
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (begun && b < blocks) copy_weights(b);
-    w4_for_pairs(
-        a, e, TX, list,
-        [&](auto pair_of, int tt) {
-          tile(tt, begun, [&](int t) { return int64_t(pair_of(t) / a.x_div); }, [&](int t) { return int64_t(pair_of(t)); });
-          begun = false;
-          copies_left<0>();  // the stores: the next tile counts its copies alone
-        },
-        [&](auto pair_of, int tt) {
-          for (int o = tid; o < sets * kRows * tt; o += waves * kWave)
-            if (row0 + o / tt < a.n) w4_store(a, int64_t(pair_of(o % tt)) * a.n + row0 + o / tt, 0.f);
-        });
-    copies_left<0>();  // no copy may outlive the workgroup's LDS
+  for (int b = 0; b < NB; ++b)
+    if (b < blocks) copy_block(b);
+
+  const int token = w4_token<TX>(col);
+  const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
+  float acc[R][A] = {};
+  // Waits for block b and starts its LDS reads.
+  auto read = [&](Block& o, int b) {
+    const int newer = min(blocks - 1 - b, NB - 1);  // blocks in flight after this one
+    if (newer >= NB - 1) copies_left<(NB - 1) * L::kCopies>();
+    else if (NB > 4 && newer == 3) copies_left<(NB > 4 ? 3 : 0) * L::kCopies>();
+    else if (NB > 3 && newer == 2) copies_left<(NB > 3 ? 2 : 0) * L::kCopies>();
+    else if (newer == 1) copies_left<L::kCopies>();
+    else copies_left<0>();
+    const char* at = ring + (b % NB) * L::kBlock;
+    const char* scales = ring + L::kScales + b / Scales::kPeriod % L::kSlots * L::kScaleSlot;
+    o.s.read(scales, col, b % Scales::kPeriod);
+    if constexpr (Z) o.z.read(scales + Scales::kBytes, col, b % Scales::kPeriod);
+    o.read_codes(at, quarter, col);
+    o.read_x(at + L::kX + token * (kUnits * 16), quarter, token);
+  };
+  // Block b's products while block b + 1 is read from LDS; its place is then copied anew.
+  auto turn = [&](Block& now, Block& next, int b) {
+    if (b + 1 < blocks) read(next, b + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    now.products(acc, (kidx + (b << lks)) * F, groups, scale_shift);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // block b + 1 has been read
+    if (b + 1 + NB < blocks) copy_block(b + 1 + NB);
+  };
+  Block o0, o1;
+  if (blocks > 0) {
+    read(o0, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (NB < blocks) copy_block(NB);
+  }
+  for (int b = 0; b < blocks; b += 2) {
+    turn(o0, o1, b);
+    if (b + 1 < blocks) turn(o1, o0, b + 1);
+  }
+
+  // ---- the sets' partial sums, added in the order of their waves
+  float* red = reinterpret_cast<float*>(lds);
+  lds_barrier();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float* p = red + (wave * kRows + r * 16 + col) * kRedLd;
+    if constexpr (TX == 16)
+      *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+    else if (quarter < TX) p[quarter] = acc[r][0];
+  }
+  lds_barrier();
+  for (int o = tid; o < sets * kRows * TX; o += waves * kWave) {
+    const int rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
+    const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < kW4Waves; ++j) {  // all reads at once
+      const float u = p[(j & (ks - 1)) * kRows * kRedLd];
+      v += j < ks ? u : 0.f;
+    }
+    if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, v);
   }
 }
 
@@ -520,9 +573,17 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
   const int first_set = blockIdx.x * (kW4Waves * a.reps), set0 = first_set + wave;  // then every kW4Waves-th
   const int total = max(0, min(a.reps, (sets - set0 + kW4Waves - 1) / kW4Waves)) * blocks;
 
-  const int e = ROUTED ? w4_expert(a) : 0;
-  const bool nowhere = ROUTED && e == a.experts;
-  const int64_t first_row = ROUTED && !nowhere ? int64_t(e) * a.n : 0;
+  int e = 0, tt = min(TX, a.m - int(blockIdx.y) * TX);
+  __shared__ W4Tile<TX> pairs;
+  if constexpr (ROUTED) {
+    e = w4_routed_tile<TX>(a, pairs, reinterpret_cast<int*>(lds), tt);
+    const int row0 = first_set * kRows;
+    if (e == a.experts) w4_store_zeros<TX>(a, row0, min(kW4Waves * a.reps * kRows, a.n - row0));
+    if (e < 0 || e == a.experts) return;
+  }
+  const auto out_row = [&](int t) { return int64_t(w4_row<ROUTED, TX>(pairs, t)); };
+  const auto x_row = [&](int t) { return int64_t(w4_row<ROUTED, TX>(pairs, t) / (ROUTED ? a.x_div : 1)); };
+  const int64_t first_row = int64_t(e) * a.n;
   const uint32_t ring_at = lds_addr(lds) + wave * L::kWave, x_at = lds_addr(lds) + kW4Waves * L::kWave;
   const char* ring = lds + wave * L::kWave;
   const char* x_lds = lds + kW4Waves * L::kWave;
@@ -573,87 +634,57 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
       start_set();
     }
   };
-  auto begin = [&]() {
-    c_block = c_slot = c_scale_slot = 0;
-    c_set = set0;
-    start_set();
+  start_set();
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (b < total) copy_next();
-  };
+  for (int b = 0; b < NB; ++b)
+    if (b < total) copy_next();
 
-  auto tile = [&](int tt, auto x_row, auto out_row) {
-    // the activations: token t's units, exchanged by t; units past the end are zero
-    const int per = x_row_bytes >> 10;
-    for (int c = wave; c < tt * per; c += kW4Waves) {
-      const int t = c / per, unit = ((c % per) * 64 + lane) ^ (t & 15);
-      const void* src = unit < a.k >> 3 ? static_cast<const void*>(a.x + x_row(t) * a.x_ld + unit * 8) : &kW4Zeros;
-      copy16_scattered_to_lds(src, x_at + c * 1024);
-    }
-    copies_left<0>();
-    lds_barrier();
+  // the activations: token t's units, exchanged by t; units past the end are zero
+  const int per = x_row_bytes >> 10;
+  for (int c = wave; c < tt * per; c += kW4Waves) {
+    const int t = c / per, unit = ((c % per) * 64 + lane) ^ (t & 15);
+    const void* src = unit < a.k >> 3 ? static_cast<const void*>(a.x + x_row(t) * a.x_ld + unit * 8) : &kW4Zeros;
+    copy16_scattered_to_lds(src, x_at + c * 1024);
+  }
+  copies_left<0>();
+  lds_barrier();
 
-    const int token = w4_token<TX>(col);
-    const char* x_mine = x_lds + token * x_row_bytes;
-    const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
-    float acc[R][A] = {};
-    int block = 0, slot = 0, scale_slot = L::kSlots - 1, set = set0;
-    for (int b = 0; b < total; ++b) {
-      const int newer = min(total - 1 - b, NB - 1);  // blocks in flight after this one
-      if (newer == 2) copies_left<2 * L::kCopies>();
-      else if (newer == 1) copies_left<L::kCopies>();
-      else copies_left<0>();
-      const char* at = ring + slot * L::kBlock;
-      slot = slot + 1 == NB ? 0 : slot + 1;
-      if (block % Scales::kPeriod == 0) scale_slot = scale_slot + 1 == L::kSlots ? 0 : scale_slot + 1;
-      const char* scales = ring + L::kScales + scale_slot * L::kScaleSlot;
-      Block o;
-      o.s.read(scales, col, block % Scales::kPeriod);
-      if constexpr (Z) o.z.read(scales + Scales::kBytes, col, block % Scales::kPeriod);
-      o.read_codes(at, quarter, col);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the block has been read
-      if (b + NB < total) copy_next();
-      o.read_x(x_mine + block * (kUnits * 16), quarter, token);
-      o.products(acc, unsigned(block) * F, groups, scale_shift);
-      if (++block == blocks) {  // the rows are done
+  const int token = w4_token<TX>(col);
+  const char* x_mine = x_lds + token * x_row_bytes;
+  const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
+  float acc[R][A] = {};
+  int block = 0, slot = 0, scale_slot = L::kSlots - 1, set = set0;
+  for (int b = 0; b < total; ++b) {
+    const int newer = min(total - 1 - b, NB - 1);  // blocks in flight after this one
+    if (newer == 2) copies_left<2 * L::kCopies>();
+    else if (newer == 1) copies_left<L::kCopies>();
+    else copies_left<0>();
+    const char* at = ring + slot * L::kBlock;
+    slot = slot + 1 == NB ? 0 : slot + 1;
+    if (block % Scales::kPeriod == 0) scale_slot = scale_slot + 1 == L::kSlots ? 0 : scale_slot + 1;
+    const char* scales = ring + L::kScales + scale_slot * L::kScaleSlot;
+    Block o;
+    o.s.read(scales, col, block % Scales::kPeriod);
+    if constexpr (Z) o.z.read(scales + Scales::kBytes, col, block % Scales::kPeriod);
+    o.read_codes(at, quarter, col);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the block has been read
+    if (b + NB < total) copy_next();
+    o.read_x(x_mine + block * (kUnits * 16), quarter, token);
+    o.products(acc, unsigned(block) * F, groups, scale_shift);
+    if (++block == blocks) {  // the rows are done
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int row = set * kRows + r * 16 + col;
+      for (int r = 0; r < R; ++r) {
+        const int row = set * kRows + r * 16 + col;
 #pragma unroll
-          for (int v = 0; v < A; ++v) {
-            const int t = TX == 16 ? quarter * 4 + v : quarter;
-            if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, acc[r][v]);
-            acc[r][v] = 0.f;
-          }
+        for (int v = 0; v < A; ++v) {
+          const int t = TX == 16 ? quarter * 4 + v : quarter;
+          if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, acc[r][v]);
+          acc[r][v] = 0.f;
         }
-        block = 0;
-        set += kW4Waves;
       }
+      block = 0;
+      set += kW4Waves;
     }
-  };
-
-  if constexpr (!ROUTED) {
-    const int base = blockIdx.y * TX;
-    const auto row = [&](int t) { return int64_t(base + t); };
-    begin();
-    tile(min(TX, a.m - base), row, row);
-  } else {
-    __shared__ W4List list;
-    bool begun = !nowhere;  // the weights need no list
-    if (begun) begin();
-    w4_for_pairs(
-        a, e, TX, list,
-        [&](auto pair_of, int tt) {
-          if (!begun) begin();
-          begun = false;
-          tile(tt, [&](int t) { return int64_t(pair_of(t) / a.x_div); }, [&](int t) { return int64_t(pair_of(t)); });
-        },
-        [&](auto pair_of, int tt) {
-          const int row0 = first_set * kRows, rows = min(a.n - row0, kW4Waves * a.reps * kRows);
-          for (int o = tid; o < rows * tt; o += blockDim.x)
-            w4_store(a, int64_t(pair_of(o / rows)) * a.n + row0 + o % rows, 0.f);
-        });
-    copies_left<0>();  // no copy may outlive the workgroup's LDS
   }
 }
 

@@ -35,12 +35,17 @@ constexpr int kStreamWorkgroups = 2048;
 
 int64_t cdiv64(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
+// Tiles of 16 that the routed form has as a rule: counted by the experts alone, 512 pairs with 8 experts of 1024 x 1024
+// took 18.8 us, not 10.1 (k split in more parts than there was room for).
+int64_t routed_tiles(const W4Args& a) { return std::max(a.experts, a.m / 16); }
+
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 int launch_kernel(W4Args a, hipStream_t s) {
-  a.by_pair = ROUTED && a.m <= a.experts;
-  const int64_t slots = !ROUTED ? cdiv64(a.m, TX) : a.by_pair ? a.m : int64_t(a.experts) + 1;
+  // Grid rows, and how many of them have a tile as a rule.
+  const int64_t slots = !ROUTED ? cdiv64(a.m, TX) : w4_by_pair(TX) ? a.m : int64_t(a.experts) + 1 + a.m / (TX + 1);
+  const int64_t tiles = ROUTED && !w4_by_pair(TX) ? routed_tiles(a) : slots;
   if (slots > 65535) return FP8G_EUNSUPPORTED;
-  const int64_t sets = cdiv64(a.n, 16 * R) * slots, blocks = cdiv64(a.k, 128 * U);
+  const int64_t sets = cdiv64(a.n, 16 * R) * tiles, blocks = cdiv64(a.k, 128 * U);
   // Rows for every place of the CUs, and a tile's activations fit LDS: whole rows per wave.
   const int64_t x_bytes = (blocks * (256 * U) + 1023) / 1024 * 1024 * TX;
   if (sets >= kStreamSets && x_bytes <= kStreamBytes) {
@@ -66,18 +71,19 @@ int launch_kernel(W4Args a, hipStream_t s) {
 
 template <int FMT, bool Z, int G, bool ROUTED>
 int launch_tiles(const W4Args& a, hipStream_t s) {
+  if (ROUTED && a.experts > kW4MaxExperts) return FP8G_EUNSUPPORTED;
   // 128-column steps of a block: two hide more of a wave's latency (one token, 4096 x 7168: 6.4 us, 6.7 with one; with
   // groups of 32 6.3 and 6.8; 8 experts of 4096 x 2048: 11.5 and 13.2).  For 16 tokens the rings would not fit LDS.
   constexpr int kSteps = 2;
   // Tokens a tile.  One, with more than one per expert unlikely (one token, 65536 x 1024: 9.1 us, 9.5 by tiles of 4;
-  // 8 experts of 4096 x 2048: 11.5 and 12.0).  Four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64 pairs with 64
-  // experts of 4096 x 2048: 53.7 and 60.9).  Else 16: a second tile decodes the matrix again (128 experts with 4 tokens
-  // each on average 451 us by tiles of 4, 293 by tiles of 16).
+  // 8 experts of 4096 x 2048: 11.5 and 12.0).  Four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64 pairs with
+  // 64 experts of 4096 x 2048: 53.7 and 60.9).  Else 16: a second tile decodes the matrix again (128 experts with 4
+  // tokens each on average 451 us by tiles of 4, 293 by tiles of 16).
   if (ROUTED ? a.m <= a.experts / 8 : a.m == 1) return launch_kernel<FMT, Z, G, 1, 1, kSteps, ROUTED>(a, s);
   if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, kSteps, ROUTED>(a, s);
   // 16 rows a wave as long as one workgroup each takes them all (16 tokens, 4096 x 7168: 7.9 us, 9.5 with 32 rows),
   // 32 from there on (16 tokens, 4608 x 7168: 9.6 us, 12.9 with 16; 7168 x 16384: 18.2, 25.8 with 16).
-  const int64_t sets = cdiv64(a.n, 16) * (ROUTED ? a.experts : cdiv64(a.m, 16));
+  const int64_t sets = cdiv64(a.n, 16) * (ROUTED ? routed_tiles(a) : cdiv64(a.m, 16));
   if (sets <= kSplit8) return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
   return launch_kernel<FMT, Z, G, 16, 2, 1, ROUTED>(a, s);
 }

@@ -20,7 +20,6 @@ struct W4Args {
   int m, n, k;                // m: tokens, or pairs in the routed form
   const int32_t* expert_idx;  // routed form, else NULL
   int experts, x_div;         // experts; pairs per row of x
-  int by_pair;                // routed form: a workgroup row per pair (else per expert)
   // set at the launch
   int split_log2;             // 2^this waves of a workgroup share rows and split k
   int reps;                   // streaming kernel: row sets a wave takes

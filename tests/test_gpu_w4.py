@@ -219,6 +219,26 @@ def test_experts_around_each_split(T, topk, E, n, k, per_pair, group, fmt, sdt, 
     check(out.numpy(), want, mag, k, odt)
 
 
+@pytest.mark.parametrize("T,topk,E,n,k", [
+    (700, 1, 70, 100, 256), (40, 8, 200, 60, 128), (64, 8, 100, 4500, 64), (16, 4, 64, 50, 512)])
+@pytest.mark.parametrize("hot", [(0,), (69, 3), (63, 64, -1)])
+def test_experts_of_a_few_hot_ones(T, topk, E, n, k, hot):
+    """Most pairs with one to three experts: tiles of one expert by the dozen, other experts with one pair or none."""
+    require_gpu()
+    rng = np.random.default_rng(T + E)
+    hot = [h if h < E else E - 1 for h in hot]
+    e = rng.choice(np.int32(hot), (T, topk))
+    e[rng.random((T, topk)) < 0.1] = rng.integers(-1, E)
+    tw, w, ts, s, tz, z = matrix(rng, (E,), n, k, 32, "bf16", True)
+    tx, x = bf16(rng.normal(size=(T, k)))
+    out = Out((T * topk, n), torch.float32, 5)
+    b.fp8_w4_matvec_experts(tx, dev(e.astype(np.int32)), tw, ts, out.view, zeros=tz)
+    want, mag = moe_ops.w4_matvec_experts(x, e, w, s, z)
+    got = out.numpy()
+    check(got, want, mag, k, "f32")
+    assert np.all(got[e.reshape(-1) < 0] == 0)
+
+
 def test_streamed_matrices_past_32_bits():
     """Experts past 2^32 bytes, with enough pairs for whole rows per wave."""
     require_gpu()
