@@ -15,10 +15,10 @@
 // Picks that do not exist (fewer eligible experts than topk) have index -1
 // and weight 0.  All arithmetic is FP32.
 //
-// What bounds it: long batches the vector instructions of ranking (about 170
+// What bounds it: long batches the vector instructions of ranking (about 220
 // a token of 256 experts; the logits alone would take 7 us at the rate of a
 // large copy), short ones the chain of loads and exchanges.  32768 tokens of
-// 256 experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 16.1 us, 92 with
+// 256 experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 15.6 us, 92 with
 // one wave per token that picks one expert at a time; 8 tokens 4.4 us (13.5).
 #pragma once
 
@@ -88,11 +88,10 @@ __device__ __forceinline__ double key_min(double a, double b) {
 }
 // Experts that are not to be picked have the lowest score there is; any other is kept above it.
 constexpr float kNotAble = -kMaxFinite, kLeastAble = -3.4e38f;
-__device__ __forceinline__ double make_key(float score, unsigned rest) {  // rest = kRouteMaxExperts - 1 - expert
-  const float s = score + 0.f;  // no negative zero
-  u32x2 k = __builtin_bit_cast(u32x2, double(s));
-  const unsigned negative = unsigned(__float_as_int(s) >> 31) >> 22;  // 10 ones
-  k.x += rest ^ negative;
+// rest = kRouteMaxExperts - 1 - expert; a score is no negative zero (it is a sum with a positive one, if of zeros).
+__device__ __forceinline__ double make_key(float score, unsigned rest) {
+  u32x2 k = __builtin_bit_cast(u32x2, double(score));
+  k.x |= rest ^ (unsigned(__float_as_int(score) >> 31) & unsigned(kRouteMaxExperts - 1));
   return __builtin_bit_cast(double, k);
 }
 __device__ __forceinline__ int key_expert(double key) {

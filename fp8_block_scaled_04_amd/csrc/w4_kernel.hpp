@@ -23,11 +23,11 @@
 // four consecutive lanes read 64 bytes, 64 cycles when every lane reads a row
 // of its own, as the operand layout has it; so rows are copied by four or
 // eight lanes and turned in LDS.
-//   one token       4096 x 7168 INT4, groups of 128       6.4 us (2.4 TB/s; an empty launch takes 1.7)
-//   5 tokens        2111 x 7168 E2M1, groups of 32        6.8 us (1.3 TB/s)
+//   one token       4096 x 7168 INT4, groups of 128       6.6 us (2.3 TB/s; an empty launch takes 1.7)
+//   5 tokens        2111 x 7168 E2M1, groups of 32        7.1 us (1.2 TB/s)
 //   16 tokens       7168 x 16384 INT4 with zero points   20.3 us (3.2 TB/s)
-//   8 experts       4096 x 2048, one token               11.7 us (3.1 TB/s)
-//   128 experts     7168 x 2048, 64 tokens, 8 each        214 us (4.6 TB/s)
+//   8 experts       4096 x 2048, one token               10.9 us (3.4 TB/s)
+//   128 experts     7168 x 2048, 64 tokens, 8 each        206 us (4.8 TB/s)
 #pragma once
 
 #include "device_common.hpp"
@@ -40,6 +40,7 @@ constexpr int kW4Waves = 8;     // per workgroup, at most (4 where k is split le
 // Rings of a workgroup of 8 waves, at most: with a tile's pairs each, two workgroups of 4 fit a CU's 160 KB.
 constexpr int kW4LdsBytes = 156 * 1024;
 constexpr int kW4MaxExperts = 4096;  // their counts take the rings' place in LDS
+constexpr int kW4MaxPairs = 65536;   // every workgroup looks through them
 // Routed form, tiles of up to 4 pairs: a workgroup row per pair; of 16: per expert.
 constexpr bool w4_by_pair(int tx) { return tx < 16; }
 
@@ -239,39 +240,64 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
 //   begins, if any;
 //   tiles of 16: y < experts the first tile of expert y, y = experts the pairs
 //   that are routed nowhere, further rows the experts' further tiles in order
-//   (a.m / 17 at most), which a count of every expert's pairs finds.
+//   (c pairs of an expert make (c - 1) / 16 of them, so (a.m - 1) / 16 at
+//   most), which a count of every expert's pairs finds.
 // So an expert that many tokens chose has a workgroup for each of its tiles,
 // not one that works through them.
 template <int TX>
 struct W4Tile {
   int pair[TX];
-  int counts[kW4Waves];  // of the waves' pairs in a window of blockDim pairs
+  int counts[2][kW4Waves];  // the waves' pairs in a window, of two windows in turn
 };
 
 // Of the pairs p in [from, to) with expert_idx[p] = e, those of rank first ..
 // first + TX - 1 are entered in the tile, where the first found has rank
-// `rank`; returns the rank after the last.
-template <int TX>
+// `rank`; returns the rank after the last.  A window is LOOK consecutive
+// pairs a thread.
+template <int TX, int LOOK>
 __device__ __forceinline__ int w4_find_pairs(const W4Args& a, int e, int from, int to, int rank, int first,
                                              W4Tile<TX>& tile) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), waves = blockDim.x >> 6;
-  for (int win = from; win < to && rank < first + TX; win += blockDim.x) {
-    const bool found = win + tid < to && a.expert_idx[win + tid] == e;
-    const uint64_t mask = __ballot(found);
-    if (lane == 0) tile.counts[wave] = __popcll(mask);
+  int turn = 0;
+  for (int win = from; win < to && rank < first + TX; win += int(blockDim.x) * LOOK, turn ^= 1) {
+    const int p0 = win + tid * LOOK;
+    int v[LOOK];
+    bool found[LOOK];
+    int before = 0, all = 0;  // the wave's pairs in lanes below this one, and all of them
+#pragma unroll
+    for (int i = 0; i < LOOK; ++i) v[i] = a.expert_idx[min(p0 + i, to - 1)];
+#pragma unroll
+    for (int i = 0; i < LOOK; ++i) {
+      found[i] = v[i] == e && p0 + i < to;
+      const uint64_t mask = __ballot(found[i]);
+      before += __popcll(mask & ((uint64_t(1) << lane) - 1));
+      all += __popcll(mask);
+    }
+    if (lane == 0) tile.counts[turn][wave] = all;
     lds_barrier();
-    int mine = rank;
+    int mine = rank + before;
     for (int w = 0; w < waves; ++w) {
-      const int c = tile.counts[w];
+      const int c = tile.counts[turn][w];
       mine += w < wave ? c : 0;
       rank += c;
     }
     rank = uniform(rank);
-    mine += __popcll(mask & ((uint64_t(1) << lane) - 1));
-    if (found && mine >= first && mine < first + TX) tile.pair[mine - first] = win + tid;
-    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < LOOK; ++i) {
+      if (found[i] && mine >= first && mine < first + TX) tile.pair[mine - first] = p0 + i;
+      mine += found[i];
+    }
   }
+  lds_barrier();
   return rank;
+}
+
+// One pair a thread where that is all of them (512 pairs, 40 experts of 4096 x 512: 30.7 us, 32.1 with four), else four.
+template <int TX>
+__device__ __forceinline__ int w4_find_pairs(const W4Args& a, int e, int from, int to, int rank, int first,
+                                             W4Tile<TX>& tile) {
+  return to - from <= int(blockDim.x) ? w4_find_pairs<TX, 1>(a, e, from, to, rank, first, tile)
+                                      : w4_find_pairs<TX, 4>(a, e, from, to, rank, first, tile);
 }
 
 // The j-th of the experts' tiles after their first ones: its expert (-1: there are fewer) and the rank it starts at.

@@ -42,7 +42,7 @@ int64_t routed_tiles(const W4Args& a) { return std::max(a.experts, a.m / 16); }
 template <int FMT, bool Z, int G, int TX, int R, int U, bool ROUTED>
 int launch_kernel(W4Args a, hipStream_t s) {
   // Grid rows, and how many of them have a tile as a rule.
-  const int64_t slots = !ROUTED ? cdiv64(a.m, TX) : w4_by_pair(TX) ? a.m : int64_t(a.experts) + 1 + a.m / (TX + 1);
+  const int64_t slots = !ROUTED ? cdiv64(a.m, TX) : w4_by_pair(TX) ? a.m : int64_t(a.experts) + 1 + (a.m - 1) / TX;
   const int64_t tiles = ROUTED && !w4_by_pair(TX) ? routed_tiles(a) : slots;
   if (slots > 65535) return FP8G_EUNSUPPORTED;
   const int64_t sets = cdiv64(a.n, 16 * R) * tiles, blocks = cdiv64(a.k, 128 * U);
@@ -71,7 +71,7 @@ int launch_kernel(W4Args a, hipStream_t s) {
 
 template <int FMT, bool Z, int G, bool ROUTED>
 int launch_tiles(const W4Args& a, hipStream_t s) {
-  if (ROUTED && a.experts > kW4MaxExperts) return FP8G_EUNSUPPORTED;
+  if (ROUTED && (a.experts > kW4MaxExperts || a.m > kW4MaxPairs)) return FP8G_EUNSUPPORTED;
   // 128-column steps of a block: two hide more of a wave's latency (one token, 4096 x 7168: 6.4 us, 6.7 with one; with
   // groups of 32 6.3 and 6.8; 8 experts of 4096 x 2048: 11.5 and 13.2).  For 16 tokens the rings would not fit LDS.
   constexpr int kSteps = 2;

@@ -467,7 +467,8 @@ int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_forma
  *       [0, num_experts)
  * An expert's matrix is read once for up to 16 of its pairs (4 where there are
  * no more pairs than experts, 1 where there are an eighth).  num_experts <=
- * 4096, num_pairs <= 1,000,000 (FP8G_EUNSUPPORTED). */
+ * 4096, num_pairs <= 65536 (FP8G_EUNSUPPORTED; the grouped GEMMs serve
+ * longer batches). */
 int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int32_t* expert_idx, int num_pairs,
                           const uint8_t* w, int w_format, const void* w_scales, int scales_dtype,
                           const uint8_t* w_zeros, int group, void* out, int out_dtype, int num_experts, int n, int k,

@@ -202,8 +202,8 @@ def test_matvec_around_each_split(m, n, k, group, fmt, sdt, with_zeros, odt):
 
 
 @pytest.mark.parametrize("T,topk,E,n,k,per_pair", [
-    (500, 1, 500, 1040, 64, False), (400, 1, 300, 3700, 64, True), (4, 2, 9, 1000, 1056, False), (5, 2, 8, 456, 1152, True),
-    (1, 3, 40, 4096, 640, False), (2, 3, 6, 4097, 640, True)])
+    (500, 1, 500, 1040, 64, False), (400, 1, 300, 3700, 64, True), (4, 2, 9, 1000, 1056, False),
+    (5, 2, 8, 456, 1152, True), (1, 3, 40, 4096, 640, False), (2, 3, 6, 4097, 640, True)])
 @pytest.mark.parametrize("group", [32, 64])
 @pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES[1:3] + TYPES[4:])
 def test_experts_around_each_split(T, topk, E, n, k, per_pair, group, fmt, sdt, with_zeros, odt):
@@ -220,7 +220,8 @@ def test_experts_around_each_split(T, topk, E, n, k, per_pair, group, fmt, sdt, 
 
 
 @pytest.mark.parametrize("T,topk,E,n,k", [
-    (700, 1, 70, 100, 256), (40, 8, 200, 60, 128), (64, 8, 100, 4500, 64), (16, 4, 64, 50, 512)])
+    (700, 1, 70, 100, 256), (40, 8, 200, 60, 128), (9000, 1, 70, 33, 64), (32768, 2, 90, 20, 32),
+    (64, 8, 100, 4500, 64), (16, 4, 64, 50, 512)])
 @pytest.mark.parametrize("hot", [(0,), (69, 3), (63, 64, -1)])
 def test_experts_of_a_few_hot_ones(T, topk, E, n, k, hot):
     """Most pairs with one to three experts: tiles of one expert by the dozen, other experts with one pair or none."""
