@@ -32,6 +32,7 @@ FP8G_GROUP_MAX, FP8G_GROUP_TOP2 = 0, 1
 FP8G_INT4, FP8G_E2M1 = 0, 1
 
 _lib = None
+_direct = None  # loaded with it
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
 
@@ -102,7 +103,7 @@ class Fp8GemmError(RuntimeError):
 
 def lib():
     """Load libfp8gemm.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _direct
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with fp8_block_scaled_04_amd.build.build()")
@@ -111,7 +112,9 @@ def lib():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
-        _lib = handle
+        from . import _direct as direct  # the same library's shortest calls, without ctypes
+        direct.setup(_current_device, _raw_stream)
+        _direct, _lib = direct, handle
     return _lib
 
 
@@ -662,10 +665,11 @@ def fp8_moe_gather_rows(y, dst_row, out, stream=None):
 
 
 # ---- expert routing, the weighted combine, products with 4-bit weights --------------
-# A decoding step makes these calls by the hundred, so their checks read each
-# attribute of a tensor once (about 0.1 us apiece) and compare; only a failed
-# comparison goes on to say what is wrong.  3 us of a call are checks and
-# marshalling, 3 us the launch.
+# A decoding step makes these calls by the hundred, so the usual ones (current
+# stream, everything given) go through _direct: checks, marshalling and launch
+# in compiled code.  It answers None where anything is not as expected, and the
+# checks here then take what is only unusual or say what is wrong.  A call of 4
+# kernel microseconds took 6.5 through these checks and ctypes.
 _FLOAT_TYPES = {torch.float32: FP8G_F32, torch.bfloat16: FP8G_BF16}
 # The current stream's address and the current device without the objects that torch.cuda builds (2.8 and 0.3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -734,6 +738,12 @@ def fp8_moe_route(logits, topk, score_func=FP8G_SOFTMAX, bias=None, expert_group
     """The topk experts of every token: logits [T][E] (float32 or bfloat16,
     rows may be strided) -> (expert_idx [T][topk] int32, weights [T][topk]
     float32), allocated unless given."""
+    if _direct and stream is None and expert_idx is not None:
+        st = _direct.moe_route(logits, topk, score_func, bias, expert_groups, topk_groups, group_score, renormalize,
+                               scale, expert_idx, weights)
+        if st is not None:
+            _check("fp8_moe_route", st)
+            return expert_idx, weights
     dt = _float_type(logits, "logits")
     T, E, ld, dev = _matrix(logits, "logits")
     shape = (T, max(int(topk), 0))
@@ -754,6 +764,11 @@ def fp8_moe_route_backward(logits, expert_idx, grad_weights, grad_logits=None, s
                            renormalize=False, scale=1.0, stream=None):
     """Gradient of the logits [T][E] from that of the weights [T][topk] that
     fp8_moe_route gave for expert_idx (same score_func, renormalize, scale)."""
+    if _direct and stream is None and grad_logits is not None:
+        st = _direct.moe_route_backward(logits, expert_idx, grad_weights, grad_logits, score_func, renormalize, scale)
+        if st is not None:
+            _check("fp8_moe_route_backward", st)
+            return grad_logits
     dt = _float_type(logits, "logits")
     T, E, ld, dev = _matrix(logits, "logits")
     _want_dim(expert_idx, "expert_idx", 2)
@@ -810,6 +825,11 @@ def fp8_moe_combine(y, dst_row, weights, out, stream=None):
     """out[t] = sum over j of weights[t][j] * y[dst_row[t][j]].  y holds rows
     of n bfloat16 (any leading shape); dst_row [T][topk] int32 or None (pair p
     in row p); weights [T][topk] float32 or None (1); out [T][n]."""
+    if _direct and stream is None:
+        st = _direct.moe_combine(y, dst_row, weights, out)
+        if st is not None:
+            _check("fp8_moe_combine", st)
+            return out
     T, topk, n, rows, dev, y_at, d_at, w_at, out_at = _check_combine(y, "y", dst_row, weights, out, "out")
     st = lib().fp8_moe_combine(y_at, rows, n, d_at, w_at, T, topk, out_at, _on(stream, dev))
     _check("fp8_moe_combine", st)
@@ -820,6 +840,11 @@ def fp8_moe_combine_backward(grad_out, y, dst_row, weights, grad_y, grad_weights
     """Gradients of fp8_moe_combine into grad_y (the shape of y; rows no pair
     names are left as they are) and grad_weights [T][topk] (None: not
     computed, and y may be None)."""
+    if _direct and stream is None:
+        st = _direct.moe_combine_backward(grad_out, y, dst_row, weights, grad_y, grad_weights)
+        if st is not None:
+            _check("fp8_moe_combine_backward", st)
+            return grad_y, grad_weights
     T, topk, n, rows, dev, gy_at, d_at, w_at, go_at = _check_combine(grad_y, "grad_y", dst_row, weights, grad_out,
                                                                      "grad_out")
     y_at = gw_at = None
@@ -859,6 +884,11 @@ def fp8_w4_matvec(x, w, scales, out, w_format=FP8G_INT4, zeros=None, stream=None
     """out [m][n] (bfloat16 or float32) = x [m][k] (bfloat16, rows may be
     strided) times the transpose of the 4-bit matrix w [n][k / 2] with scales
     [n][k / group] (float32 or bfloat16) and zero points (uint8, INT4 only)."""
+    if _direct and stream is None:
+        st = _direct.w4_matvec(x, w, scales, out, w_format, zeros)
+        if st is not None:
+            _check("fp8_w4_matvec", st)
+            return out
     m, k, ld, dev = _matrix(x, "x")
     n, group, sd, od, w_at, s_at, z_at, out_at = _check_w4(x, k, dev, w, scales, zeros, out, (), m)
     st = lib().fp8_w4_matvec(x.data_ptr(), ld, w_at, w_format, s_at, sd, z_at, group, out_at, od, m, n, k,
@@ -871,6 +901,11 @@ def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zer
     """out [P][n]: row p = x row p // (P // x rows) times the matrix of expert
     expert_idx.view(-1)[p] of w [E][n][k / 2] (scales, zeros [E][n][k /
     group]); zeros where that is no expert."""
+    if _direct and stream is None:
+        st = _direct.w4_matvec_experts(x, expert_idx, w, scales, out, w_format, zeros)
+        if st is not None:
+            _check("fp8_w4_matvec_experts", st)
+            return out
     rows, k, ld, dev = _matrix(x, "x")
     P = expert_idx.numel()
     if P and (rows == 0 or P % rows):

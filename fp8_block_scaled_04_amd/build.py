@@ -1,13 +1,16 @@
-"""Build libfp8gemm.so (the gfx950 kernels and their C ABI) with hipcc.
+"""Build libfp8gemm.so (the gfx950 kernels and their C ABI) with hipcc, and
+_direct.so (Python's way to its shortest calls) with the host compiler.
 
 The library is built in-tree, next to this file, so it travels with the
 source tree.  Nothing here is needed at run time except the built library.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8gemm.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fp8gemm.hip", "moe.hip", "moe_ops.hip", "w4.hip", "jit.hip")]
 DENSE_SOURCE = os.path.join(CSRC, "dense_launch.hip")  # compiled once per operand-format pair
+DIRECT = os.path.join(HERE, "_direct.so")
+DIRECT_SOURCE = os.path.join(CSRC, "direct.cpp")
 W4_SOURCE = os.path.join(CSRC, "w4_launch.hip")  # compiled once per kind of 4-bit matrix
 
 # Device code generation; the runtime specialisation compiles with the same.
@@ -77,6 +82,17 @@ def _compile_jobs(gen: str, objdir: str):
     return jobs
 
 
+def _direct_command(out: str) -> list:
+    """The host compiler's command for _direct.so (against the installed torch and the built library)."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+            "-I", os.path.join(torch_dir, "include"),
+            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], DIRECT_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-L", HERE, f"-l:{os.path.basename(LIB)}",
+            "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     with tempfile.TemporaryDirectory() as gen:
@@ -99,6 +115,11 @@ def build(verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("hipcc link failed:\n" + res.stderr)
     os.replace(tmp, LIB)
+    tmp = DIRECT + ".tmp"
+    res = subprocess.run(_direct_command(tmp), capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building {os.path.basename(DIRECT)} failed:\n" + res.stderr)
+    os.replace(tmp, DIRECT)
     return LIB
 
 
