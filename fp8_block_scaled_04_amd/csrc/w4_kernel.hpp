@@ -147,9 +147,12 @@ __device__ __forceinline__ constexpr int w4_swap(int row) {
 }
 
 // The token in a lane's operand row (its `col`).  Up to four tokens stand in
-// the rows 0, 4, 8, 12, so that result register 0 is all a lane has to scale.
+// the rows 0, 4, 8, 12, so that result register 0 is all a lane has to scale;
+// eight in the rows 0, 1, 4, 5, ..., so that it is 0 and 1.
 template <int TX>
-__device__ __forceinline__ int w4_token(int col) { return TX == 16 ? col : TX == 4 ? col >> 2 : 0; }
+__device__ __forceinline__ int w4_token(int col) {
+  return TX == 16 ? col : TX == 8 ? (col >> 2) * 2 + (col & 1) : TX == 4 ? col >> 2 : 0;
+}
 
 // A block: U steps of 128 columns by 16 R rows of the matrix and TX tokens,
 // as a lane (operand row `col`, columns' `quarter`) holds it.  Groups of 128
@@ -159,7 +162,7 @@ __device__ __forceinline__ int w4_token(int col) { return TX == 16 ? col : TX ==
 template <int FMT, bool Z, int G, int TX, int R, int U>
 struct W4Block {
   static constexpr int Q = 128 / G, F = U * Q, JG = 4 / Q;  // groups per step and block; instructions per group
-  static constexpr int A = TX == 16 ? 4 : 1;                // result registers in use
+  static constexpr int A = TX == 16 ? 4 : TX == 8 ? 2 : 1;  // result registers in use: tokens A * quarter ..
   using Scales = W4Scales<R, F>;
   v4i q[U][R], x[U][4];
   Scales s, z;
@@ -292,7 +295,8 @@ __device__ __forceinline__ int w4_find_pairs(const W4Args& a, int e, int from, i
   return rank;
 }
 
-// One pair a thread where that is all of them (512 pairs, 40 experts of 4096 x 512: 30.7 us, 32.1 with four), else four.
+// One pair a thread where that is all of them (512 pairs, 40 experts of 4096 x 512: 30.7 us, 32.1 with four), else
+// four.
 template <int TX>
 __device__ __forceinline__ int w4_find_pairs(const W4Args& a, int e, int from, int to, int rank, int first,
                                              W4Tile<TX>& tile) {
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
   using Block = W4Block<FMT, Z, G, TX, R, U>;
   using Scales = typename Block::Scales;
   constexpr int F = Block::F, A = Block::A, NB = L::kBlocks, kPieces = 4 * U, kUnits = 16 * U;
-  constexpr int kRows = 16 * R, kRedLd = TX == 16 ? 20 : TX;
+  constexpr int kRows = 16 * R, kRedLd = TX == 16 ? 20 : TX == 8 ? 10 : TX;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), waves = blockDim.x >> 6;
   const int quarter = lane >> 4, col = lane & 15;
@@ -549,6 +553,8 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     float* p = red + (wave * kRows + r * 16 + col) * kRedLd;
     if constexpr (TX == 16)
       *reinterpret_cast<v4f*>(p + quarter * 4) = v4f{acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+    else if constexpr (TX == 8)
+      *reinterpret_cast<v2f*>(p + quarter * 2) = v2f{acc[r][0], acc[r][1]};
     else if (quarter < TX) p[quarter] = acc[r][0];
   }
   lds_barrier();
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
         const int row = set * kRows + r * 16 + col;
 #pragma unroll
         for (int v = 0; v < A; ++v) {
-          const int t = TX == 16 ? quarter * 4 + v : quarter;
+          const int t = quarter * A + v;
           if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, acc[r][v]);
           acc[r][v] = 0.f;
         }

@@ -46,17 +46,19 @@ int launch_kernel(W4Args a, hipStream_t s) {
   const int64_t tiles = ROUTED && !w4_by_pair(TX) ? routed_tiles(a) : slots;
   if (slots > 65535) return FP8G_EUNSUPPORTED;
   const int64_t sets = cdiv64(a.n, 16 * R) * tiles, blocks = cdiv64(a.k, 128 * U);
-  // Rows for every place of the CUs, and a tile's activations fit LDS: whole rows per wave.
-  const int64_t x_bytes = (blocks * (256 * U) + 1023) / 1024 * 1024 * TX;
-  if (sets >= kStreamSets && x_bytes <= kStreamBytes) {
-    using L = W4StreamRing<Z, G, R, U>;
-    const int64_t row_sets = cdiv64(a.n, 16 * R);
-    a.reps = int(std::max<int64_t>(1, sets / (kW4Waves * kStreamWorkgroups)));
-    const int lds = kW4Waves * L::kWave + int(x_bytes);
-    hipLaunchKernelGGL((w4_stream_kernel<FMT, Z, G, TX, R, U, ROUTED>),
-                       dim3(unsigned(cdiv64(row_sets, kW4Waves * a.reps)), unsigned(slots)),
-                       dim3(kW4Waves * kWave), lds, s, a);
-    return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH;
+  if constexpr (TX < 8 || R > 1) {  // the others are for few row sets
+    // Rows for every place of the CUs, and a tile's activations fit LDS: whole rows per wave.
+    const int64_t x_bytes = (blocks * (256 * U) + 1023) / 1024 * 1024 * TX;
+    if (sets >= kStreamSets && x_bytes <= kStreamBytes) {
+      using L = W4StreamRing<Z, G, R, U>;
+      const int64_t row_sets = cdiv64(a.n, 16 * R);
+      a.reps = int(std::max<int64_t>(1, sets / (kW4Waves * kStreamWorkgroups)));
+      const int lds = kW4Waves * L::kWave + int(x_bytes);
+      hipLaunchKernelGGL((w4_stream_kernel<FMT, Z, G, TX, R, U, ROUTED>),
+                         dim3(unsigned(cdiv64(row_sets, kW4Waves * a.reps)), unsigned(slots)),
+                         dim3(kW4Waves * kWave), lds, s, a);
+      return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH;
+    }
   }
   int lks = sets <= kSplit8 ? 3 : sets <= kSplit4 ? 2 : sets < kStreamSets ? 1 : 0;
   while ((1 << lks) > std::max<int64_t>(1, blocks)) --lks;
@@ -76,15 +78,22 @@ int launch_tiles(const W4Args& a, hipStream_t s) {
   // groups of 32 6.3 and 6.8; 8 experts of 4096 x 2048: 11.5 and 13.2).  For 16 tokens the rings would not fit LDS.
   constexpr int kSteps = 2;
   // Tokens a tile.  One, with more than one per expert unlikely (one token, 65536 x 1024: 9.1 us, 9.5 by tiles of 4;
-  // 8 experts of 4096 x 2048: 11.5 and 12.0).  Four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64 pairs with
-  // 64 experts of 4096 x 2048: 53.7 and 60.9).  Else 16: a second tile decodes the matrix again (128 experts with 4
-  // tokens each on average 451 us by tiles of 4, 293 by tiles of 16).
+  // 8 experts of 4096 x 2048: 11.5 and 12.0).  Up to 4: four (4 tokens, 4096 x 7168: 6.5 us, 8.6 by tiles of 16; 64
+  // pairs with 64 experts of 4096 x 2048: 53.7 and 60.9).  Else 16 of 32 rows: a second tile decodes the matrix again
+  // (16 tokens, 4096 x 7168: 7.9 us, 13.5 by tiles of 4; 128 experts with 4 tokens each on average 293, 451 by 4).
   if (ROUTED ? a.m <= a.experts / 8 : a.m == 1) return launch_kernel<FMT, Z, G, 1, 1, kSteps, ROUTED>(a, s);
   if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, kSteps, ROUTED>(a, s);
-  // 16 rows a wave as long as one workgroup each takes them all (16 tokens, 4096 x 7168: 7.9 us, 9.5 with 32 rows),
-  // 32 from there on (16 tokens, 4608 x 7168: 9.6 us, 12.9 with 16; 7168 x 16384: 18.2, 25.8 with 16).
-  const int64_t sets = cdiv64(a.n, 16) * (ROUTED ? routed_tiles(a) : cdiv64(a.m, 16));
-  if (sets <= kSplit8) return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
+  // But the smallest tiles and 16 rows as long as one workgroup for each takes them all; then a wave's chain is what
+  // counts.  By 4, 8 and 16 tokens: 16 tokens, 1024 x 7168: 5.5, -, 6.5; 5 tokens, 2111 x 7168: 9.0, 5.8, 6.6; 8
+  // tokens, 4096 x 7168: 9.0, 6.9, 7.2; beyond, 8 tokens, 4608 x 7168: -, 9.8, 8.9 (of 32 rows, 12.9 of 16); 16
+  // tokens, 4096 x 7168: 7.9 of 16 rows, 9.5 of 32; 7168 x 16384: 25.8 of 16, 18.2 of 32.
+  const int64_t row_sets = cdiv64(a.n, 16);
+  if constexpr (!ROUTED) {
+    if (row_sets * cdiv64(a.m, 4) <= kSplit8) return launch_kernel<FMT, Z, G, 4, 1, kSteps, false>(a, s);
+    if (row_sets * cdiv64(a.m, 8) <= kSplit8) return launch_kernel<FMT, Z, G, 8, 1, kSteps, false>(a, s);
+  }
+  if (row_sets * (ROUTED ? routed_tiles(a) : cdiv64(a.m, 16)) <= kSplit8)
+    return launch_kernel<FMT, Z, G, 16, 1, 1, ROUTED>(a, s);
   return launch_kernel<FMT, Z, G, 16, 2, 1, ROUTED>(a, s);
 }
 

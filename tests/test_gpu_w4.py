@@ -184,6 +184,8 @@ def test_experts_of_many_rows(T, topk, E, n, k, per_pair, group, fmt, sdt, with_
 @pytest.mark.parametrize("m,n,k", [
     (1, 4096, 1152), (4, 4097, 1152), (1, 12288, 1056), (3, 12289, 1152), (1, 24560, 1056), (2, 24561, 1152),
     (16, 4096, 1152), (9, 4097, 1152), (17, 2048, 2176), (33, 1400, 2176), (16, 8192, 1056), (7, 8193, 1152),
+    (5, 2111, 1056), (8, 4096, 1152),
+    (8, 4097, 1152), (16, 2048, 1056), (7, 3000, 640), (30, 1000, 2176), (6, 2049, 384), (11, 2033, 160),
     (16, 24576, 640), (8, 24577, 640), (12, 49120, 320), (16, 49121, 320), (1, 560000, 64), (16, 1050000, 32)])
 @pytest.mark.parametrize("group", [32, 128])
 @pytest.mark.parametrize("fmt,sdt,with_zeros,odt", TYPES[1:3] + TYPES[4:])
