@@ -23,10 +23,10 @@
 // four consecutive lanes read 64 bytes, 64 cycles when every lane reads a row
 // of its own, as the operand layout has it; so rows are copied by four or
 // eight lanes and turned in LDS.
-//   one token       4096 x 7168 INT4, groups of 128       6.6 us (2.3 TB/s; an empty launch takes 1.7)
-//   5 tokens        2111 x 7168 E2M1, groups of 32        7.1 us (1.2 TB/s)
-//   16 tokens       7168 x 16384 INT4 with zero points   20.3 us (3.2 TB/s)
-//   8 experts       4096 x 2048, one token               10.9 us (3.4 TB/s)
+//   one token       4096 x 7168 INT4, groups of 128       6.3 us (2.4 TB/s; an empty launch takes 1.7)
+//   5 tokens        2111 x 7168 E2M1, groups of 32        6.2 us (1.4 TB/s)
+//   16 tokens       7168 x 16384 INT4 with zero points   20.1 us (3.2 TB/s)
+//   8 experts       4096 x 2048, one token               11.1 us (3.3 TB/s)
 //   128 experts     7168 x 2048, 64 tokens, 8 each        206 us (4.8 TB/s)
 #pragma once
 
