@@ -38,7 +38,8 @@ def unpack_int4(codes, scales, zeros):
 
 
 def difference(got, want):
-    return float((got.float() - want.float()).norm() / want.float().norm())
+    got, want = got.detach().float(), want.detach().float()
+    return float((got - want).norm() / want.norm())
 
 
 def decode(x, router, bias, up, down, topk):

@@ -85,8 +85,8 @@ int launch_tiles(const W4Args& a, hipStream_t s) {
   if (ROUTED ? a.m <= a.experts : a.m <= 4) return launch_kernel<FMT, Z, G, 4, 1, kSteps, ROUTED>(a, s);
   // But the smallest tiles and 16 rows as long as one workgroup for each takes them all; then a wave's chain is what
   // counts.  By 4, 8 and 16 tokens: 16 tokens, 1024 x 7168: 5.5, -, 6.5; 5 tokens, 2111 x 7168: 9.0, 5.8, 6.6; 8
-  // tokens, 4096 x 7168: 9.0, 6.9, 7.2; beyond, 8 tokens, 4608 x 7168: -, 9.8, 8.9 (of 32 rows, 12.9 of 16); 16
-  // tokens, 4096 x 7168: 7.9 of 16 rows, 9.5 of 32; 7168 x 16384: 25.8 of 16, 18.2 of 32.
+  // tokens, 4096 x 7168: 9.0, 6.9, 7.2; beyond, 8 tokens, 4608 x 7168: -, 9.8, 8.9.  16 tokens by 16 and 32 rows:
+  // 4096 x 7168 7.9 and 9.5; 4608 x 7168 11.1 and 9.6; 7168 x 16384 21.1 and 18.1.
   const int64_t row_sets = cdiv64(a.n, 16);
   if constexpr (!ROUTED) {
     if (row_sets * cdiv64(a.m, 4) <= kSplit8) return launch_kernel<FMT, Z, G, 4, 1, kSteps, false>(a, s);
