@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
       m2 = fmaxf(fminf(m1, p1), fmaxf(m2, p2));
       m1 = fmaxf(m1, p1);
     });
-    const float score = r.group_score == kGroupTop2 && m2 > kNotAble ? fmaxf(m1 + m2, kLeastAble) : m1;
+    // Halves: of two masked experts (biases of FP32's lowest value) the sum itself would pass the range, and so be no
+    // lower than that of one.
+    const float score = r.group_score == kGroupTop2 && m1 > kNotAble ? 0.5f * m1 + (m2 > kNotAble ? 0.5f * m2 : 0.f) : m1;
     int better = 0;  // groups before this one
     const int first = (threadIdx.x & (kWave - 1)) & ~((1 << n) - 1);
     for (int g = 0; g < r.groups; ++g) {
