@@ -86,8 +86,10 @@ __device__ __forceinline__ double key_min(double a, double b) {
   asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
   return r;
 }
-// Experts that are not to be picked have the lowest score there is; any other is kept above it.
-constexpr float kNotAble = -kMaxFinite, kLeastAble = -3.4e38f;
+// Experts that are not to be picked have the lowest score there is; any other is kept above it, by one step of FP32 (so
+// that biases in the last thousandth of the range keep their order).  Logits that stand for a score above 0 are kept
+// above that again.
+constexpr float kNotAble = -kMaxFinite, kLeastAble = -0x1.fffffcp127f, kLeastLogit = -0x1.fffffap127f;
 // rest = kRouteMaxExperts - 1 - expert; a score is no negative zero (it is a sum with a positive one, if of zeros).
 __device__ __forceinline__ double make_key(float score, unsigned rest) {
   u32x2 k = __builtin_bit_cast(u32x2, double(score));
@@ -97,7 +99,7 @@ __device__ __forceinline__ double make_key(float score, unsigned rest) {
 __device__ __forceinline__ int key_expert(double key) {
   const u32x2 k = __builtin_bit_cast(u32x2, key);
   const int i = int(k.x & unsigned(kRouteMaxExperts - 1));
-  return key < double(kLeastAble) * 1.00001 ? -1 : int(k.y) < 0 ? i : kRouteMaxExperts - 1 - i;
+  return key <= double(kNotAble) ? -1 : int(k.y) < 0 ? i : kRouteMaxExperts - 1 - i;
 }
 
 // The partner's value at level 0 .. 5 of an exchange in which after level n
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
   float sel[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float s = by_logit  ? (below(l[i], top) >= -104.f ? l[i] : kLeastAble)
+    const float s = by_logit  ? (below(l[i], top) >= -104.f ? fmaxf(l[i], kLeastLogit) : kLeastAble)
                     : softmax ? exp_below(l[i], top) * inv_sum
                               : sigmoid_rank(l[i]);
     sel[i] = l[i] > kNegInf && b[i] > kNegInf ? __builtin_amdgcn_fmed3f(s + b[i], kLeastAble, kMaxFinite) : kNotAble;

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from _gpu import require_gpu
+from _gpu import dev, require_gpu
 from test_gpu_moe_ops import check_route, spread_logits
 
 pytestmark = pytest.mark.gpu
@@ -29,3 +29,24 @@ def test_group_sums_of_masked_biases(E, groups, sigmoid, dtype):
     got, _ = check_route(t, l, 2, sigmoid, bias, groups, 1, True, False, 1.0)
     assert np.all(got // size == live - 1)
     check_route(t, l, 3, sigmoid, bias, groups, 2, True, True, 1.0)
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+def test_values_next_to_the_lowest(groups):
+    """Logits and biases between FP32's lowest value and a thousandth above it keep their order."""
+    require_gpu()
+    E = 32
+    l = np.full((3, E), LOWEST)
+    l[0, 21] = -3.401e38
+    l[1, [5, 30]] = -3.4012e38, -3.4011e38
+    l[2, 9] = np.nextafter(LOWEST, np.float32(0))
+    for renormalize in (False, True):
+        got, w = check_route(dev(l), l, 1, False, None, groups, 1, False, renormalize, 1.0, True)
+        assert got[:, 0].tolist() == [21, 30, 9] and np.all(w == 1)
+    rng = np.random.default_rng(1)
+    t, x = spread_logits(rng, 4, E, "f32")
+    bias = np.full(E, np.float32(-3.402e38))
+    bias[[11, 23]] = -3.4011e38, -3.401e38
+    for sigmoid in (False, True):
+        got, _ = check_route(t, x, 2, sigmoid, bias, groups, min(2, groups), False, False, 1.0)
+        assert np.all(got == [23, 11])
