@@ -33,6 +33,7 @@ constexpr int kScoreSoftmax = 0, kScoreSigmoid = 1;
 constexpr int kGroupMax = 0, kGroupTop2 = 1;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kMaxFinite = 3.402823466e38f;
+constexpr float kSigmoidOne = 17.328679f;  // 25 ln 2: the sigmoid of more rounds to 1
 
 struct RouteShape {
   int T, E, groups, topk_groups, topk;
@@ -48,25 +49,27 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = uint16_
 // l - m, 0 where both are the same infinity.
 __device__ __forceinline__ float below(float l, float m) { return l == m ? 0.f : l - m; }
 
-// exp(x) for -104 <= x <= 88 (0 from the bottom of the range on): exp2 of the product with log2(e), whose rounding
-// error is put back (without that, |x| * 2^-24 of relative error).
+// exp(x) for -104 <= x <= 88 (0 from the bottom of the range on): exp2 of t, the rounded product of x with log2(e), and
+// r, what t lacks of the exact product (by a fused multiply-add, and log2(e) in two parts), put back to first order:
+// exp2(t + r) = exp2(t) (1 + r ln 2).  Without r, |x| * 2^-24 of relative error.
 __device__ __forceinline__ float exp_near(float x) {
   const float t = x * 1.44269502f;
   const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * 0.693147181f, e);
 }
-// 1 / d, one Newton step after the 1-ulp estimate.
+// 1 / d, one step of Newton's method after the 1-ulp estimate.
 __device__ __forceinline__ float reciprocal(float d) {
   const float r = __builtin_amdgcn_rcpf(d);
   return fmaf(fmaf(-d, r, 1.f), r, r);
 }
-// A sigmoid for ranking: within 3e-7 of it.
-__device__ __forceinline__ float sigmoid_rank(float l) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * -1.44269502f));
-}
 __device__ __forceinline__ float sigmoid_near(float l) {
   return reciprocal(1.f + exp_near(-__builtin_amdgcn_fmed3f(l, -88.f, 88.f)));
+}
+// The same for ranking, without the Newton step: within 2^-21.4 of its value (an ulp each, 2^-23, of the exponential and
+// the reciprocal, half an ulp each of the exponential's correction and of the sum with 1); 0 below 2^-126.
+__device__ __forceinline__ float sigmoid_rank(float l) {
+  return __builtin_amdgcn_rcpf(1.f + exp_near(-__builtin_amdgcn_fmed3f(l, -88.f, 88.f)));
 }
 __device__ __forceinline__ float exp_below(float l, float m) { return exp_near(fmaxf(below(l, m), -104.f)); }
 
@@ -296,9 +299,10 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
     }
   }
 
-  // by the logits themselves where that is the same order (scores of 0 are equal)
+  // by the logits themselves where that is the same order (scores that round to 0 are equal, and so are sigmoids that
+  // round to 1)
   const bool softmax = r.score == kScoreSoftmax;
-  const bool by_logit = softmax && !bias && (r.groups == 1 || r.group_score == kGroupMax);
+  const bool by_logit = !bias && (r.groups == 1 || r.group_score == kGroupMax);
   float top = 0.f, sum = 1.f;
   if (softmax) {
     top = kNegInf;
@@ -317,9 +321,11 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
   float sel[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float s = by_logit  ? (below(l[i], top) >= -104.f ? fmaxf(l[i], kLeastLogit) : kLeastAble)
-                    : softmax ? exp_below(l[i], top) * inv_sum
-                              : sigmoid_rank(l[i]);
+    const float s = softmax ? (!by_logit                      ? exp_below(l[i], top) * inv_sum
+                               : below(l[i], top) >= -104.f ? fmaxf(l[i], kLeastLogit)
+                                                              : kLeastAble)
+                    : by_logit ? __builtin_amdgcn_fmed3f(l[i], -104.f, kSigmoidOne)
+                               : sigmoid_rank(l[i]);
     sel[i] = l[i] > kNegInf && b[i] > kNegInf ? __builtin_amdgcn_fmed3f(s + b[i], kLeastAble, kMaxFinite) : kNotAble;
   }
   if (r.groups > 1) {

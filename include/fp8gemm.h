@@ -388,8 +388,12 @@ enum { FP8G_GROUP_MAX = 0, FP8G_GROUP_TOP2 = 1 };  /* score of a group of expert
  *   expert_idx [num_tokens][topk] int32, best first; -1 (which routes a pair
  *              nowhere) where a token has fewer experts left than topk
  *   weights    [num_tokens][topk] FP32, 0 where expert_idx is -1
- * Scores are FP32: of two selection scores closer than their rounding either
- * may come first.  Limits (FP8G_EUNSUPPORTED): num_experts <= 1024, topk <=
+ * Without a bias (and with no group scored by a sum) experts rank as their
+ * logits do; only scores that round to 0 in FP32, and sigmoids that round to
+ * 1, are equal.  Otherwise the sums are FP32, of scores within 2^-21 of their
+ * exact value (relatively; below 2^-126 they may be 0): of two experts or
+ * groups whose sums are closer than 2^-20 of the scores in them (and 2^-24 of
+ * the biases) either may come first.  Limits (FP8G_EUNSUPPORTED): num_experts <= 1024, topk <=
  * 32, expert_groups <= 64.  FP8G_EINVAL: expert_groups does not divide
  * num_experts, topk exceeds the experts of topk_groups groups. */
 int fp8_moe_route(const void* logits, int logits_dtype, int64_t logits_ld, const float* bias, int num_tokens,
