@@ -236,6 +236,50 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
   else static_cast<uint16_t*>(a.out)[at] = uint16_t(pack_bf16x2(v, 0.f));
 }
 
+// A group's codes are summed before their scale, so the sums of activations of
+// 1e35 or more may pass FP32's range where the product does not (for INT4 both
+// sums may, and their difference is a NaN).  An infinity or a NaN never leaves
+// an FP32 sum again, so such a product shows at the end, and only there: it is
+// formed anew from the definition, in FP64, by the whole wave.  The result is
+// the definition's for every input, infinities among them.
+template <int FMT, bool Z, int G>
+__device__ __forceinline__ float w4_product(const W4Args& a, int64_t w_row, int64_t x_row) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const uint8_t* w = a.w + w_row * (a.k >> 1);
+  const uint16_t* x = a.x + x_row * a.x_ld;
+  double sum = 0.;
+  for (int c = lane * 8; c < a.k; c += kWave * 8) {  // 8 columns, of one group
+    const v4i values = w4_decode<FMT>(*reinterpret_cast<const unsigned*>(w + (c >> 1)));
+    const v4i xs = *reinterpret_cast<const v4i*>(x + c);
+    const int64_t g = w_row * (a.k / G) + c / G;
+    const double scale = a.scales_bf16 ? __uint_as_float(unsigned(static_cast<const uint16_t*>(a.scales)[g]) << 16)
+                                       : static_cast<const float*>(a.scales)[g];
+    double zero = FMT == kW4Int4 ? 8. : 0.;
+    if constexpr (Z) zero = a.zeros[g];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int v = values[i / 2], u = xs[i / 2];
+      sum = fma(double(__int_as_float(i % 2 ? u & 0xffff0000 : u << 16)),
+                (double(__int_as_float(i % 2 ? v & 0xffff0000 : v << 16)) - zero) * scale, sum);
+    }
+  }
+#pragma unroll
+  for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s, kWave);
+  return float(sum);
+}
+
+// v where it is finite, or not `wanted`; else the product of w_row and x_row.  The whole wave has to call it.
+template <int FMT, bool Z, int G>
+__device__ __forceinline__ float w4_in_range(const W4Args& a, float v, bool wanted, int64_t w_row, int64_t x_row) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (uint64_t left = __ballot(wanted && !(fabsf(v) < __builtin_inff())); left; left &= left - 1) {
+    const int src = __ffsll(static_cast<unsigned long long>(left)) - 1;
+    const float u = w4_product<FMT, Z, G>(a, __shfl(w_row, src, kWave), __shfl(x_row, src, kWave));
+    v = lane == src ? u : v;
+  }
+  return v;
+}
+
 // ---- routed form -------------------------------------------------------------
 // A tile is TX pairs of one expert that follow one another, the t-th tile the
 // pairs of rank t * TX .. in the order of their indices.  Grid row y takes
@@ -558,7 +602,9 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     else if (quarter < TX) p[quarter] = acc[r][0];
   }
   lds_barrier();
-  for (int o = tid; o < sets * kRows * TX; o += waves * kWave) {
+  const int outs = sets * kRows * TX;
+  for (int o0 = wave * kWave; o0 < outs; o0 += waves * kWave) {
+    const int o = min(o0 + lane, outs - 1);
     const int rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
     const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
     float v = 0.f;
@@ -567,7 +613,10 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       const float u = p[(j & (ks - 1)) * kRows * kRedLd];
       v += j < ks ? u : 0.f;
     }
-    if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, v);
+    const bool wanted = o == o0 + lane && row < a.n && t < tt;
+    const int64_t pair = wanted ? out_row(t) : 0;
+    v = w4_in_range<FMT, Z, G>(a, v, wanted, int64_t(e) * a.n + row, wanted ? x_row(t) : 0);
+    if (wanted) w4_store(a, pair * a.n + row, v);
   }
 }
 
@@ -704,6 +753,24 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     o.read_x(x_mine + block * (kUnits * 16), quarter, token);
     o.products(acc, unsigned(block) * F, groups, scale_shift);
     if (++block == blocks) {  // the rows are done
+      bool past = false;  // the range: then one value after the other is looked at
+#pragma unroll
+      for (int v = 0; v < A; ++v)
+#pragma unroll
+        for (int r = 0; r < R; ++r) past |= quarter * A + v < tt && !(fabsf(acc[r][v]) < __builtin_inff());
+      if (__builtin_expect(__ballot(past) != 0, 0)) {
+#pragma unroll 1
+        for (int i = 0; i < R * A; ++i) {
+          const int row = set * kRows + i / A * 16 + col, t = quarter * A + i % A;
+          const bool wanted = row < a.n && t < tt;
+          float p = 0.f;
+#pragma unroll
+          for (int j = 0; j < R * A; ++j) p = i == j ? acc[j / A][j % A] : p;
+          p = w4_in_range<FMT, Z, G>(a, p, wanted, int64_t(e) * a.n + row, wanted ? x_row(t) : 0);
+#pragma unroll
+          for (int j = 0; j < R * A; ++j) acc[j / A][j % A] = i == j ? p : acc[j / A][j % A];
+        }
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int row = set * kRows + r * 16 + col;

@@ -454,9 +454,10 @@ enum {
  * 16 (FP8G_EUNSUPPORTED otherwise); any other m and n.  k = 0 gives zeros.
  * x, w, w_scales, w_zeros, out 16-byte aligned.
  * Meant for up to a few tens of rows: every 16 rows decode the matrix anew
- * (the FP8 GEMMs serve longer batches).  The zero point is applied to a
- * group's sums, so with FP8G_INT4 an infinity or a NaN in a row of x makes
- * that row's outputs NaN; other rows do not see it. */
+ * (the FP8 GEMMs serve longer batches).  Scales and zero points are applied
+ * to a group's sums.  An output that is not finite after that (activations of
+ * 1e35 or more, an infinity, a NaN) is formed anew from the definition in
+ * FP64, so it is what the definition gives, at the cost of a slower call. */
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream);
