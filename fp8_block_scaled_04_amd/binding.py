@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import warnings
 
 import torch
 
@@ -32,7 +33,7 @@ FP8G_GROUP_MAX, FP8G_GROUP_TOP2 = 0, 1
 FP8G_INT4, FP8G_E2M1 = 0, 1
 
 _lib = None
-_direct = None  # loaded with it
+_direct = None  # loaded with it; None where it cannot be
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
 
@@ -112,8 +113,13 @@ def lib():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
-        from . import _direct as direct  # the same library's shortest calls, without ctypes
-        direct.setup(_current_device, _raw_stream)
+        try:
+            from . import _direct as direct  # the same library's shortest calls, without ctypes
+            direct.setup(_current_device, _raw_stream)
+        except ImportError as e:  # not built, or against another torch: the same calls are made through ctypes
+            warnings.warn(f"fp8_block_scaled_04_amd._direct cannot be imported ({e}): the routing, combine and 4-bit "
+                          "calls take some 3 us longer on the host; build the library again", RuntimeWarning)
+            direct = None
         _direct, _lib = direct, handle
     return _lib
 

@@ -2,12 +2,14 @@
 _direct.so (Python's way to its shortest calls) with the host compiler.
 
 The library is built in-tree, next to this file, so it travels with the
-source tree.  Nothing here is needed at run time except the built library.
+source tree.  Nothing here is needed at run time except the built library
+(without _direct.so the binding makes the same calls through ctypes).
 """
 from __future__ import annotations
 
 import importlib.util
 import os
+import shlex
 import shutil
 import subprocess
 import sysconfig
@@ -82,10 +84,17 @@ def _compile_jobs(gen: str, objdir: str):
     return jobs
 
 
+def host_cxx() -> list:
+    """The host compiler's command: $CXX, g++, or the ROCm compiler that hipcc runs."""
+    if os.environ.get("CXX"):
+        return shlex.split(os.environ["CXX"])
+    return [shutil.which("g++") or os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin", "clang++")]
+
+
 def _direct_command(out: str) -> list:
     """The host compiler's command for _direct.so (against the installed torch and the built library)."""
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+    return [*host_cxx(), "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
             "-I", os.path.join(torch_dir, "include"),
             "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], DIRECT_SOURCE, "-o", out, "-L", os.path.join(torch_dir, "lib"),
@@ -118,6 +127,8 @@ def build(verbose: bool = False) -> str:
     tmp = DIRECT + ".tmp"
     res = subprocess.run(_direct_command(tmp), capture_output=True, text=True)
     if res.returncode != 0:
+        if os.path.exists(DIRECT):  # of an earlier build, perhaps of other entry points
+            os.remove(DIRECT)
         raise RuntimeError(f"building {os.path.basename(DIRECT)} failed:\n" + res.stderr)
     os.replace(tmp, DIRECT)
     return LIB
