@@ -19,6 +19,8 @@ constexpr int64_t kRouteFullLanes = 2048 * 64;  // two waves on each SIMD of 256
 // 16.3, 4096 of 1024 53.1 against 39.1.
 constexpr int kCombinePairTokens = 256;
 
+constexpr int kCombineMaxColumns = 1 << 30;  // a thread's column is an int, and steps up to 8192 past the row's end
+
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int launched() { return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH; }
@@ -115,7 +117,7 @@ int launch_route_backward(const L* logits, int64_t ld, const int32_t* expert_idx
 
 int check_combine(int rows, int n, const int32_t* dst_row, const float* weights, int num_tokens, int topk) {
   if (rows < 0 || n < 0 || num_tokens < 0 || topk < 1) return FP8G_EINVAL;
-  if (n % 8 != 0) return FP8G_EUNSUPPORTED;
+  if (n % 8 != 0 || n > kCombineMaxColumns) return FP8G_EUNSUPPORTED;
   if ((dst_row && !aligned(dst_row, 4)) || (weights && !aligned(weights, 4))) return FP8G_EINVAL;
   return FP8G_OK;
 }

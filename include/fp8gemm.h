@@ -417,8 +417,8 @@ int fp8_moe_route_backward(const void* logits, int logits_dtype, int64_t logits_
  *   dst_row  [num_tokens][topk] int32 rows of y (a row outside [0, y_rows)
  *            adds nothing and is not read); NULL: pair p sits in row p
  *   weights  [num_tokens][topk] FP32; NULL: 1
- * FP32 sums in the order of j, one rounding.  n % 8 == 0; y and out 16-byte
- * aligned. */
+ * FP32 sums in the order of j, one rounding.  n % 8 == 0 and n <= 2^30
+ * (FP8G_EUNSUPPORTED otherwise); y and out 16-byte aligned. */
 int fp8_moe_combine(const uint16_t* y, int y_rows, int n, const int32_t* dst_row, const float* weights,
                     int num_tokens, int topk, uint16_t* out, void* stream);
 

@@ -81,3 +81,12 @@ def test_w4_refusals(lib):
     assert _call(f, e, group=48) == EUNSUPPORTED
     assert _call(f, e, E=4097) == EUNSUPPORTED and _call(f, e, pairs=65538) == EUNSUPPORTED
     assert _call(f, e, pairs=0, rows=0) == OK
+
+
+def test_combine_refuses_rows_past_its_column_index(lib):
+    """A thread's column is 32 bits, and steps past the end of the row."""
+    a = dict(y=P, rows=1, n=64, dst=None, w=None, T=1, topk=1, out=P, stream=None)
+    g = dict(go=P, y=P, rows=1, n=64, dst=None, w=None, T=1, topk=1, gy=P, gw=P, stream=None)
+    for n in ((1 << 30) + 8, (1 << 31) - 8):
+        assert _call(lib.fp8_moe_combine, a, n=n) == EUNSUPPORTED
+        assert _call(lib.fp8_moe_combine_backward, g, n=n) == EUNSUPPORTED
