@@ -36,12 +36,12 @@ __device__ __forceinline__ int pair_row(const int32_t* dst, int64_t pair, int ro
   return d >= 0 && d < rows ? int(d) : -1;
 }
 
-// Grid: tokens x column blocks of 2048; a thread holds 8 columns.
+// Grid: tokens from `first` on x column blocks of 2048; a thread holds 8 columns.
 __global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __restrict__ y, int rows, int n,
                                                           const int32_t* __restrict__ dst,
                                                           const float* __restrict__ weights, int topk,
-                                                          uint16_t* __restrict__ out) {
-  const int64_t t = blockIdx.x;
+                                                          uint16_t* __restrict__ out, int64_t first) {
+  const int64_t t = first + blockIdx.x;
   const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
   if (c >= n) return;
   float acc[8] = {};
@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t* __rest
   *reinterpret_cast<v4i*>(out + t * n + c) = pack8(acc);
 }
 
-// PAIRS = false: a workgroup per token, which takes its pairs one after the
+// PAIRS = false: a workgroup per token from `first` on, which takes its pairs one after the
 // other (its row of grad_out then comes from the cache after the first).
-// PAIRS = true: a workgroup per pair.  A thread holds up to kBwdChunks pieces
+// PAIRS = true: a workgroup per pair of all tokens.  A thread holds up to kBwdChunks pieces
 // of 8 columns at a time, all loaded before any is used.
 constexpr int kBwdChunks = 4;
 template <bool PAIRS>
@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const uint16_
                                                                    const int32_t* __restrict__ dst,
                                                                    const float* __restrict__ weights, int topk,
                                                                    uint16_t* __restrict__ grad_y,
-                                                                   float* __restrict__ grad_w) {
+                                                                   float* __restrict__ grad_w, int64_t first) {
   __shared__ float part[4];
-  const int64_t t = PAIRS ? int64_t(blockIdx.x) / topk : blockIdx.x;
+  const int64_t t = PAIRS ? int64_t(blockIdx.x) / topk : first + blockIdx.x;
   const int j0 = PAIRS ? int(blockIdx.x - t * topk) : 0, j1 = PAIRS ? j0 + 1 : topk;
   for (int j = j0; j < j1; ++j) {
     const int d = pair_row(dst, t * topk + j, rows);

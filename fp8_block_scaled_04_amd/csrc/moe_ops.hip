@@ -21,6 +21,8 @@ constexpr int kCombinePairTokens = 256;
 
 constexpr int kCombineMaxColumns = 1 << 30;  // a thread's column is an int, and steps up to 8192 past the row's end
 
+constexpr int64_t kMaxBlocks = 0xffffffff / 256;  // of 256 threads in a launch: their number is 32 bits
+
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int launched() { return hipGetLastError() == hipSuccess ? FP8G_OK : FP8G_ELAUNCH; }
@@ -47,7 +49,7 @@ int launch_route(const L* logits, int64_t ld, const float* bias, const fp8g::Rou
   lanes.vector = (r.E / r.groups) % V == 0 && ld * sizeof(L) % piece == 0 && aligned(logits, piece) &&
                  (!bias || aligned(bias, std::min(V * 4, 16)));
   const int64_t grid = cdiv64(int64_t(r.T) << lanes.log2_lanes, 256);
-  if (grid > 0x7fffffff) return FP8G_EUNSUPPORTED;
+  if (grid > kMaxBlocks) return FP8G_EUNSUPPORTED;
   hipLaunchKernelGGL((fp8g::moe_route_kernel<L, V, KL>), dim3(unsigned(grid)), dim3(256), 0, s, logits, ld, bias, r,
                      lanes, expert_idx, weights);
   return launched();
@@ -95,7 +97,7 @@ int launch_route_backward(const L* logits, int64_t ld, const int32_t* expert_idx
                                r.E % V == 0 && ld * sizeof(L) % piece == 0 && grad_ld * sizeof(L) % piece == 0 &&
                                    aligned(logits, piece) && aligned(grad, piece)};
   const int64_t grid = cdiv64(int64_t(r.T) << n, 256);
-  if (grid > 0x7fffffff) return FP8G_EUNSUPPORTED;
+  if (grid > kMaxBlocks) return FP8G_EUNSUPPORTED;
   hipLaunchKernelGGL((fp8g::moe_route_backward_kernel<L, V>), dim3(unsigned(grid)), dim3(256), 0, s, logits, ld,
                      expert_idx, grad_weights, r, lanes, grad, grad_ld);
   return launched();
@@ -172,8 +174,10 @@ int fp8_moe_combine(const uint16_t* y, int y_rows, int n, const int32_t* dst_row
   if (int st = check_combine(y_rows, n, dst_row, weights, num_tokens, topk)) return st;
   if (num_tokens == 0 || n == 0) return FP8G_OK;
   if (!out || !aligned(out, 16) || (y_rows > 0 && !y) || (y && !aligned(y, 16))) return FP8G_EINVAL;
-  hipLaunchKernelGGL(fp8g::moe_combine_kernel, dim3(unsigned(num_tokens), unsigned(cdiv64(n, 2048))), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), y, y_rows, n, dst_row, weights, topk, out);
+  for (int64_t first = 0; first < num_tokens; first += kMaxBlocks)
+    hipLaunchKernelGGL(fp8g::moe_combine_kernel,
+                       dim3(unsigned(std::min(num_tokens - first, kMaxBlocks)), unsigned(cdiv64(n, 2048))), dim3(256),
+                       0, static_cast<hipStream_t>(stream), y, y_rows, n, dst_row, weights, topk, out, first);
   return launched();
 }
 
@@ -189,12 +193,15 @@ int fp8_moe_combine_backward(const uint16_t* grad_out, const uint16_t* y, int y_
   if (n == 0 && !grad_weights) return FP8G_OK;
   const int64_t pairs = int64_t(num_tokens) * topk;
   auto s = static_cast<hipStream_t>(stream);
-  if (num_tokens <= kCombinePairTokens && pairs <= 0x7fffffff)
+  if (num_tokens <= kCombinePairTokens && pairs <= kMaxBlocks) {
     hipLaunchKernelGGL(fp8g::moe_combine_backward_kernel<true>, dim3(unsigned(pairs)), dim3(256), 0, s, grad_out, y,
-                       y_rows, n, dst_row, weights, topk, grad_y, grad_weights);
-  else
-    hipLaunchKernelGGL(fp8g::moe_combine_backward_kernel<false>, dim3(unsigned(num_tokens)), dim3(256), 0, s, grad_out,
-                       y, y_rows, n, dst_row, weights, topk, grad_y, grad_weights);
+                       y_rows, n, dst_row, weights, topk, grad_y, grad_weights, int64_t(0));
+    return launched();
+  }
+  for (int64_t first = 0; first < num_tokens; first += kMaxBlocks)
+    hipLaunchKernelGGL(fp8g::moe_combine_backward_kernel<false>,
+                       dim3(unsigned(std::min(num_tokens - first, kMaxBlocks))), dim3(256), 0, s, grad_out, y, y_rows,
+                       n, dst_row, weights, topk, grad_y, grad_weights, first);
   return launched();
 }
 
