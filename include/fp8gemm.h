@@ -454,7 +454,8 @@ enum {
  * 16 (FP8G_EUNSUPPORTED otherwise); any other m and n.  k = 0 gives zeros.
  * x, w, w_scales, w_zeros, out 16-byte aligned.
  * Meant for up to a few tens of rows: every 16 rows decode the matrix anew
- * (the FP8 GEMMs serve longer batches).  Scales and zero points are applied
+ * (for longer batches the weights have to be had in FP8, for fp8_gemm_nt; the
+ * library does not convert 4-bit codes).  Scales and zero points are applied
  * to a group's FP32 sums.  With FP8G_INT4 that is the difference of sum
  * code * x and zero * sum x: where a group's activations share a sign both
  * are several times their difference, and the rounding goes by terms of
@@ -478,8 +479,7 @@ int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_forma
  *       [0, num_experts)
  * An expert's matrix is read once for up to 16 of its pairs (4 where there are
  * no more pairs than experts, 1 where there are an eighth).  num_experts <=
- * 4096, num_pairs <= 65536 (FP8G_EUNSUPPORTED; the grouped GEMMs serve
- * longer batches). */
+ * 4096, num_pairs <= 65536 (FP8G_EUNSUPPORTED otherwise). */
 int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int32_t* expert_idx, int num_pairs,
                           const uint8_t* w, int w_format, const void* w_scales, int scales_dtype,
                           const uint8_t* w_zeros, int group, void* out, int out_dtype, int num_experts, int n, int k,
