@@ -15,11 +15,12 @@
 // Picks that do not exist (fewer eligible experts than topk) have index -1
 // and weight 0.  All arithmetic is FP32.
 //
-// What bounds it: long batches the vector instructions of ranking (about 220
-// a token of 256 experts; the logits alone would take 7 us at the rate of a
-// large copy), short ones the chain of loads and exchanges.  32768 tokens of
-// 256 experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 15.6 us, 92 with
-// one wave per token that picks one expert at a time; 8 tokens 4.4 us (13.5).
+// What bounds it: long batches the vector instructions of ranking (239 a token
+// of 256 experts; the logits alone would take 7 us at the rate of a large
+// copy), short ones the chain of loads and exchanges.  32768 tokens of 256
+// experts (FP32, sigmoid, bias, 4 of 8 groups, top 8) take 15.7 us a call, 92
+// with one wave per token that picks one expert at a time; 8 tokens 4.5 us
+// (13.5).
 #pragma once
 
 #include "device_common.hpp"
@@ -442,9 +443,10 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const L* __restrict__ lo
 //
 // 2^log2_lanes (at least topk) lanes per token, V consecutive experts per
 // lane; lane j computes v_j, which then goes round the lanes.  Bound by its
-// writes where the batch is long: 16384 tokens of 128 experts (BF16, softmax
-// over all) take 6.1 us, against 3.6 for the bytes at the rate of a large copy
-// and the launch.
+// writes and by the compares of every pick with every expert where the batch
+// is long: 16384 tokens of 128 experts, 8 picks (BF16) take 6.1 us with a
+// softmax over all, against 3.6 for the bytes at the rate of a large copy and
+// the launch, and 4.9 with a sigmoid, against 2.8.
 template <typename L, int V>
 __global__ void __launch_bounds__(256) moe_route_backward_kernel(const L* __restrict__ logits, int64_t ld,
                                                                  const int32_t* __restrict__ expert_idx,

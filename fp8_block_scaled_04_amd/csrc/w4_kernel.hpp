@@ -12,7 +12,11 @@
 // matrix rows x 32 columns): codes 0..15 and E2M1 values are exact in BF16,
 // and the group's scale and zero point are applied to the FP32 sum,
 //     sum (code - zero) * scale * x = scale * (sum code * x - zero * sum x),
-// with sum x from the same instruction against ones.
+// with sum x from the same instruction against ones.  The difference rounds as
+// its larger sum does: where a group's activations share a sign, as terms of
+// code + zero instead of code - zero (4 x 512 x 7168 against 64 bits: up to 6e-7
+// of the outputs' norm, 1e-7 for random signs; an FP32 product of the decoded
+// matrix 5e-7 to 1e-6).
 //
 // What bounds it: the codes are read once, 0.5 byte a weight, and a CU has to
 // decode what it reads.  A lane's 16 bytes take 36 (INT4) or 16 (E2M1) vector
@@ -23,11 +27,14 @@
 // four consecutive lanes read 64 bytes, 64 cycles when every lane reads a row
 // of its own, as the operand layout has it; so rows are copied by four or
 // eight lanes and turned in LDS.
-//   one token       4096 x 7168 INT4, groups of 128       6.3 us (2.4 TB/s; an empty launch takes 1.7)
-//   5 tokens        2111 x 7168 E2M1, groups of 32        6.2 us (1.4 TB/s)
-//   16 tokens       7168 x 16384 INT4 with zero points   20.1 us (3.2 TB/s)
-//   8 experts       4096 x 2048, one token               11.1 us (3.3 TB/s)
-//   128 experts     7168 x 2048, 64 tokens, 8 each        206 us (4.8 TB/s)
+// Time per call of many issued back to back, three sets of inputs in turn (most
+// of which stay in the last-level cache), and with more sets than that holds:
+//   one token       4096 x 7168 INT4, groups of 128       5.9 us (2.6 TB/s)    6.8
+//   5 tokens        2111 x 7168 E2M1, groups of 32        5.7 us (1.5 TB/s)    7.2
+//   16 tokens       7168 x 16384 INT4 with zero points   19.1 us (3.4 TB/s)   23.6
+//   8 experts       4096 x 2048, one token               10.3 us (3.6 TB/s)   11.3
+//   128 experts     7168 x 2048, 64 tokens, 8 each        207 us (4.8 TB/s)
+// An empty launch takes 1.7.
 #pragma once
 
 #include "device_common.hpp"
@@ -237,7 +244,7 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
 }
 
 // A group's codes are summed before their scale, so the sums of activations of
-// 1e35 or more may pass FP32's range where the product does not (for INT4 both
+// 1e34 or more may pass FP32's range where the product does not (for INT4 both
 // sums may, and their difference is a NaN).  An infinity or a NaN never leaves
 // an FP32 sum again, so such a product shows at the end, and only there: it is
 // formed anew from the definition, in FP64, by the whole wave.  The result is

@@ -11,6 +11,8 @@ namespace fp8g {
 namespace host {
 namespace {
 
+// Figures below: both sides by calls issued back to back, in one run.
+//
 // k is split over the waves of a workgroup, 8 ways up to kSplit8 row sets, 4
 // ways up to kSplit4, else 2 ways.  A workgroup of 8 waves fills a CU's LDS, one
 // of 4 half of it, so kSplit8 workgroups run at once, or twice as many small

@@ -462,7 +462,7 @@ enum {
  * code + zero (4 x 512 x 7168, groups of 128, against 64 bits: 1e-7 of the
  * outputs' norm for activations of random sign, up to 6e-7 for those of one
  * sign, where an FP32 product of the decoded matrix is off by 5e-7 to 1e-6).
- * An output that is not finite after that (activations of 1e35 or more, an
+ * An output that is not finite after that (activations of 1e34 or more, an
  * infinity, a NaN) is formed anew from the definition in FP64, so it is what
  * the definition gives, at the cost of a slower call. */
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
