@@ -247,27 +247,45 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int64_t at, float v) {
 // 1e34 or more may pass FP32's range where the product does not (for INT4 both
 // sums may, and their difference is a NaN).  An infinity or a NaN never leaves
 // an FP32 sum again, so such a product shows at the end, and only there: it is
-// formed anew from the definition, in FP64, by the whole wave.  The result is
-// the definition's for every input, infinities among them.
+// formed anew from the definition, in FP64, by the whole wave, after all of its
+// outputs are stored (the way there then costs one compare an output, and no
+// time that could be measured).  The result is the definition's for every
+// input, infinities among them.  A token with a NaN, as a row of padding may
+// have, has NaN everywhere and is only looked through, once a wave.  16 tokens
+// of 7168 x 16384, 18 us: 21 with a NaN in one token, 26 in all; 250 and 700
+// with an infinity, where every output is formed anew.
+constexpr int kW4Ahead = 4;  // loads of 512 columns in flight
 template <int FMT, bool Z, int G>
 __device__ __forceinline__ float w4_product(const W4Args& a, int64_t w_row, int64_t x_row) {
   const int lane = threadIdx.x & (kWave - 1);
   const uint8_t* w = a.w + w_row * (a.k >> 1);
   const uint16_t* x = a.x + x_row * a.x_ld;
   double sum = 0.;
-  for (int c = lane * 8; c < a.k; c += kWave * 8) {  // 8 columns, of one group
-    const v4i values = w4_decode<FMT>(*reinterpret_cast<const unsigned*>(w + (c >> 1)));
-    const v4i xs = *reinterpret_cast<const v4i*>(x + c);
-    const int64_t g = w_row * (a.k / G) + c / G;
-    const double scale = a.scales_bf16 ? __uint_as_float(unsigned(static_cast<const uint16_t*>(a.scales)[g]) << 16)
-                                       : static_cast<const float*>(a.scales)[g];
-    double zero = FMT == kW4Int4 ? 8. : 0.;
-    if constexpr (Z) zero = a.zeros[g];
+  for (int c0 = lane * 8; c0 < a.k; c0 += kWave * 8 * kW4Ahead) {  // 8 columns, of one group
+    unsigned q[kW4Ahead];
+    v4i xs[kW4Ahead];
+    float scale[kW4Ahead], zero[kW4Ahead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int v = values[i / 2], u = xs[i / 2];
-      sum = fma(double(__int_as_float(i % 2 ? u & 0xffff0000 : u << 16)),
-                (double(__int_as_float(i % 2 ? v & 0xffff0000 : v << 16)) - zero) * scale, sum);
+    for (int u = 0; u < kW4Ahead; ++u) {
+      const int c = min(c0 + u * kWave * 8, a.k - 8);
+      const int64_t g = w_row * (a.k / G) + c / G;
+      q[u] = *reinterpret_cast<const unsigned*>(w + (c >> 1));
+      xs[u] = *reinterpret_cast<const v4i*>(x + c);
+      scale[u] = a.scales_bf16 ? __uint_as_float(unsigned(static_cast<const uint16_t*>(a.scales)[g]) << 16)
+                               : static_cast<const float*>(a.scales)[g];
+      zero[u] = FMT == kW4Int4 ? 8.f : 0.f;
+      if constexpr (Z) zero[u] = a.zeros[g];
+    }
+#pragma unroll
+    for (int u = 0; u < kW4Ahead; ++u) {
+      if (c0 + u * kWave * 8 >= a.k) break;
+      const v4i values = w4_decode<FMT>(q[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int v = values[i / 2], b = xs[u][i / 2];
+        const float value = __int_as_float(i % 2 ? v & 0xffff0000 : v << 16) - zero[u];  // exact
+        sum = fma(double(__int_as_float(i % 2 ? b & 0xffff0000 : b << 16)), double(value) * double(scale[u]), sum);
+      }
     }
   }
 #pragma unroll
@@ -275,16 +293,62 @@ __device__ __forceinline__ float w4_product(const W4Args& a, int64_t w_row, int6
   return float(sum);
 }
 
-// v where it is finite, or not `wanted`; else the product of w_row and x_row.  The whole wave has to call it.
-template <int FMT, bool Z, int G>
-__device__ __forceinline__ float w4_in_range(const W4Args& a, float v, bool wanted, int64_t w_row, int64_t x_row) {
-  const int lane = threadIdx.x & (kWave - 1);
-  for (uint64_t left = __ballot(wanted && !(fabsf(v) < __builtin_inff())); left; left &= left - 1) {
-    const int src = __ffsll(static_cast<unsigned long long>(left)) - 1;
-    const float u = w4_product<FMT, Z, G>(a, __shfl(w_row, src, kWave), __shfl(x_row, src, kWave));
-    v = lane == src ? u : v;
+// Whether a row of x has a NaN.
+__device__ __forceinline__ bool w4_has_nan(const W4Args& a, int64_t x_row) {
+  const uint16_t* x = a.x + x_row * a.x_ld;
+  bool nan = false;
+  for (int c0 = (threadIdx.x & (kWave - 1)) * 8; c0 < a.k; c0 += kWave * 8 * kW4Ahead) {
+    v4i xs[kW4Ahead];  // those past the end are the last ones again
+#pragma unroll
+    for (int u = 0; u < kW4Ahead; ++u) xs[u] = *reinterpret_cast<const v4i*>(x + min(c0 + u * kWave * 8, a.k - 8));
+#pragma unroll
+    for (int u = 0; u < kW4Ahead; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        nan |= (xs[u][i] & 0x7fff) > 0x7f80 || (unsigned(xs[u][i]) >> 16 & 0x7fff) > 0x7f80;
   }
-  return v;
+  return __ballot(nan) != 0;
+}
+
+// Tokens of a tile that the wave has looked through, and those of them that have a NaN.
+struct W4Nans {
+  unsigned looked = 0, found = 0;
+};
+
+__device__ __forceinline__ bool w4_finite(float v) { return fabsf(v) < __builtin_inff(); }
+
+// Looks at stored outputs again, one per lane where `wanted`: at out[at], of w_row and x_row, which is token t of the
+// tile.  The whole wave has to call it, the wave's stores done.  (They are read past the L1 cache, which may hold what
+// was there before.)
+template <int FMT, bool Z, int G>
+__device__ __forceinline__ void w4_mend(const W4Args& a, bool wanted, int64_t at, int64_t w_row, int64_t x_row, int t,
+                                        W4Nans& nans) {
+  const int lane = threadIdx.x & (kWave - 1);
+  float v = 0.f;
+  if (wanted) {
+    if (a.out_f32)
+      v = __hip_atomic_load(static_cast<const float*>(a.out) + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else
+      v = __uint_as_float(unsigned(__hip_atomic_load(static_cast<const uint16_t*>(a.out) + at, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT)) << 16);
+  }
+  const bool past = !w4_finite(v);
+  for (uint64_t left = __ballot(past); left;) {
+    const int src = __ffsll(static_cast<unsigned long long>(left)) - 1;
+    const int64_t row = __shfl(x_row, src, kWave);
+    const int token = uniform(__shfl(t, src, kWave));
+    if (!(nans.looked >> token & 1)) {
+      nans.looked |= 1u << token;
+      nans.found |= unsigned(w4_has_nan(a, row)) << token;
+    }
+    uint64_t done = uint64_t(1) << src;
+    float u = __builtin_nanf("");
+    if (nans.found >> token & 1) done = left & __ballot(t == token);
+    else u = w4_product<FMT, Z, G>(a, __shfl(w_row, src, kWave), row);
+    v = done >> lane & 1 ? u : v;
+    left &= ~done;
+  }
+  if (past) w4_store(a, at, v);
 }
 
 // ---- routed form -------------------------------------------------------------
@@ -609,10 +673,15 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
     else if (quarter < TX) p[quarter] = acc[r][0];
   }
   lds_barrier();
+  bool past = false;  // of this thread's outputs one is not finite
   const int outs = sets * kRows * TX;
-  for (int o0 = wave * kWave; o0 < outs; o0 += waves * kWave) {
-    const int o = min(o0 + lane, outs - 1);
-    const int rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
+  const auto place = [&](int o, int& st, int& rr, int& t, int& row) {
+    rr = o % kRows, t = o / kRows % TX, st = o / (kRows * TX), row = row0 + st * kRows + rr;
+    return row < a.n && t < tt;
+  };
+  for (int o = tid; o < outs; o += waves * kWave) {
+    int st, rr, t, row;
+    const bool wanted = place(o, st, rr, t, row);
     const float* p = red + ((st << lks) * kRows + rr) * kRedLd + t;
     float v = 0.f;
 #pragma unroll
@@ -620,10 +689,18 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_kernel(W4Args a) {
       const float u = p[(j & (ks - 1)) * kRows * kRedLd];
       v += j < ks ? u : 0.f;
     }
-    const bool wanted = o == o0 + lane && row < a.n && t < tt;
-    const int64_t pair = wanted ? out_row(t) : 0;
-    v = w4_in_range<FMT, Z, G>(a, v, wanted, int64_t(e) * a.n + row, wanted ? x_row(t) : 0);
-    if (wanted) w4_store(a, pair * a.n + row, v);
+    if (!wanted) continue;
+    w4_store(a, out_row(t) * a.n + row, v);
+    past |= !w4_finite(v);
+  }
+  if (__builtin_expect(__ballot(past) == 0, 1)) return;
+  copies_left<0>();  // the stores are done
+  W4Nans nans;
+  for (int o0 = wave * kWave; o0 < outs; o0 += waves * kWave) {
+    int st, rr, t, row;
+    const bool wanted = place(min(o0 + lane, outs - 1), st, rr, t, row) && o0 + lane < outs;
+    w4_mend<FMT, Z, G>(a, wanted, wanted ? out_row(t) * a.n + row : 0, int64_t(e) * a.n + row, wanted ? x_row(t) : 0, t,
+                       nans);
   }
 }
 
@@ -742,6 +819,7 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
   const unsigned scale_shift = a.scales_bf16 ? 16 : 0;
   float acc[R][A] = {};
   int block = 0, slot = 0, scale_slot = L::kSlots - 1, set = set0;
+  bool past = false;  // of this lane's outputs one is not finite
   for (int b = 0; b < total; ++b) {
     const int newer = min(total - 1 - b, NB - 1);  // blocks in flight after this one
     if (newer == 2) copies_left<2 * L::kCopies>();
@@ -760,31 +838,16 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
     o.read_x(x_mine + block * (kUnits * 16), quarter, token);
     o.products(acc, unsigned(block) * F, groups, scale_shift);
     if (++block == blocks) {  // the rows are done
-      bool past = false;  // the range: then one value after the other is looked at
-#pragma unroll
-      for (int v = 0; v < A; ++v)
-#pragma unroll
-        for (int r = 0; r < R; ++r) past |= quarter * A + v < tt && !(fabsf(acc[r][v]) < __builtin_inff());
-      if (__builtin_expect(__ballot(past) != 0, 0)) {
-#pragma unroll 1
-        for (int i = 0; i < R * A; ++i) {
-          const int row = set * kRows + i / A * 16 + col, t = quarter * A + i % A;
-          const bool wanted = row < a.n && t < tt;
-          float p = 0.f;
-#pragma unroll
-          for (int j = 0; j < R * A; ++j) p = i == j ? acc[j / A][j % A] : p;
-          p = w4_in_range<FMT, Z, G>(a, p, wanted, int64_t(e) * a.n + row, wanted ? x_row(t) : 0);
-#pragma unroll
-          for (int j = 0; j < R * A; ++j) acc[j / A][j % A] = i == j ? p : acc[j / A][j % A];
-        }
-      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int row = set * kRows + r * 16 + col;
 #pragma unroll
         for (int v = 0; v < A; ++v) {
           const int t = quarter * A + v;
-          if (row < a.n && t < tt) w4_store(a, out_row(t) * a.n + row, acc[r][v]);
+          if (row < a.n && t < tt) {
+            w4_store(a, out_row(t) * a.n + row, acc[r][v]);
+            past |= !w4_finite(acc[r][v]);
+          }
           acc[r][v] = 0.f;
         }
       }
@@ -792,6 +855,17 @@ __global__ void __launch_bounds__(kW4Waves * kWave) w4_stream_kernel(W4Args a) {
       set += kW4Waves;
     }
   }
+  if (__builtin_expect(__ballot(past) == 0, 1)) return;
+  copies_left<0>();  // the stores are done
+  W4Nans nans;
+  for (int st = set0; st < set; st += kW4Waves)
+#pragma unroll 1
+    for (int t0 = 0; t0 < tt; t0 += kWave / kRows) {
+      const int t = min(t0 + lane / kRows, TX - 1), row = st * kRows + lane % kRows;
+      const bool wanted = row < a.n && t0 + lane / kRows < tt;
+      w4_mend<FMT, Z, G>(a, wanted, wanted ? out_row(t) * a.n + row : 0, int64_t(e) * a.n + row, wanted ? x_row(t) : 0,
+                         t, nans);
+    }
 }
 
 }  // namespace fp8g

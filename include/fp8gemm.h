@@ -463,8 +463,9 @@ enum {
  * outputs' norm for activations of random sign, up to 6e-7 for those of one
  * sign, where an FP32 product of the decoded matrix is off by 5e-7 to 1e-6).
  * An output that is not finite after that (activations of 1e34 or more, an
- * infinity, a NaN) is formed anew from the definition in FP64, so it is what
- * the definition gives, at the cost of a slower call. */
+ * infinity) is formed anew from the definition in FP64, so it is what the
+ * definition gives; a call with many of them is slower, some 10 to 40 times
+ * where they are all.  A NaN in a row of x makes that row's outputs NaN. */
 int fp8_w4_matvec(const uint16_t* x, int64_t x_ld, const uint8_t* w, int w_format, const void* w_scales,
                   int scales_dtype, const uint8_t* w_zeros, int group, void* out, int out_dtype, int m, int n, int k,
                   void* stream);

@@ -99,3 +99,33 @@ def test_finite_bound_of_unscaled_sums():
             out = Out((m, n), torch.float32)
             b.fp8_w4_matvec(tx, dev(w), dev(s), out.view)
             assert np.array_equal(out.numpy(), np.full((m, n), 2.0 ** (power - 1), np.float32))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 70, 2080), (3, 33, 1152), (8, 2060, 2560), (13, 50, 384), (20, 4500, 256),
+                                   (4, 25000, 544), (16, 49300, 128)])
+@pytest.mark.parametrize("fmt,sdt,with_zeros,odt", KINDS)
+def test_tokens_of_every_sort_in_a_tile(m, n, k, fmt, sdt, with_zeros, odt):
+    """Ordinary ones, with a NaN at any place, with an infinity, and past the range before their scale."""
+    require_gpu()
+    rng = np.random.default_rng(m * k)
+    tw, w, ts, s, tz, z = matrix(rng, (), n, k, 32, sdt, with_zeros)
+    x = rng.normal(size=(m, k))
+    sort = (np.arange(m) + 1) % 4  # 0 ordinary, 1 NaN, 2 large, 3 infinite
+    x[sort == 2] = (np.abs(x[sort == 2]) + 0.5) * 2e37
+    for i in np.nonzero(sort % 2)[0]:
+        x[i, rng.integers(0, k)] = np.nan if sort[i] == 1 else -np.inf
+    x[sort == 1, -1] = np.nan
+    tx, x = bf16(x)
+    out = Out((m, n), DT[odt], 5)
+    b.fp8_w4_matvec(tx, tw, ts, out.view, FMT[fmt], tz)
+    rows = np.arange(n) if n < 300 else np.unique(rng.integers(0, n, 300))
+    got = out.numpy()[:, rows]
+    v, zero, scale = moe_ops.w4_parts(w[rows], s[rows], None if z is None else z[rows], fmt == "e2m1")
+    with np.errstate(invalid="ignore"):
+        want = np.stack([(t * ((v - zero) * scale)).sum(-1) for t in x.astype(np.float64)])
+    mag = np.abs(np.nan_to_num(x.astype(np.float64), posinf=0, neginf=0)) @ ((np.abs(v) + zero) * scale).T
+    assert np.all(np.isnan(got[sort == 1]))
+    special = ~np.isfinite(want)
+    assert np.array_equal(got[special], want[special], equal_nan=True)
+    fits = np.abs(want) < (3.38e38 if odt == "bf16" else 3.4e38)
+    check(got[fits], want[fits], mag[fits], k, odt)
