@@ -29,11 +29,11 @@
 // eight lanes and turned in LDS.
 // Time per call of many issued back to back, three sets of inputs in turn (most
 // of which stay in the last-level cache), and with more sets than that holds:
-//   one token       4096 x 7168 INT4, groups of 128       5.9 us (2.6 TB/s)    6.8
-//   5 tokens        2111 x 7168 E2M1, groups of 32        5.7 us (1.5 TB/s)    7.2
-//   16 tokens       7168 x 16384 INT4 with zero points   19.1 us (3.4 TB/s)   23.6
-//   8 experts       4096 x 2048, one token               10.3 us (3.6 TB/s)   11.3
-//   128 experts     7168 x 2048, 64 tokens, 8 each        207 us (4.8 TB/s)
+//   one token       4096 x 7168 INT4, groups of 128       5.8 us (2.6 TB/s)    6.4
+//   5 tokens        2111 x 7168 E2M1, groups of 32        5.6 us (1.5 TB/s)    7.1
+//   16 tokens       7168 x 16384 INT4 with zero points   19.0 us (3.4 TB/s)   23.3
+//   8 experts       4096 x 2048, one token               10.1 us (3.6 TB/s)   11.0
+//   128 experts     7168 x 2048, 64 tokens, 8 each        204 us (4.9 TB/s)
 // An empty launch takes 1.7.
 #pragma once
 
