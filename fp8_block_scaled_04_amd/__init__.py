@@ -20,4 +20,8 @@ from .binding import (  # noqa: F401
     FP8G_GROUP_MAX, FP8G_GROUP_TOP2, FP8G_SIGMOID, FP8G_SOFTMAX, fp8_moe_combine, fp8_moe_combine_backward,
     fp8_moe_route, fp8_moe_route_backward,
     FP8G_E2M1, FP8G_INT4, fp8_w4_matvec, fp8_w4_matvec_experts,
+    FP8G_ACT_GELU, FP8G_ACT_GELU_TANH, FP8G_ACT_NONE, FP8G_ACT_RELU, FP8G_ACT_SILU, FP8G_NORM_LAYER, FP8G_NORM_RMS,
+    fp8_epilogue_backward, fp8_epilogue_backward_workspace_bytes, fp8_gemm_nt_epilogue, fp8_moe_few_tokens,
+    fp8_moe_few_tokens_workspace_bytes, fp8_norm_residual, fp8_norm_residual_backward,
+    fp8_norm_residual_backward_workspace_bytes,
 )

@@ -11,6 +11,7 @@ RHS scales ``[NB][KG]`` (``[G][NB][KG]`` grouped) float32; outputs bfloat16.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -31,10 +32,13 @@ FP8G_JIT_DENSE, FP8G_JIT_CONTIGUOUS, FP8G_JIT_MASKED = 0, 1, 2
 FP8G_SOFTMAX, FP8G_SIGMOID = 0, 1
 FP8G_GROUP_MAX, FP8G_GROUP_TOP2 = 0, 1
 FP8G_INT4, FP8G_E2M1 = 0, 1
+FP8G_ACT_NONE, FP8G_ACT_RELU, FP8G_ACT_GELU, FP8G_ACT_GELU_TANH, FP8G_ACT_SILU = range(5)
+FP8G_NORM_RMS, FP8G_NORM_LAYER = 0, 1
 
 _lib = None
 _direct = None  # loaded with it; None where it cannot be
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f32c = ctypes.c_float
 
 
 class Fp8GemmConfig(ctypes.Structure):
@@ -93,6 +97,18 @@ _SIGNATURES = {
     "fp8_w4_matvec": ([_vp, _i64, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp], _i32),
     "fp8_w4_matvec_experts": ([_vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
                                _i32, _vp], _i32),
+    "fp8_gemm_nt_epilogue": ([_vp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
+                              _vp, _sz, _vp], _i32),
+    "fp8_epilogue_backward_workspace_bytes": ([_i32, _i32], _sz),
+    "fp8_epilogue_backward": ([_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "fp8_norm_residual": ([_vp, _i32, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _f32c, _i32, _vp, _vp, _i32, _f32c, _vp,
+                           _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp], _i32),
+    "fp8_norm_residual_backward_workspace_bytes": ([_i32, _i32], _sz),
+    "fp8_norm_residual_backward": ([_vp, _vp, _vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _f32c, _i32, _vp, _vp,
+                                    _i32, _f32c, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "fp8_moe_few_tokens_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "fp8_moe_few_tokens": ([_vp, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp,
+                            _sz, _vp], _i32),
 }
 
 
@@ -922,4 +938,222 @@ def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zer
                                      _tensor(expert_idx, "expert_idx", torch.int32, expert_idx.shape, dev), P, w_at,
                                      w_format, s_at, sd, z_at, group, out_at, od, E, n, k, _on(stream, dev))
     _check("fp8_w4_matvec_experts", st)
+    return out
+
+
+# ---- the feed-forward block around the products ------------------------------------------
+def _ws(workspace, needed, device):
+    """(address, bytes) of a workspace of the given device, allocated where none is given and one is needed."""
+    if workspace is None:
+        if not needed:
+            return None, 0, None
+        workspace = torch.empty(needed, dtype=torch.uint8, device=device)
+    _dev(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the other tensors on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _optional(t, name, dtypes, shape, device):
+    return None if t is None else _tensor(t, name, dtypes, shape, device)
+
+
+def fp8_gemm_nt_epilogue(lhs, lhs_scales, rhs, rhs_scales, out, bias=None, activation=FP8G_ACT_NONE, residual=None,
+                         preact=None, lhs_format=FP8G_E4M3, rhs_format=FP8G_E4M3, workspace=None, stream=None):
+    """out [m][n] = activation(fp8_gemm_nt + bias) + residual, of the FP32
+    sums.  bias [n] float32 or bfloat16; residual [m][n] bfloat16 (may be
+    out); preact [m][n] bfloat16 receives the sums with their bias."""
+    lhs_format, rhs_format = _fmt(lhs_format, "lhs_format"), _fmt(rhs_format, "rhs_format")
+    lhs, rhs = _codes(lhs, "lhs", lhs_format), _codes(rhs, "rhs", rhs_format)
+    lhs_scales, rhs_scales = _f32(lhs_scales, "lhs_scales"), _f32(rhs_scales, "rhs_scales")
+    out = _bf16(out, "out")
+    m, n, k = _check_gemm_nt(lhs, lhs_scales, rhs, rhs_scales, out, workspace)
+    dev = out.get_device()
+    bias_dtype = FP8G_F32 if bias is None else _float_type(bias, "bias")
+    bias_at = _optional(bias, "bias", (torch.float32, torch.bfloat16), (n,), dev)
+    residual_at = _optional(residual, "residual", torch.bfloat16, (m, n), dev)
+    preact_at = _optional(preact, "preact", torch.bfloat16, (m, n), dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().fp8_gemm_nt_epilogue(_p(lhs), lhs_format, _p(lhs_scales), lhs_scales.shape[-1], _p(rhs), rhs_format,
+                                    _p(rhs_scales), bias_at, bias_dtype, activation, residual_at, preact_at, _p(out),
+                                    m, n, k, _p(workspace), ws_bytes, _on(stream, dev))
+    _check("fp8_gemm_nt_epilogue", st)
+    return out
+
+
+def fp8_epilogue_backward_workspace_bytes(m: int, n: int) -> int:
+    return int(lib().fp8_epilogue_backward_workspace_bytes(int(m), int(n)))
+
+
+def fp8_epilogue_backward(grad_out, preact, activation, grad_preact, grad_bias=None, workspace=None, stream=None):
+    """Gradients of fp8_gemm_nt_epilogue's sums (grad_preact [m][n] bfloat16)
+    and of its bias (grad_bias [n] float32, None: not computed) from that of
+    its output; workspace: allocated unless given."""
+    _want_dim(preact, "preact", 2)
+    m, n = preact.shape
+    dev = preact.get_device()
+    p_at = _tensor(preact, "preact", torch.bfloat16, (m, n), None)
+    go_at = _tensor(grad_out, "grad_out", torch.bfloat16, (m, n), dev)
+    gp_at = _tensor(grad_preact, "grad_preact", torch.bfloat16, (m, n), dev)
+    gb_at = _optional(grad_bias, "grad_bias", torch.float32, (n,), dev)
+    s = _on(stream, dev)
+    needed = fp8_epilogue_backward_workspace_bytes(m, n) if grad_bias is not None and workspace is None else 0
+    with _allocating(stream):
+        ws_at, ws_bytes, _keep = _ws(workspace, needed, preact.device)
+    st = lib().fp8_epilogue_backward(go_at, p_at, activation, m, n, gp_at, gb_at, ws_at, ws_bytes, s)
+    _check("fp8_epilogue_backward", st)
+    return grad_preact, grad_bias
+
+
+def _allocating(stream):
+    """Allocations belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _norm_params(x, n, T, dev, post_norm, post_weight, gate, pre_weight):
+    """(param type, addresses of post_weight, gate and pre_weight, gate rows)."""
+    given = [(p, name) for p, name in ((post_weight, "post_weight"), (gate, "gate"), (pre_weight, "pre_weight"))
+             if p is not None]
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    dtype = given[0][0].dtype if given else torch.float32
+    pd = _float_type(given[0][0], given[0][1]) if given else FP8G_F32
+    gate_rows = 1
+    if gate is not None and gate.dim() == 2:
+        gate_rows = gate.shape[0]
+        if gate_rows not in (1, T):
+            raise ValueError(f"gate has {gate_rows} rows, expected 1 or {T}")
+    return (pd, _optional(post_weight, "post_weight", dtype, (n,), dev),
+            _optional(gate, "gate", dtype, (n,) if gate is None or gate.dim() == 1 else (gate_rows, n), dev),
+            _optional(pre_weight, "pre_weight", dtype, (n,), dev), gate_rows)
+
+
+def fp8_norm_residual(x, residual=None, h=None, y=None, q=None, q_scales=None, *, pre_weight=None, post_norm=False,
+                      post_weight=None, gate=None, residual_scale=1.0, kind=FP8G_NORM_RMS, eps=1e-6,
+                      q_format=FP8G_E4M3, stream=None):
+    """The step between two blocks: u = norm(x) * post_weight (or x), h =
+    residual_scale * residual + gate * u, y = norm(h) * pre_weight.  x, y
+    [T][n] float32 or bfloat16; residual, h [T][n] float32 or bfloat16; q
+    [T][n] the FP8 codes of y with q_scales [KG][ld >= T]; gate [n], [1][n] or
+    [T][n]; x and residual rows may be strided.  Outputs not given are not
+    computed.  Returns (h, y, q, q_scales)."""
+    xd = _float_type(x, "x")
+    T, n, x_ld, dev = _matrix(x, "x")
+    stream_t = residual if residual is not None else h
+    sd, r_at, r_ld = FP8G_F32, None, n
+    if stream_t is not None:
+        sd = _float_type(stream_t, "residual" if residual is not None else "h")
+    if residual is not None:
+        rows, cols, r_ld, r_dev = _matrix(residual, "residual")
+        _want(residual, "residual", (T, n))
+        if r_dev != dev:
+            raise ValueError(f"residual is on {residual.device}, x on {x.device}")
+        r_at = residual.data_ptr()
+    h_at = None if h is None else _tensor(h, "h", stream_t.dtype, (T, n), dev)
+    y_at = _optional(y, "y", x.dtype, (T, n), dev)
+    q_at = s_at = None
+    ld = T
+    if q is not None:
+        if q_scales is None:
+            raise ValueError("q needs q_scales")
+        q_codes = _codes(q, "q", _fmt(q_format, "q_format"))
+        _want(q_codes, "q", (T, n))
+        _want_scales_mn(_f32(q_scales, "q_scales"), "q_scales", (_kg(n),), T)
+        _same_device(x=x, q=q_codes, q_scales=q_scales)
+        q_at, s_at, ld = q_codes.data_ptr(), q_scales.data_ptr(), q_scales.shape[-1]
+    pd, post_at, gate_at, pre_at, gate_rows = _norm_params(x, n, T, dev, post_norm, post_weight, gate, pre_weight)
+    st = lib().fp8_norm_residual(x.data_ptr(), xd, x_ld, r_at, r_ld, sd, T, n, kind, eps, bool(post_norm), post_at,
+                                 gate_at, gate_rows, residual_scale, pre_at, pd, h_at, y_at, q_at, q_format, s_at, ld,
+                                 _on(stream, dev))
+    _check("fp8_norm_residual", st)
+    return h, y, q, q_scales
+
+
+def fp8_norm_residual_backward_workspace_bytes(num_rows: int, n: int) -> int:
+    return int(lib().fp8_norm_residual_backward_workspace_bytes(int(num_rows), int(n)))
+
+
+def fp8_norm_residual_backward(grad_h, grad_y, x, h, grad_x=None, grad_residual=None, grad_pre_weight=None,
+                               grad_post_weight=None, grad_gate=None, *, pre_weight=None, post_norm=False,
+                               post_weight=None, gate=None, residual_scale=1.0, kind=FP8G_NORM_RMS, eps=1e-6,
+                               workspace=None, stream=None):
+    """Gradients of fp8_norm_residual from those of h (grad_h, or None) and of y
+    (grad_y, or None); x and h are the forward pass's (x may be None without
+    post_norm and gate, h without grad_y).  Those not given are not computed;
+    the parameters' are float32, grad_gate of the gate's shape.  workspace:
+    allocated unless given."""
+    shape_of = grad_y if grad_y is not None else grad_h
+    if shape_of is None:
+        raise ValueError("one of grad_h and grad_y is needed")
+    _want_dim(shape_of, "grad_y" if grad_y is not None else "grad_h", 2)
+    T, n = shape_of.shape
+    dev = shape_of.get_device()
+    if dev < 0:
+        raise TypeError("the gradients must be device tensors")
+    xs = [(t, name) for t, name in ((x, "x"), (grad_y, "grad_y"), (grad_x, "grad_x")) if t is not None]
+    rs = [(t, name) for t, name in ((h, "h"), (grad_h, "grad_h"), (grad_residual, "grad_residual")) if t is not None]
+    xd = _float_type(*xs[0]) if xs else FP8G_BF16
+    sd = _float_type(*rs[0]) if rs else FP8G_BF16
+    x_type, r_type = xs[0][0].dtype if xs else None, rs[0][0].dtype if rs else None
+    x_at, x_ld = None, n
+    if x is not None:
+        rows, cols, x_ld, x_dev = _matrix(x, "x")
+        _want(x, "x", (T, n))
+        if x_dev != dev:
+            raise ValueError(f"x is on {x.device}, the gradients on {shape_of.device}")
+        x_at = x.data_ptr()
+    pd, post_at, gate_at, pre_at, gate_rows = _norm_params(x, n, T, dev, post_norm, post_weight, gate, pre_weight)
+    if grad_gate is not None and gate is None:
+        raise ValueError("grad_gate needs gate")
+    f32 = torch.float32
+    ats = (_optional(grad_x, "grad_x", x_type, (T, n), dev), _optional(grad_residual, "grad_residual", r_type, (T, n), dev),
+           _optional(grad_pre_weight, "grad_pre_weight", f32, (n,), dev),
+           _optional(grad_post_weight, "grad_post_weight", f32, (n,), dev),
+           None if grad_gate is None else _tensor(grad_gate, "grad_gate", f32, gate.shape, dev))
+    gh_at, gy_at = _optional(grad_h, "grad_h", r_type, (T, n), dev), _optional(grad_y, "grad_y", x_type, (T, n), dev)
+    h_at = _optional(h, "h", r_type, (T, n), dev)
+    s = _on(stream, dev)
+    needed = fp8_norm_residual_backward_workspace_bytes(T, n) if workspace is None else 0
+    with _allocating(stream):
+        ws_at, ws_bytes, _keep = _ws(workspace, needed, shape_of.device)
+    st = lib().fp8_norm_residual_backward(gh_at, gy_at, x_at, xd, x_ld, h_at, sd, T, n, kind, eps, bool(post_norm),
+                                          post_at, gate_at, gate_rows, residual_scale, pre_at, pd, *ats, ws_at,
+                                          ws_bytes, s)
+    _check("fp8_norm_residual_backward", st)
+    return grad_x, grad_residual, grad_pre_weight, grad_post_weight, grad_gate
+
+
+def fp8_moe_few_tokens_workspace_bytes(num_tokens: int, topk: int, inter: int) -> int:
+    return int(lib().fp8_moe_few_tokens_workspace_bytes(int(num_tokens), int(topk), int(inter)))
+
+
+def fp8_moe_few_tokens(x, expert_idx, weights, up, up_scales, down, down_scales, out, activation=FP8G_ACT_SILU,
+                       workspace=None, stream=None):
+    """out [T][hidden] = sum over a token's experts of weights * down(act(gate
+    x) * (up x)): x [T][hidden] bfloat16 (rows may be strided), expert_idx
+    [T][topk] int32, weights [T][topk] float32 or None (1), up [E][2
+    inter][hidden] (gate rows first) and down [E][hidden][inter] E4M3 codes
+    with scales per 128 x 128 block.  workspace: allocated unless given."""
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    T, hidden, x_ld, dev = _matrix(x, "x")
+    up, down = _codes(up, "up"), _codes(down, "down")
+    _want_dim(up, "up", 3)
+    _want_dim(down, "down", 3)
+    E, inter = down.shape[0], down.shape[2]
+    _want_dim(expert_idx, "expert_idx", 2)
+    topk = expert_idx.shape[1]
+    u8, f32 = torch.uint8, torch.float32
+    ats = (_tensor(expert_idx, "expert_idx", torch.int32, (T, topk), dev), _optional(weights, "weights", f32, (T, topk), dev),
+           T, topk, _tensor(up, "up", u8, (E, 2 * inter, hidden), dev),
+           _tensor(up_scales, "up_scales", f32, (E, _kg(2 * inter), _kg(hidden)), dev),
+           _tensor(down, "down", u8, (E, hidden, inter), dev),
+           _tensor(down_scales, "down_scales", f32, (E, _kg(hidden), _kg(inter)), dev))
+    out_at = _tensor(out, "out", torch.bfloat16, (T, hidden), dev)
+    s = _on(stream, dev)
+    needed = fp8_moe_few_tokens_workspace_bytes(T, topk, inter) if workspace is None else 0
+    with _allocating(stream):
+        ws_at, ws_bytes, _keep = _ws(workspace, needed, x.device)
+    st = lib().fp8_moe_few_tokens(x.data_ptr(), x_ld, *ats, E, hidden, inter, activation, out_at, ws_at, ws_bytes, s)
+    _check("fp8_moe_few_tokens", st)
     return out

@@ -20,8 +20,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8gemm.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fp8gemm.hip", "moe.hip", "moe_ops.hip", "w4.hip", "jit.hip")]
-DENSE_SOURCE = os.path.join(CSRC, "dense_launch.hip")  # compiled once per operand-format pair
+SOURCES = [os.path.join(CSRC, f) for f in ("fp8gemm.hip", "moe.hip", "moe_ops.hip", "w4.hip", "block_ops.hip",
+                                                    "moe_few.hip", "jit.hip")]
+DENSE_SOURCE = os.path.join(CSRC, "dense_launch.hip")  # once per operand-format pair, with an epilogue and without
 DIRECT = os.path.join(HERE, "_direct.so")
 DIRECT_SOURCE = os.path.join(CSRC, "direct.cpp")
 W4_SOURCE = os.path.join(CSRC, "w4_launch.hip")  # compiled once per kind of 4-bit matrix
@@ -67,17 +68,20 @@ def hipcc() -> str:
 
 def _compile_jobs(gen: str, objdir: str):
     """(command, object) per translation unit: the host/grouped/cast unit, the
-    MoE layout unit, the routing and combine unit, the 4-bit unit, the
+    MoE layout unit, the routing and combine unit, the 4-bit unit, the unit of
+    norms and the epilogue's gradients, that of whole MoE layers, the
     runtime-specialisation unit, the dense GEMM instantiations once per
-    operand-format pair and the 4-bit kernels once per kind of matrix."""
+    operand-format pair (with and without an epilogue) and the 4-bit kernels
+    once per kind of matrix."""
     base = [hipcc(), *DEVICE_FLAGS, "--offload-arch=gfx950", "-fPIC", "-c", "-I", INCLUDE, "-I", CSRC, "-I", gen]
     jobs = []
     for src in SOURCES:
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         jobs.append(([*base, src, "-o", obj], obj))
     for fmt in range(4):
-        obj = os.path.join(objdir, f"dense_launch_fmt{fmt}.o")
-        jobs.append(([*base, f"-DFP8G_DENSE_FMT={fmt}", DENSE_SOURCE, "-o", obj], obj))
+        for epi in range(2):
+            obj = os.path.join(objdir, f"dense_launch_fmt{fmt}_epi{epi}.o")
+            jobs.append(([*base, f"-DFP8G_DENSE_FMT={fmt}", f"-DFP8G_DENSE_EPI={epi}", DENSE_SOURCE, "-o", obj], obj))
     for kind in range(3):
         obj = os.path.join(objdir, f"w4_launch_kind{kind}.o")
         jobs.append(([*base, f"-DFP8G_W4_KIND={kind}", W4_SOURCE, "-o", obj], obj))

@@ -1,22 +1,33 @@
 // Dense GEMM instantiations for one operand-format pair, FP8G_DENSE_FMT
-// (0..3; the build compiles this file once per value).  Every instantiation
+// (0..3), with an epilogue or without one, FP8G_DENSE_EPI (0, 1); the build
+// compiles this file once per pair of values.  Every instantiation
 // matches its row of kShapes: tile, wave grid, ring depth, K groups per
 // stage and waves sharing a sub-tile.
 #include "dense_launch.hpp"
+#include "epilogue_kernel.hpp"
 #include "host_common.hpp"
 
 #ifndef FP8G_DENSE_FMT
 #define FP8G_DENSE_FMT 0
+#endif
+#ifndef FP8G_DENSE_EPI
+#define FP8G_DENSE_EPI 0
 #endif
 
 namespace fp8g {
 namespace host {
 namespace {
 
+constexpr bool kEpilogue = FP8G_DENSE_EPI != 0;
+
 template <int BM, int BN, int WMW, int WNW, int ST, bool SPLIT, int KU, int WK, int FMT>
 void launch(const GemmParams& p, int64_t grid, hipStream_t s) {
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WMW, WNW, ST, kDense, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
-                     dim3(64 * WMW * WNW * WK), 0, s, p);
+  if constexpr (kEpilogue)
+    hipLaunchKernelGGL((gemm_epilogue_kernel<BM, BN, WMW, WNW, ST, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
+                       dim3(64 * WMW * WNW * WK), 0, s, p);
+  else
+    hipLaunchKernelGGL((gemm_kernel<BM, BN, WMW, WNW, ST, kDense, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
+                       dim3(64 * WMW * WNW * WK), 0, s, p);
 }
 
 template <bool SPLIT, int FMT>
@@ -37,12 +48,12 @@ int launch_kind(int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
 
 }  // namespace
 
-template <int FMT>
+template <int FMT, bool>
 int launch_dense_kind(bool split, int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
   return split ? launch_kind<true, FMT>(kind, p, grid, s) : launch_kind<false, FMT>(kind, p, grid, s);
 }
 
-template int launch_dense_kind<FP8G_DENSE_FMT>(bool, int, const GemmParams&, int64_t, hipStream_t);
+template int launch_dense_kind<FP8G_DENSE_FMT, kEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
 
 }  // namespace host
 }  // namespace fp8g

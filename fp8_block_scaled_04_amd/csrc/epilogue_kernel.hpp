@@ -1,0 +1,134 @@
+// What follows the dense product, applied to its FP32 sums before their one
+// rounding:
+//
+//   z = acc + bias[n]             (z itself as BF16 too, where it is asked for)
+//   out = bf16( act(z) + residual )
+//
+// The tile goes through LDS as FP32, in row order, so that one piece
+// of code does everything: a thread keeps 8 columns (and their bias) for all of
+// its rows, reads the residual and writes the output in whole 16-byte pieces
+// of rows, and the activation is chosen once per piece in a loop instead of in
+// an unrolled copy for every accumulator.  The 256 x 256 tile, whose FP32 form
+// is twice the ring, goes in two halves.
+#pragma once
+
+#include "activation.hpp"
+#include "gemm_kernel.hpp"
+
+namespace fp8g {
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& a, float v[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack_bf16x8(const float v[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+struct Epilogue {
+  static constexpr bool kActive = true;
+
+  // N (4 or 8) consecutive values of the bias, from column `col` on.
+  template <int N>
+  static __device__ __forceinline__ void load_bias(const GemmParams& p, int col, float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = 0.f;
+    if (!p.bias) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      b[i] = p.bias_bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p.bias)[col + i]) << 16)
+                         : static_cast<const float*>(p.bias)[col + i];
+  }
+
+  // Four sums of the split-K fix-up, at out[at] in column `col`.
+  static __device__ __forceinline__ void store4(const GemmParams& p, const v4f& sum, int64_t at, int col) {
+    float b[4];
+    load_bias(p, col, b);
+    uint2 r = make_uint2(0, 0), v;
+    if (p.residual) r = *reinterpret_cast<const uint2*>(p.residual + at);
+    float z[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = sum[i] + b[i];
+    if (p.preact) {
+      v.x = pack_bf16x2(z[0], z[1]);
+      v.y = pack_bf16x2(z[2], z[3]);
+      *reinterpret_cast<uint2*>(p.preact + at) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? r.x : r.y;
+      y[i] = activate(p.activation, z[i]) + __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+    v.x = pack_bf16x2(y[0], y[1]);
+    v.y = pack_bf16x2(y[2], y[3]);
+    *reinterpret_cast<uint2*>(p.out + at) = v;
+  }
+
+  // A whole tile from the accumulators (write_tile's arguments; SMEM bytes of LDS, free once the K loop is done).
+  template <int BM, int BN, int TM, int TN, int SMEM>
+  static __device__ __forceinline__ void store_tile(const GemmParams& p, const v4f (&acc)[TN][TM], uint8_t* smem,
+                                                    bool holder, int wrow_m, int wrow_n, int m0, int n0, int rows,
+                                                    int shape_n) {
+    constexpr int LDT = BN + 4;  // padded row stride (floats) of the staged tile
+    constexpr int PASSES = BM * LDT * 4 <= SMEM ? 1 : 2, PR = BM / PASSES;
+    static_assert(PR * LDT * 4 <= SMEM && PR % (16 * TM) == 0, "a pass is whole waves' rows and fits");
+    constexpr int CHUNKS = BN / 8, AHEAD = 4;
+    const int lane = threadIdx.x & (kWave - 1);
+    float* stage = reinterpret_cast<float*>(smem);
+    const int c8 = 8 * (threadIdx.x % CHUNKS), col = n0 + c8;  // n % 8 == 0: a piece is all in or all out
+    const int r0 = threadIdx.x / CHUNKS, step = blockDim.x / CHUNKS;
+    const bool in = col < shape_n;
+    float b[8] = {};
+    if (in) load_bias(p, col, b);
+    for (int pass = 0; pass < PASSES; ++pass) {
+      const int first = pass * PR, last = min(PR, rows - m0 - first);  // rows of this pass
+      __syncthreads();  // the ring, or the rows staged before, are read
+      if (holder && wrow_m / PR == pass) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+            *reinterpret_cast<v4f*>(stage + (wrow_m - first + 16 * j + (lane & 15)) * LDT + wrow_n + 16 * i +
+                                    4 * (lane >> 4)) = acc[i][j];
+      }
+      __syncthreads();
+      if (!in) continue;
+      const int64_t at0 = int64_t(m0 + first) * shape_n + col;
+      for (int r = r0; r < last; r += AHEAD * step) {
+        uint4 res[AHEAD] = {};
+        if (p.residual) {
+#pragma unroll
+          for (int u = 0; u < AHEAD; ++u)  // rows past the end: the last one again
+            res[u] = *reinterpret_cast<const uint4*>(p.residual + at0 + int64_t(min(r + u * step, last - 1)) * shape_n);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int row = r + u * step;
+          if (row >= last) break;
+          const v4f lo = *reinterpret_cast<const v4f*>(stage + row * LDT + c8);
+          const v4f hi = *reinterpret_cast<const v4f*>(stage + row * LDT + c8 + 4);
+          float z[8], y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = (i < 4 ? lo[i] : hi[i - 4]) + b[i];
+          const int64_t at = at0 + int64_t(row) * shape_n;
+          if (p.preact) *reinterpret_cast<uint4*>(p.preact + at) = pack_bf16x8(z);
+          unpack_bf16x8(res[u], y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] += activate(p.activation, z[i]);
+          *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(y);
+        }
+      }
+    }
+  }
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, bool SPLIT, int KU, int WK, int FMT>
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N * WK, 1) gemm_epilogue_kernel(const GemmParams p) {
+  gemm_body<BM, BN, WAVES_M, WAVES_N, STAGES, kDense, SPLIT, KU, WK, FMT, 0, 0, Epilogue>(p);
+}
+
+}  // namespace fp8g

@@ -37,13 +37,15 @@ void launch_gemm(const GemmParams& p, int64_t grid, hipStream_t s) {
 }
 
 // The dense GEMM kernels are instantiated in dense_launch.hip, one object per
-// operand-format pair (FMT: bit 0 = LHS in E5M2, bit 1 = RHS in E5M2).
+// operand-format pair (FMT: bit 0 = LHS in E5M2, bit 1 = RHS in E5M2), with
+// and without an epilogue.
+template <bool EPI>
 int launch_dense_fmt(bool split, int fmt, int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
   switch (fmt) {
-    case 1: return fp8g::host::launch_dense_kind<1>(split, kind, p, grid, s);
-    case 2: return fp8g::host::launch_dense_kind<2>(split, kind, p, grid, s);
-    case 3: return fp8g::host::launch_dense_kind<3>(split, kind, p, grid, s);
-    default: return fp8g::host::launch_dense_kind<0>(split, kind, p, grid, s);
+    case 1: return fp8g::host::launch_dense_kind<1, EPI>(split, kind, p, grid, s);
+    case 2: return fp8g::host::launch_dense_kind<2, EPI>(split, kind, p, grid, s);
+    case 3: return fp8g::host::launch_dense_kind<3, EPI>(split, kind, p, grid, s);
+    default: return fp8g::host::launch_dense_kind<0, EPI>(split, kind, p, grid, s);
   }
 }
 
@@ -86,15 +88,15 @@ int check_dense_args(const uint8_t* lhs, int lhs_format, const float* lhs_scales
 }
 
 // The dense GEMM of checked arguments (m, n > 0): configuration, split-K
-// workspace layout, launches.
+// workspace layout, launches.  EPI: with the epilogue that p holds.
+template <bool EPI = false>
 int run_dense_gemm(const uint8_t* lhs, int fmt, const float* lhs_scales, int64_t lhs_scales_ld, const uint8_t* rhs,
                    const float* rhs_scales, uint16_t* out, int m, int n, int k, void* workspace,
-                   size_t workspace_bytes, void* stream) {
+                   size_t workspace_bytes, void* stream, GemmParams p = GemmParams{}) {
   DenseConfig c = dense_config(m, n, k, true);
   if (c.splits > 1 && (!workspace || workspace_bytes < dense_workspace(c, m, n)))
     c = dense_config(m, n, k, false);
 
-  GemmParams p{};
   p.a = lhs; p.sa = lhs_scales; p.b = rhs; p.sb = rhs_scales; p.out = out;
   if (c.splits > 1) {
     p.tile_counters = static_cast<unsigned long long*>(workspace);
@@ -111,7 +113,7 @@ int run_dense_gemm(const uint8_t* lhs, int fmt, const float* lhs_scales, int64_t
     std::fprintf(stderr, "[fp8gemm] dense m=%d n=%d k=%d kind=%d tiles=%dx%d splits=%d grid=%lld\n", m, n, k,
                  c.kind, c.tiles_m, c.tiles_n, c.splits, (long long)grid);
   return launch_units(p, grid, [&](int64_t g) {
-    if (const int st = launch_dense_fmt(c.splits > 1, fmt, c.kind, p, g, s)) return st;  // before any launch
+    if (const int st = launch_dense_fmt<EPI>(c.splits > 1, fmt, c.kind, p, g, s)) return st;  // before any launch
     return launched("gemm");
   });
 }
@@ -313,6 +315,27 @@ int fp8_gemm_nt_fmt(const uint8_t* lhs, int lhs_format, const float* lhs_scales,
   if (m == 0 || n == 0) return FP8G_OK;
   return run_dense_gemm(lhs, fmt, lhs_scales, lhs_scales_ld, rhs, rhs_scales, out, m, n, k, workspace,
                         workspace_bytes, stream);
+}
+
+int fp8_gemm_nt_epilogue(const uint8_t* lhs, int lhs_format, const float* lhs_scales, int64_t lhs_scales_ld,
+                         const uint8_t* rhs, int rhs_format, const float* rhs_scales, const void* bias, int bias_dtype,
+                         int activation, const uint16_t* residual, uint16_t* preact, uint16_t* out, int m, int n,
+                         int k, void* workspace, size_t workspace_bytes, void* stream) {
+  int fmt = 0;
+  if (activation < FP8G_ACT_NONE || activation > FP8G_ACT_SILU) return FP8G_EINVAL;
+  if (bias_dtype != FP8G_F32 && bias_dtype != FP8G_BF16) return FP8G_EINVAL;
+  if (const int st = check_dense_args(lhs, lhs_format, lhs_scales, lhs_scales_ld, rhs, rhs_format, rhs_scales, out,
+                                      m, n, k, workspace, &fmt))
+    return st;
+  if (m == 0 || n == 0) return FP8G_OK;
+  if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (preact && !aligned16(preact)))
+    return FP8G_EINVAL;
+  if (preact && (preact == out || preact == residual)) return FP8G_EINVAL;
+  GemmParams p{};
+  p.bias = bias; p.bias_bf16 = bias_dtype == FP8G_BF16; p.activation = activation;
+  p.residual = residual; p.preact = preact;
+  return run_dense_gemm<true>(lhs, fmt, lhs_scales, lhs_scales_ld, rhs, rhs_scales, out, m, n, k, workspace,
+                              workspace_bytes, stream, p);
 }
 
 int fp8_gemm_nt_noalloc(const uint8_t* lhs, const float* lhs_scales, int64_t lhs_scales_ld, const uint8_t* rhs,

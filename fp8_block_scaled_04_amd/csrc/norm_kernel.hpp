@@ -1,0 +1,381 @@
+// The step between two blocks of a model, and its gradients, for gfx950.
+//
+//   u = norm(x) post_weight   (or x),     h = residual_scale residual + gate u,
+//   y = norm(h) pre_weight    -> y in x's type, and / or FP8 codes with a scale per 128 columns
+//   norm(v) = (v - mean) / sqrt(var + eps)   or   v / sqrt(mean v^2 + eps)
+// All of it in FP32, every output rounded once; y and the codes come from h
+// before it is rounded.
+//
+// Gradients, with gy that of y and gh that of h from everything else that
+// reads it; h as the forward pass stored it:
+//   a = gy pre_weight,  dh = gh + D(a, h),    grad_residual = residual_scale dh
+//   du = gate dh,       grad_gate = dh u  (summed over rows where rows share it)
+//   grad_x = D(du post_weight, x)  (or du)
+//   grad_pre_weight = sum over rows of gy n(h),  grad_post_weight = that of du n(x)
+//   D(b, v) = (b - n mean(b n) [- mean b]) / sqrt(..),  n = norm(v)   [layer norms]
+#pragma once
+
+#include "cast_kernel.hpp"
+#include "gemm_kernel.hpp"  // xcd_logical
+
+namespace fp8g {
+
+struct NormArgs {
+  const void *x, *residual, *post_weight, *gate, *pre_weight;
+  void *h, *y;
+  uint8_t* q;
+  float* q_scales;
+  int64_t x_ld, residual_ld, q_ld;
+  int rows, n;
+  bool post_norm, gate_per_row, params_bf16, q_e5m2;
+  float eps, residual_scale;
+};
+
+struct NormGradArgs {
+  const void *grad_h, *grad_y, *x, *h, *post_weight, *gate, *pre_weight;
+  void *grad_x, *grad_residual;
+  float* grad_gate;  // [rows][n], of a gate per row
+  float* partial;    // [slices][3][n]: pre_weight, post_weight, gate; null: no sums
+  int64_t x_ld;
+  int rows, n, rows_per_slice;
+  bool post_norm, gate_per_row, params_bf16;
+  float eps, residual_scale;
+};
+
+// 8 consecutive elements as they are stored.
+template <typename T>
+struct Raw8 {
+  static constexpr int kWords = sizeof(T) / 2;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = p[i];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4& q = w[i * kWords / 8];
+      const int at = kWords == 2 ? i & 3 : i >> 1;
+      const uint32_t u = at == 0 ? q.x : at == 1 ? q.y : at == 2 ? q.z : q.w;
+      v[i] = __uint_as_float(kWords == 2 ? u : i & 1 ? u & 0xffff0000u : u << 16);
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store8(void* base, int64_t at, const float v[8]) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(base) + at);
+  if constexpr (sizeof(T) == 4) {
+    p[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    p[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  } else {
+    p[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+}
+
+// 8 values of a parameter (FP32 or BF16), 1 where there is none.
+__device__ __forceinline__ void param8(const void* p, bool bf16, int64_t at, float v[8]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.f;
+  } else if (bf16) {
+    load8(static_cast<const uint16_t*>(p) + at, v);
+  } else {
+    load8(static_cast<const float*>(p) + at, v);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int s = 32; s; s >>= 1) v += __shfl_xor(v, s, kWave);
+  return v;
+}
+
+// Sums of up to two values over the `waves` waves of a row (one wave: no barrier).  `part`: a place of LDS of its own.
+constexpr int kNormMaxWaves = 16;
+struct NormPart {
+  float v[2][kNormMaxWaves];
+};
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int waves, NormPart& part) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (waves == 1) return;
+  const int lane = threadIdx.x & (kWave - 1);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) part.v[i][threadIdx.x >> 6] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float t = (lane & 15) < waves ? part.v[i][lane & 15] : 0.f;
+#pragma unroll
+    for (int s = 8; s; s >>= 1) t += __shfl_xor(t, s, 16);
+    v[i] = t;
+  }
+}
+
+// v = norm(v) over a row's n columns, of which this thread holds C pieces of 8; returns 1 / sqrt(..).  `in`: the piece
+// is inside the row (the others hold zeros, before and after).
+template <bool LAYER, int C>
+__device__ __forceinline__ float normalise(float (&v)[C][8], const bool (&in)[C], int n, float eps, int waves,
+                                           NormPart* parts) {
+  float s[1] = {0.f};
+  if constexpr (LAYER) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += v[c][i];
+    row_sums(s, waves, parts[0]);
+    const float mean = s[0] / n;
+    s[0] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = in[c] ? v[c][i] - mean : 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[0] = fmaf(v[c][i], v[c][i], s[0]);
+  row_sums(s, waves, parts[1]);
+  const float r = 1.f / sqrtf(s[0] / n + eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[c][i] *= r;
+  return r;
+}
+
+// A thread holds C pieces of 8 columns, blockDim.x threads a row, blockDim.y rows a workgroup (more than one only
+// where a row is one wave's).  Consecutive rows run on one XCD, so that its L2 gathers the lines of the scales.
+template <typename X, typename R, bool LAYER, int C>
+__global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(const NormArgs a) {
+  __shared__ NormPart parts[4];
+  const int row = xcd_logical(blockIdx.x, gridDim.x) * int(blockDim.y) + int(threadIdx.y);
+  if (row >= a.rows) return;  // (whole waves: no barrier is left out)
+  const int waves = blockDim.x >> 6;
+  int col[C];
+  bool in[C];
+  float v[C][8];
+  Raw8<X> xs[C];
+  Raw8<R> rs[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = 8 * int(threadIdx.x + c * blockDim.x);
+    in[c] = col[c] < a.n;
+    xs[c].clear();
+    rs[c].clear();
+    if (in[c]) {
+      xs[c].load(a.x, row * a.x_ld + col[c]);
+      if (a.residual) rs[c].load(a.residual, row * a.residual_ld + col[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) xs[c].get(v[c]);
+  if (a.post_norm) normalise<LAYER>(v, in, a.n, a.eps, waves, parts);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (!in[c]) continue;
+    float w[8], r[8];
+    if (a.post_norm && a.post_weight) {
+      param8(a.post_weight, a.params_bf16, col[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+    }
+    if (a.gate) {
+      param8(a.gate, a.params_bf16, (a.gate_per_row ? int64_t(row) * a.n : 0) + col[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+    }
+    if (a.residual) {
+      rs[c].get(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = fmaf(a.residual_scale, r[i], v[c][i]);
+    }
+    if (a.h) store8<R>(a.h, int64_t(row) * a.n + col[c], v[c]);
+  }
+  if (!a.y && !a.q) return;
+  normalise<LAYER>(v, in, a.n, a.eps, waves, parts + 2);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (in[c]) {
+      float w[8];
+      param8(a.pre_weight, a.params_bf16, col[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+      if (a.y) store8<X>(a.y, int64_t(row) * a.n + col[c], v[c]);
+    }
+    if (a.q) {  // as the per-token-group cast: 16 lanes hold a group
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[c][i]));
+#pragma unroll
+      for (int s = 1; s < 16; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, 16));
+      const float s = a.q_e5m2 ? group_scale<kFmtE5M2>(top) : group_scale<kFmtE4M3>(top);
+      float d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = __fdiv_rn(v[c][i], s);
+      uint2 w;
+      if (a.q_e5m2) {
+        w.x = fp8x4<kFmtE5M2>(d[0], d[1], d[2], d[3]);
+        w.y = fp8x4<kFmtE5M2>(d[4], d[5], d[6], d[7]);
+      } else {
+        w.x = fp8x4<kFmtE4M3>(d[0], d[1], d[2], d[3]);
+        w.y = fp8x4<kFmtE4M3>(d[4], d[5], d[6], d[7]);
+      }
+      if (in[c]) {
+        *reinterpret_cast<uint2*>(a.q + int64_t(row) * a.n + col[c]) = w;
+        if ((threadIdx.x & 15) == 0) a.q_scales[(col[c] >> 7) * a.q_ld + row] = s;
+      }
+    }
+  }
+}
+
+// Grid: slices of rows, which a workgroup takes one after the other, each thread with its C pieces of 8 columns, whose
+// sums over the rows stay in its registers.
+template <typename X, typename R, bool LAYER, int C, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
+  __shared__ NormPart parts[4];
+  const int waves = blockDim.x >> 6, n = a.n;
+  const float inv_n = 1.f / n;
+  int col[C];
+  bool in[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = 8 * int(threadIdx.x + c * blockDim.x);
+    in[c] = col[c] < n;
+  }
+  float s_pre[C][8] = {}, s_post[C][8] = {}, s_gate[C][8] = {};
+  const int first = blockIdx.x * a.rows_per_slice, last = min(a.rows, first + a.rows_per_slice);
+  for (int row = first; row < last; ++row) {
+    const int64_t at0 = int64_t(row) * n;
+    Raw8<X> xs[C], gys[C];
+    Raw8<R> hs[C], ghs[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      xs[c].clear(), gys[c].clear(), hs[c].clear(), ghs[c].clear();
+      if (!in[c]) continue;
+      if (a.x) xs[c].load(a.x, row * a.x_ld + col[c]);
+      if (a.grad_y) {
+        gys[c].load(a.grad_y, at0 + col[c]);
+        hs[c].load(a.h, at0 + col[c]);
+      }
+      if (a.grad_h) ghs[c].load(a.grad_h, at0 + col[c]);
+    }
+    float d[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) ghs[c].get(d[c]);
+    if (a.grad_y) {
+      float v[C][8], m[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) hs[c].get(v[c]);
+      const float r = normalise<LAYER>(v, in, n, a.eps, waves, parts);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float g[8], w[8];
+        gys[c].get(g);
+        if (in[c]) param8(a.pre_weight, a.params_bf16, col[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float b = in[c] ? g[i] * w[i] : 0.f;
+          m[0] = fmaf(b, v[c][i], m[0]);
+          m[1] += b;
+        }
+      }
+      row_sums(m, waves, parts[2]);
+      m[0] *= inv_n;
+      m[1] = LAYER ? m[1] * inv_n : 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float g[8], w[8];
+        gys[c].get(g);
+        if (!in[c]) continue;
+        param8(a.pre_weight, a.params_bf16, col[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s_pre[c][i] = fmaf(g[i], v[c][i], s_pre[c][i]);
+          d[c][i] = fmaf(r, fmaf(-m[0], v[c][i], g[i] * w[i]) - m[1], d[c][i]);
+        }
+      }
+    }
+    if (a.grad_residual) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (!in[c]) continue;
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = a.residual_scale * d[c][i];
+        store8<R>(a.grad_residual, at0 + col[c], g);
+      }
+    }
+    float v[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) xs[c].get(v[c]);
+    const float r = a.post_norm ? normalise<LAYER>(v, in, n, a.eps, waves, parts) : 1.f;
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x
+      if (!in[c]) continue;
+      float w[8], g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (a.post_norm) param8(a.post_weight, a.params_bf16, col[c], w);
+      if (a.gate) {
+        float u[8];
+        param8(a.gate, a.params_bf16, (a.gate_per_row ? at0 : 0) + col[c], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (v[c][i] * w[i]);
+        if (a.gate_per_row) {
+          if (a.grad_gate) store8<float>(a.grad_gate, at0 + col[c], u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s_gate[c][i] += u[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[c][i] *= g[i];
+      }
+      if (a.post_norm) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s_post[c][i] = fmaf(d[c][i], v[c][i], s_post[c][i]);
+          d[c][i] *= w[i];
+          m[0] = fmaf(d[c][i], v[c][i], m[0]);
+          m[1] += d[c][i];
+        }
+      }
+    }
+    if (a.post_norm) {
+      row_sums(m, waves, parts[3]);
+      m[0] *= inv_n;
+      m[1] = LAYER ? m[1] * inv_n : 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[c][i] = r * (fmaf(-m[0], v[c][i], d[c][i]) - m[1]);
+    }
+    if (a.grad_x) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (in[c]) store8<X>(a.grad_x, at0 + col[c], d[c]);
+    }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (!in[c]) continue;
+    float* p = a.partial + int64_t(blockIdx.x) * 3 * n + col[c];
+    store8<float>(p, 0, s_pre[c]);
+    store8<float>(p, n, s_post[c]);
+    store8<float>(p, 2 * int64_t(n), s_gate[c]);
+  }
+}
+
+}  // namespace fp8g

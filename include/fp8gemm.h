@@ -486,6 +486,131 @@ int fp8_w4_matvec_experts(const uint16_t* x, int64_t x_ld, int x_rows, const int
                           const uint8_t* w_zeros, int group, void* out, int out_dtype, int num_experts, int n, int k,
                           void* stream);
 
+/* ---- The feed-forward block around the products ------------------------------
+ * What follows a dense product, what stands between two blocks, and a whole
+ * mixture-of-experts layer for a few tokens. */
+enum {              /* activations */
+  FP8G_ACT_NONE = 0,
+  FP8G_ACT_RELU = 1,
+  FP8G_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution's function */
+  FP8G_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  FP8G_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+};
+
+/* The dense GEMM with what follows it, applied to its FP32 sums:
+ *   z = sums + bias[n],   out = bf16(act(z) + residual)
+ *   bias      [n] FP32 or BF16 (bias_dtype FP8G_F32 / FP8G_BF16), or NULL
+ *   residual  [m][n] BF16 or NULL; may be `out` itself
+ *   preact    [m][n] BF16 or NULL: z, rounded, for fp8_epilogue_backward; not
+ *             `out` and not `residual`
+ * Everything else (operands, formats, workspace, CU limit, configurations) as
+ * fp8_gemm_nt_fmt; with no bias, no residual and FP8G_ACT_NONE the same bits.
+ * An activation of minus infinity is its limit (0), of a NaN a NaN. */
+int fp8_gemm_nt_epilogue(const uint8_t* lhs, int lhs_format, const float* lhs_scales, int64_t lhs_scales_ld,
+                         const uint8_t* rhs, int rhs_format, const float* rhs_scales, const void* bias,
+                         int bias_dtype, int activation, const uint16_t* residual, uint16_t* preact, uint16_t* out,
+                         int m, int n, int k, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of z and of the bias, from that of out (which is the residual's
+ * too):
+ *   grad_preact [m][n] BF16 = bf16(grad_out * act'(preact)); may be grad_out or
+ *               preact itself
+ *   grad_bias   [n] FP32 = sum over rows of grad_out * act'(preact) (FP32, before
+ *               that rounding), or NULL: not computed
+ * ReLU's derivative at 0 is 0.  n % 8 == 0 (FP8G_EUNSUPPORTED otherwise);
+ * tensors 16-byte aligned.  With grad_bias the call needs a workspace of
+ * fp8_epilogue_backward_workspace_bytes() bytes (0: none), uninitialised, not
+ * shared by concurrent calls; FP8G_EINVAL without it.  Sums have a fixed order:
+ * equal calls give equal bits.  m = 0 gives a grad_bias of zeros. */
+size_t fp8_epilogue_backward_workspace_bytes(int m, int n);
+int fp8_epilogue_backward(const uint16_t* grad_out, const uint16_t* preact, int activation, int m, int n,
+                          uint16_t* grad_preact, float* grad_bias, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+enum { FP8G_NORM_RMS = 0, FP8G_NORM_LAYER = 1 };
+
+/* The step between two blocks, for every row of n columns:
+ *   u = norm(x) * post_weight  (post_norm nonzero),  else x
+ *   h = residual_scale * residual + gate * u
+ *   y = norm(h) * pre_weight
+ *   norm(v) = v / sqrt(mean(v^2) + eps)            (FP8G_NORM_RMS)
+ *             (v - mean(v)) / sqrt(var(v) + eps)   (FP8G_NORM_LAYER)
+ * in FP32, every output rounded once (y and the codes from h before it is
+ * rounded).
+ *   x         [num_rows][n] FP32 or BF16 (x_dtype), row stride x_ld >= n
+ *   residual  [num_rows][n] FP32 or BF16 (stream_dtype), row stride residual_ld
+ *             >= n, or NULL (h = gate * u; residual_scale is then not used)
+ *   gate      [gate_rows][n], gate_rows 1 (one for all rows) or num_rows, or NULL
+ *   post_weight, pre_weight [n] or NULL (1); they and the gate are param_dtype
+ *   h         [num_rows][n] stream_dtype, or NULL; may be the residual itself
+ *             where residual_ld == n
+ *   y         [num_rows][n] x_dtype, or NULL; may be x itself where x_ld == n
+ *   q         [num_rows][n] FP8 codes of y (q_format), or NULL, with q_scales
+ *             [ceil(n / 128)][q_scales_ld >= num_rows]: what
+ *             fp8_cast_per_token_group makes of y in FP32
+ * At least one of h, y and q.  Strides are multiples of 8, n % 8 == 0 and n <=
+ * 16384 (FP8G_EUNSUPPORTED otherwise); tensors 16-byte aligned.  Sums of
+ * squares are FP32: rows of values above 1e18 come out as zeros. */
+int fp8_norm_residual(const void* x, int x_dtype, int64_t x_ld, const void* residual, int64_t residual_ld,
+                      int stream_dtype, int num_rows, int n, int kind, float eps, int post_norm,
+                      const void* post_weight, const void* gate, int gate_rows, float residual_scale,
+                      const void* pre_weight, int param_dtype, void* h, void* y, uint8_t* q, int q_format,
+                      float* q_scales, int64_t q_scales_ld, void* stream);
+
+/* Gradients of fp8_norm_residual.
+ *   grad_h    [num_rows][n] stream_dtype: the gradient of h from all that reads
+ *             it but y, or NULL (none)
+ *   grad_y    [num_rows][n] x_dtype: that of y (of FP8 codes: of the values they
+ *             stand for), or NULL (none).  One of the two at least.
+ *   x, h      as the forward pass had and left them; x may be NULL without
+ *             post_norm and gate, h without grad_y
+ *   grad_x    [num_rows][n] x_dtype, or NULL
+ *   grad_residual [num_rows][n] stream_dtype, or NULL
+ *   grad_pre_weight, grad_post_weight [n] FP32, or NULL
+ *   grad_gate [gate_rows][n] FP32, or NULL
+ * grad_x may be grad_y, and grad_residual grad_h.  Where one of the three
+ * gradients summed over rows (that of a gate with gate_rows == num_rows > 1 is
+ * not) is asked for, the call needs a workspace of
+ * fp8_norm_residual_backward_workspace_bytes() bytes, uninitialised, not shared
+ * by concurrent calls; FP8G_EINVAL without it.  Sums have a fixed order: equal
+ * calls give equal bits.  num_rows = 0 gives sums of zero. */
+size_t fp8_norm_residual_backward_workspace_bytes(int num_rows, int n);
+int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const void* x, int x_dtype, int64_t x_ld,
+                               const void* h, int stream_dtype, int num_rows, int n, int kind, float eps,
+                               int post_norm, const void* post_weight, const void* gate, int gate_rows,
+                               float residual_scale, const void* pre_weight, int param_dtype, void* grad_x,
+                               void* grad_residual, float* grad_pre_weight, float* grad_post_weight,
+                               float* grad_gate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A mixture-of-experts layer for a few tokens (a decoding step), in two kernels:
+ *   mid[p] = bf16(act(G x_t) * (U x_t)),  out[t] = bf16(sum over j of weights[p] * (D mid[p]))
+ * for pair p = t * topk + j with the matrices of expert expert_idx[p], FP8 E4M3
+ * codes and block scales as fp8_grouped_gemm_contiguous takes them (so a layer's
+ * prefill and decode share one copy); the activations stay BF16.
+ *   x          [num_tokens][hidden] BF16, row stride x_ld >= hidden, x_ld % 8 == 0
+ *   expert_idx [num_tokens][topk] int32; a pair with an index outside [0,
+ *              num_experts) adds nothing, and a token without any other has a row of
+ *              zeros; an expert may be named twice
+ *   weights    [num_tokens][topk] FP32, or NULL (1)
+ *   up         [num_experts][2 inter][hidden]: G, then U;
+ *              up_scales [num_experts][2 inter / 128][hidden / 128]
+ *   down       [num_experts][hidden][inter];
+ *              down_scales [num_experts][hidden / 128][inter / 128]
+ *   out        [num_tokens][hidden] BF16 (written in full)
+ *   workspace  fp8_moe_few_tokens_workspace_bytes() bytes, uninitialised, not shared
+ *              by concurrent calls; FP8G_EINVAL without it
+ * Any number of tokens, min(64, 1024 / topk) at a time: an expert's matrices are
+ * read once for up to 16 of its pairs, so beyond a few hundred pairs the grouped
+ * GEMMs are the way.  hidden % 128 == 0 and inter % 128 == 0, both <= 65536, inter
+ * > 0, topk <= 32, num_experts <= 65535 (FP8G_EUNSUPPORTED otherwise).  Tensors
+ * 16-byte aligned (expert_idx, weights 4).  A token's sum goes over its experts in a
+ * fixed order: equal calls give equal bits. */
+size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int inter);
+int fp8_moe_few_tokens(const uint16_t* x, int64_t x_ld, const int32_t* expert_idx, const float* weights,
+                       int num_tokens, int topk, const uint8_t* up, const float* up_scales, const uint8_t* down,
+                       const float* down_scales, int num_experts, int hidden, int inter, int activation,
+                       uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes that let fp8_gemm_nt choose split-K for this shape
  * (0 = never needed).  An upper bound; depends on the CU limit in force. */
 size_t fp8_gemm_workspace_bytes(int m, int n, int k, int num_groups);
