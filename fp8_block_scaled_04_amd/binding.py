@@ -963,6 +963,12 @@ def fp8_gemm_nt_epilogue(lhs, lhs_scales, rhs, rhs_scales, out, bias=None, activ
     """out [m][n] = activation(fp8_gemm_nt + bias) + residual, of the FP32
     sums.  bias [n] float32 or bfloat16; residual [m][n] bfloat16 (may be
     out); preact [m][n] bfloat16 receives the sums with their bias."""
+    if _direct and stream is None:
+        st = _direct.gemm_nt_epilogue(lhs, lhs_scales, rhs, rhs_scales, out, bias, activation, residual, preact,
+                                      lhs_format, rhs_format, workspace)
+        if st is not None:
+            _check("fp8_gemm_nt_epilogue", st)
+            return out
     lhs_format, rhs_format = _fmt(lhs_format, "lhs_format"), _fmt(rhs_format, "rhs_format")
     lhs, rhs = _codes(lhs, "lhs", lhs_format), _codes(rhs, "rhs", rhs_format)
     lhs_scales, rhs_scales = _f32(lhs_scales, "lhs_scales"), _f32(rhs_scales, "rhs_scales")
@@ -989,6 +995,11 @@ def fp8_epilogue_backward(grad_out, preact, activation, grad_preact, grad_bias=N
     """Gradients of fp8_gemm_nt_epilogue's sums (grad_preact [m][n] bfloat16)
     and of its bias (grad_bias [n] float32, None: not computed) from that of
     its output; workspace: allocated unless given."""
+    if _direct and stream is None:
+        st = _direct.epilogue_backward(grad_out, preact, activation, grad_preact, grad_bias, workspace)
+        if st is not None:
+            _check("fp8_epilogue_backward", st)
+            return grad_preact, grad_bias
     _want_dim(preact, "preact", 2)
     m, n = preact.shape
     dev = preact.get_device()
@@ -1037,6 +1048,12 @@ def fp8_norm_residual(x, residual=None, h=None, y=None, q=None, q_scales=None, *
     [T][n] the FP8 codes of y with q_scales [KG][ld >= T]; gate [n], [1][n] or
     [T][n]; x and residual rows may be strided.  Outputs not given are not
     computed.  Returns (h, y, q, q_scales)."""
+    if _direct and stream is None:
+        st = _direct.norm_residual(x, residual, h, y, q, q_scales, pre_weight, post_norm, post_weight, gate,
+                                   residual_scale, kind, eps, q_format)
+        if st is not None:
+            _check("fp8_norm_residual", st)
+            return h, y, q, q_scales
     xd = _float_type(x, "x")
     T, n, x_ld, dev = _matrix(x, "x")
     stream_t = residual if residual is not None else h
@@ -1082,6 +1099,13 @@ def fp8_norm_residual_backward(grad_h, grad_y, x, h, grad_x=None, grad_residual=
     post_norm and gate, h without grad_y).  Those not given are not computed;
     the parameters' are float32, grad_gate of the gate's shape.  workspace:
     allocated unless given."""
+    if _direct and stream is None:
+        st = _direct.norm_residual_backward(grad_h, grad_y, x, h, grad_x, grad_residual, grad_pre_weight,
+                                            grad_post_weight, grad_gate, pre_weight, post_norm, post_weight, gate,
+                                            residual_scale, kind, eps, workspace)
+        if st is not None:
+            _check("fp8_norm_residual_backward", st)
+            return grad_x, grad_residual, grad_pre_weight, grad_post_weight, grad_gate
     shape_of = grad_y if grad_y is not None else grad_h
     if shape_of is None:
         raise ValueError("one of grad_h and grad_y is needed")
@@ -1134,6 +1158,12 @@ def fp8_moe_few_tokens(x, expert_idx, weights, up, up_scales, down, down_scales,
     [T][topk] int32, weights [T][topk] float32 or None (1), up [E][2
     inter][hidden] (gate rows first) and down [E][hidden][inter] E4M3 codes
     with scales per 128 x 128 block.  workspace: allocated unless given."""
+    if _direct and stream is None:
+        st = _direct.moe_few_tokens(x, expert_idx, weights, up, up_scales, down, down_scales, out, activation,
+                                    workspace)
+        if st is not None:
+            _check("fp8_moe_few_tokens", st)
+            return out
     if x.dtype is not torch.bfloat16:
         raise TypeError(f"x must be bfloat16, got {x.dtype}")
     T, hidden, x_ld, dev = _matrix(x, "x")

@@ -72,8 +72,8 @@ int slice_rows(int64_t rows, int64_t at_most) { return int(cdiv(rows, std::min<i
 
 void launch_column_sums(const float* partial, int slices, int sets, int n, float* out0, float* out1, float* out2,
                         hipStream_t s) {
-  hipLaunchKernelGGL(fp8g::column_sums_kernel, dim3(unsigned(cdiv(n, 16)), unsigned(sets)), dim3(256), 0, s, partial,
-                     slices, n, out0, out1, out2);
+  hipLaunchKernelGGL(fp8g::column_sums_kernel, dim3(unsigned(cdiv(n, 64)), unsigned(sets)),
+                     dim3(64 * fp8g::kSumRuns), 0, s, partial, slices, n, out0, out1, out2);
 }
 
 // Slices of the epilogue's gradients: about 2048 workgroups, 32 rows each at least.
@@ -202,8 +202,8 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
     using R = decltype(r_);
     constexpr bool L = decltype(layer)::value;
     if (n > 8192) return launch_norm_backward<X, R, L, 2, 1024>(a, slices, s);
-    if (n > 2048) return launch_norm_backward<X, R, L, 2, 512>(a, slices, s);
-    return launch_norm_backward<X, R, L, 1, 256>(a, slices, s);
+    if (n > 4096) return launch_norm_backward<X, R, L, 1, 1024>(a, slices, s);
+    return launch_norm_backward<X, R, L, 1, 512>(a, slices, s);
   });
   if (st || !sums) return st;
   launch_column_sums(a.partial, slices, 3, n, grad_pre_weight, grad_post_weight, shared_gate, s);

@@ -1,5 +1,5 @@
-// The calls of expert routing, the weighted combine and the 4-bit products,
-// from Python without ctypes: a decoding step makes them by the hundred, and
+// The calls of expert routing, the weighted combine, the 4-bit products and the
+// feed-forward block, from Python without ctypes: a decoding step makes them by the hundred, and
 // their checks and marshalling in Python cost 3 us a call, as much as the
 // launch.  Each function here takes the tensors of the binding's function of
 // the same name.  It checks types, shapes, strides and devices, launches on the
@@ -262,6 +262,194 @@ PyObject* w4_matvec_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// FP8 codes of a format: bytes, or torch's type of it.
+uint8_t* codes(const at::Tensor& t, int format, at::IntArrayRef shape, int device) {
+  const at::ScalarType type = format == FP8G_E4M3   ? at::kFloat8_e4m3fn
+                              : format == FP8G_E5M2 ? at::kFloat8_e5m2
+                                                    : throw Unusual();
+  return static_cast<uint8_t*>(dense(t, t.scalar_type() == type ? type : at::kByte, shape, device));
+}
+
+// Scales [..][ld] with ld >= rows.
+float* scales_mn(const at::Tensor& t, int64_t groups, int64_t rows, int device, int64_t* ld) {
+  if (t.dim() != 2 || t.size(0) != groups || t.size(1) < rows) throw Unusual();
+  *ld = t.size(1);
+  return static_cast<float*>(dense(t, at::kFloat, t.sizes(), device));
+}
+
+struct Workspace {
+  void* at = nullptr;
+  size_t bytes = 0;
+  Workspace(PyObject* o, int device) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o);
+    at = dense(t, t.scalar_type(), t.sizes(), device);
+    bytes = t.nbytes();
+  }
+};
+
+int64_t groups_of(int64_t k) { return (k + 127) / 128; }
+
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Unusual();
+  return v;
+}
+
+PyObject* gemm_nt_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n_) {
+  // lhs, lhs_scales, rhs, rhs_scales, out, bias, activation, residual, preact, lhs_format, rhs_format, workspace
+  return guarded(n_, 12, [&] {
+    const at::Tensor &l = tensor(a[0]), &r = tensor(a[2]);
+    if (l.dim() != 2 || r.dim() != 2 || !l.is_cuda()) throw Unusual();
+    const int device = l.get_device(), m = as_int(l.size(0)), k = as_int(l.size(1)), n = as_int(r.size(0));
+    const int activation = as_int(a[6]), lf = as_int(a[9]), rf = as_int(a[10]);
+    int64_t ld;
+    const uint8_t* lhs = codes(l, lf, {m, k}, device);
+    const float* ls = scales_mn(tensor(a[1]), groups_of(k), m, device, &ld);
+    const uint8_t* rhs = codes(r, rf, {n, k}, device);
+    const auto* rs = static_cast<const float*>(dense(a[3], at::kFloat, {groups_of(n), groups_of(k)}, device));
+    auto* out = static_cast<uint16_t*>(dense(a[4], at::kBFloat16, {m, n}, device));
+    const int bias_type = a[5] == Py_None ? FP8G_F32 : float_type(tensor(a[5]));
+    const void* bias = dense_or_null(a[5], bias_type == FP8G_F32 ? at::kFloat : at::kBFloat16, {n}, device);
+    const auto* residual = static_cast<const uint16_t*>(dense_or_null(a[7], at::kBFloat16, {m, n}, device));
+    auto* preact = static_cast<uint16_t*>(dense_or_null(a[8], at::kBFloat16, {m, n}, device));
+    const Workspace w(a[11], device);
+    void* s = stream_of(device);
+    return released([&] {
+      return fp8_gemm_nt_epilogue(lhs, lf, ls, ld, rhs, rf, rs, bias, bias_type, activation, residual, preact, out, m,
+                                  n, k, w.at, w.bytes, s);
+    });
+  });
+}
+
+PyObject* epilogue_backward(PyObject*, PyObject* const* a, Py_ssize_t n_) {
+  // grad_out, preact, activation, grad_preact, grad_bias, workspace
+  return guarded(n_, 6, [&] {
+    const at::Tensor& z = tensor(a[1]);
+    if (z.dim() != 2 || !z.is_cuda()) throw Unusual();
+    const int device = z.get_device(), m = as_int(z.size(0)), n = as_int(z.size(1)), activation = as_int(a[2]);
+    const auto* zp = static_cast<const uint16_t*>(dense(z, at::kBFloat16, {m, n}, device));
+    const auto* go = static_cast<const uint16_t*>(dense(a[0], at::kBFloat16, {m, n}, device));
+    auto* gz = static_cast<uint16_t*>(dense(a[3], at::kBFloat16, {m, n}, device));
+    auto* gb = static_cast<float*>(dense_or_null(a[4], at::kFloat, {n}, device));
+    const Workspace w(a[5], device);
+    if (!w.at && gb && fp8_epilogue_backward_workspace_bytes(m, n)) throw Unusual();  // to be allocated
+    void* s = stream_of(device);
+    return released([&] { return fp8_epilogue_backward(go, zp, activation, m, n, gz, gb, w.at, w.bytes, s); });
+  });
+}
+
+// The parameters of the norms: all of one type, a gate of one row or of one for each.
+struct NormParams {
+  const void *post, *gate, *pre;
+  int type = FP8G_F32, gate_rows = 1;
+  NormParams(PyObject* post_, PyObject* gate_, PyObject* pre_, int post_norm, int T, int n, int device) {
+    if (post_ != Py_None && !post_norm) throw Unusual();
+    PyObject* any = post_ != Py_None ? post_ : gate_ != Py_None ? gate_ : pre_;
+    if (any != Py_None) type = float_type(tensor(any));
+    const at::ScalarType t = type == FP8G_F32 ? at::kFloat : at::kBFloat16;
+    post = dense_or_null(post_, t, {n}, device);
+    pre = dense_or_null(pre_, t, {n}, device);
+    gate = nullptr;
+    if (gate_ == Py_None) return;
+    const at::Tensor& g = tensor(gate_);
+    if (g.dim() == 2) {
+      gate_rows = as_int(g.size(0));
+      if (gate_rows != 1 && gate_rows != T) throw Unusual();
+      gate = dense(g, t, {gate_rows, n}, device);
+    } else {
+      gate = dense(g, t, {n}, device);
+    }
+  }
+};
+
+at::ScalarType scalar(int type) { return type == FP8G_F32 ? at::kFloat : at::kBFloat16; }
+
+PyObject* norm_residual(PyObject*, PyObject* const* a, Py_ssize_t n_) {
+  // x, residual, h, y, q, q_scales, pre_weight, post_norm, post_weight, gate, residual_scale, kind, eps, q_format
+  return guarded(n_, 14, [&] {
+    const at::Tensor& xt = tensor(a[0]);
+    const Matrix x(xt);
+    const int device = x.device, T = as_int(x.rows), n = as_int(x.cols), type = float_type(xt);
+    PyObject* any = a[1] != Py_None ? a[1] : a[2];
+    const int stream_type = any == Py_None ? FP8G_F32 : float_type(tensor(any));
+    const void* residual = nullptr;
+    int64_t r_ld = n, q_ld = T;
+    if (a[1] != Py_None) {
+      const Matrix r(tensor(a[1]));
+      if (r.rows != T || r.cols != n || r.device != device) throw Unusual();
+      residual = r.at, r_ld = r.ld;
+    }
+    void* h = dense_or_null(a[2], scalar(stream_type), {T, n}, device);
+    void* y = dense_or_null(a[3], scalar(type), {T, n}, device);
+    const int format = as_int(a[13]), post_norm = truth(a[7]), kind = as_int(a[11]);
+    uint8_t* q = a[4] == Py_None ? nullptr : codes(tensor(a[4]), format, {T, n}, device);
+    float* qs = q || a[4] != Py_None ? scales_mn(tensor(a[5]), groups_of(n), T, device, &q_ld) : nullptr;
+    const NormParams p(a[8], a[9], a[6], post_norm, T, n, device);
+    const float scale = as_float(a[10]), eps = as_float(a[12]);
+    void* s = stream_of(device);
+    return released([&] {
+      return fp8_norm_residual(x.at, type, x.ld, residual, r_ld, stream_type, T, n, kind, eps, post_norm, p.post,
+                               p.gate, p.gate_rows, scale, p.pre, p.type, h, y, q, format, qs, q_ld, s);
+    });
+  });
+}
+
+PyObject* norm_residual_backward(PyObject*, PyObject* const* a, Py_ssize_t n_) {
+  // grad_h, grad_y, x, h, grad_x, grad_residual, grad_pre_weight, grad_post_weight, grad_gate, pre_weight, post_norm,
+  // post_weight, gate, residual_scale, kind, eps, workspace
+  return guarded(n_, 17, [&] {
+    if (a[0] == Py_None || a[1] == Py_None || a[2] == Py_None || a[3] == Py_None || a[16] == Py_None) throw Unusual();
+    const at::Tensor &gh = tensor(a[0]), &xt = tensor(a[2]);
+    const Matrix x(xt);
+    const int device = x.device, T = as_int(x.rows), n = as_int(x.cols);
+    const int type = float_type(xt), stream_type = float_type(gh), post_norm = truth(a[10]), kind = as_int(a[14]);
+    const at::ScalarType xs = scalar(type), rs = scalar(stream_type);
+    const void *ghp = dense(gh, rs, {T, n}, device), *gyp = dense(a[1], xs, {T, n}, device);
+    const void* h = dense(a[3], rs, {T, n}, device);
+    void *gx = dense_or_null(a[4], xs, {T, n}, device), *gr = dense_or_null(a[5], rs, {T, n}, device);
+    auto* g_pre = static_cast<float*>(dense_or_null(a[6], at::kFloat, {n}, device));
+    auto* g_post = static_cast<float*>(dense_or_null(a[7], at::kFloat, {n}, device));
+    const NormParams p(a[11], a[12], a[9], post_norm, T, n, device);
+    if (a[8] != Py_None && a[12] == Py_None) throw Unusual();
+    auto* g_gate = a[8] == Py_None ? nullptr
+                                   : static_cast<float*>(dense(a[8], at::kFloat, tensor(a[12]).sizes(), device));
+    const float scale = as_float(a[13]), eps = as_float(a[15]);
+    const Workspace w(a[16], device);
+    void* s = stream_of(device);
+    return released([&] {
+      return fp8_norm_residual_backward(ghp, gyp, x.at, type, x.ld, h, stream_type, T, n, kind, eps, post_norm, p.post,
+                                        p.gate, p.gate_rows, scale, p.pre, p.type, gx, gr, g_pre, g_post, g_gate, w.at,
+                                        w.bytes, s);
+    });
+  });
+}
+
+PyObject* moe_few_tokens(PyObject*, PyObject* const* a, Py_ssize_t n_) {
+  // x, expert_idx, weights, up, up_scales, down, down_scales, out, activation, workspace
+  return guarded(n_, 10, [&] {
+    const at::Tensor &xt = tensor(a[0]), &i = tensor(a[1]), &d = tensor(a[5]);
+    const Matrix x(xt);
+    if (xt.scalar_type() != at::kBFloat16 || i.dim() != 2 || d.dim() != 3 || a[9] == Py_None) throw Unusual();
+    const int device = x.device, T = as_int(x.rows), hidden = as_int(x.cols), topk = as_int(i.size(1));
+    const int E = as_int(d.size(0)), inter = as_int(d.size(2)), activation = as_int(a[8]);
+    const auto* idx = static_cast<const int32_t*>(dense(i, at::kInt, {T, topk}, device));
+    const auto* weights = static_cast<const float*>(dense_or_null(a[2], at::kFloat, {T, topk}, device));
+    const int64_t kh = groups_of(hidden), ki = groups_of(inter);
+    const uint8_t* up = codes(tensor(a[3]), FP8G_E4M3, {E, 2 * int64_t(inter), hidden}, device);
+    const auto* us = static_cast<const float*>(dense(a[4], at::kFloat, {E, groups_of(2 * int64_t(inter)), kh}, device));
+    const uint8_t* down = codes(d, FP8G_E4M3, {E, hidden, inter}, device);
+    const auto* ds = static_cast<const float*>(dense(a[6], at::kFloat, {E, kh, ki}, device));
+    auto* out = static_cast<uint16_t*>(dense(a[7], at::kBFloat16, {T, hidden}, device));
+    const Workspace w(a[9], device);
+    void* s = stream_of(device);
+    return released([&] {
+      return fp8_moe_few_tokens(static_cast<const uint16_t*>(x.at), x.ld, idx, weights, T, topk, up, us, down, ds, E,
+                                hidden, inter, activation, out, w.at, w.bytes, s);
+    });
+  });
+}
+
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2) {
     PyErr_SetString(PyExc_TypeError, "setup(current_device, raw_stream)");
@@ -282,6 +470,11 @@ PyMethodDef g_methods[] = {FP8G_DIRECT(setup),
                            FP8G_DIRECT(moe_combine_backward),
                            FP8G_DIRECT(w4_matvec),
                            FP8G_DIRECT(w4_matvec_experts),
+                           FP8G_DIRECT(gemm_nt_epilogue),
+                           FP8G_DIRECT(epilogue_backward),
+                           FP8G_DIRECT(norm_residual),
+                           FP8G_DIRECT(norm_residual_backward),
+                           FP8G_DIRECT(moe_few_tokens),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_direct", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

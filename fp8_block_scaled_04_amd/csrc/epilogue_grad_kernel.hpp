@@ -23,7 +23,9 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, col = blockIdx.x * kEpilogueColumns + 8 * tx;
   const int first = blockIdx.y * rows_per_slice, last = min(m, first + rows_per_slice);
   float acc[8] = {};
-  if (col < n) {
+  if (col < n)
+    by_activation(activation, [&](auto tag) __attribute__((always_inline)) {
+    constexpr int ACT = decltype(tag)::value;
     for (int r = first + ty; r < last; r += 8 * AHEAD) {
       uint4 g[AHEAD], z[AHEAD];
 #pragma unroll
@@ -40,13 +42,13 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
         unpack_bf16x8(z[u], b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          a[i] *= activate_grad(activation, b[i]);
+          a[i] *= activate_grad<ACT>(b[i]);
           acc[i] += a[i];
         }
         *reinterpret_cast<uint4*>(grad_preact + int64_t(r + 8 * u) * n + col) = pack_bf16x8(a);
       }
     }
-  }
+    });
   if (!partial) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sums[ty][8 * tx + i] = acc[i];
@@ -60,23 +62,31 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
 }
 
 // out[y][c] = sum over s < slices of partial[s][y][c] (rows of n, `sets` = gridDim.y of them side by side): 16 runs of
-// slices per column, each in order, then the runs.  Grid: x column blocks of 16, y sets.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, int slices, int n, float* out0,
-                                                          float* out1, float* out2) {
-  __shared__ float sums[16][17];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = blockIdx.x * 16 + tx, sets = gridDim.y;
-  const int per = (slices + 15) / 16, s0 = ty * per, s1 = min(slices, s0 + per);
+// slices per column, each in order, then the runs.  Grid: x column blocks of 64, y sets.
+constexpr int kSumRuns = 16;
+__global__ void __launch_bounds__(64 * kSumRuns) column_sums_kernel(const float* partial, int slices, int n,
+                                                                    float* out0, float* out1, float* out2) {
+  constexpr int AHEAD = 8;
+  __shared__ float sums[kSumRuns][64];
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx, sets = gridDim.y;
+  const int per = (slices + kSumRuns - 1) / kSumRuns, s0 = ty * per, s1 = min(slices, s0 + per);
   float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
   if (!out) return;
   float v = 0.f;
   if (c < n)
-    for (int s = s0; s < s1; ++s) v += partial[(int64_t(s) * sets + blockIdx.y) * n + c];
+    for (int s = s0; s < s1; s += AHEAD) {
+      float t[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) t[u] = partial[(int64_t(min(s + u, s1 - 1)) * sets + blockIdx.y) * n + c];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) v += s + u < s1 ? t[u] : 0.f;
+    }
   sums[ty][tx] = v;
   __syncthreads();
   if (ty != 0 || c >= n) return;
   v = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v += sums[i][tx];
+  for (int i = 0; i < kSumRuns; ++i) v += sums[i][tx];
   out[c] = v;
 }
 

@@ -98,6 +98,8 @@ struct Epilogue {
       __syncthreads();
       if (!in) continue;
       const int64_t at0 = int64_t(m0 + first) * shape_n + col;
+      by_activation(p.activation, [&](auto tag) __attribute__((always_inline)) {
+      constexpr int ACT = decltype(tag)::value;
       for (int r = r0; r < last; r += AHEAD * step) {
         uint4 res[AHEAD] = {};
         if (p.residual) {
@@ -118,10 +120,11 @@ struct Epilogue {
           if (p.preact) *reinterpret_cast<uint4*>(p.preact + at) = pack_bf16x8(z);
           unpack_bf16x8(res[u], y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] += activate(p.activation, z[i]);
+          for (int i = 0; i < 8; ++i) y[i] += activate<ACT>(z[i]);
           *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(y);
         }
       }
+      });
     }
   }
 };

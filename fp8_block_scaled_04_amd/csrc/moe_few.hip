@@ -15,20 +15,43 @@ namespace {
 using fp8g::MoeFewArgs;
 using namespace fp8g::host;
 
-constexpr int kMaxTopk = 32, kMaxExperts = 65535, kMaxWidth = 65536;
+constexpr int kMaxTopk = fp8g::kFewMaxTopk, kMaxExperts = 65535, kMaxWidth = 65536;
 
 // Tokens that one pair of launches takes.
 int chunk_tokens(int topk) { return std::min(fp8g::kFewTokens, fp8g::kFewMaxPairs / topk); }
 
+template <int TX, int R>
+int launch_down(const MoeFewArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((fp8g::moe_few_down_kernel<TX, R>), dim3(unsigned(a.hidden / (16 * R))),
+                     dim3(fp8g::kFewDownWaves * fp8g::kWave), 0, s, a);
+  return launched("moe few down");
+}
+
+template <int TX, typename Plan>
+int launch_up(const MoeFewArgs& a, int64_t tiles, hipStream_t s) {
+  const int64_t units = tiles * (a.inter / fp8g::kFewGroup);
+  const int64_t grid = std::min<int64_t>(units, int64_t(device_cus()) * (TX == 4 ? 2 : 1));
+  hipLaunchKernelGGL((fp8g::moe_few_up_kernel<TX, Plan>), dim3(unsigned(grid)),
+                     dim3(fp8g::kFewUpWaves * fp8g::kWave), 0, s, a);
+  return launched("moe few up");
+}
+
+// Up to TX tokens.
 template <int TX>
+int launch_tokens(const MoeFewArgs& a, hipStream_t s) {
+  const int64_t tiles = std::min(a.tokens * a.topk, a.experts);
+  if (const int st = launch_up<TX, fp8g::FewTokenPlan<TX>>(a, tiles, s)) return st;
+  return a.hidden / 16 <= device_cus() ? launch_down<TX, 1>(a, s) : launch_down<TX, 2>(a, s);
+}
+
 int launch(const MoeFewArgs& a, hipStream_t s) {
-  const int64_t pairs = int64_t(a.tokens) * a.topk;
-  const int64_t tiles = std::min<int64_t>(pairs, a.experts + pairs / TX), units = tiles * (a.inter / 16);
-  const int64_t grid = std::min<int64_t>(units, int64_t(device_cus()) * (TX == 16 ? 1 : 2));
-  hipLaunchKernelGGL((fp8g::moe_few_up_kernel<TX>), dim3(unsigned(grid)), dim3(fp8g::kFewThreads), 0, s, a);
-  if (const int st = launched("moe few up")) return st;
-  hipLaunchKernelGGL((fp8g::moe_few_down_kernel<TX>), dim3(unsigned(a.hidden / fp8g::kFewRows)),
-                     dim3(fp8g::kFewThreads), 0, s, a);
+  if (a.tokens <= 4) return launch_tokens<4>(a, s);
+  if (a.tokens <= 8) return launch_tokens<8>(a, s);
+  if (a.tokens <= 16) return launch_tokens<16>(a, s);
+  const int pairs = a.tokens * a.topk;
+  if (const int st = launch_up<16, fp8g::FewPairPlan<16>>(a, std::min(pairs, a.experts + pairs / 16), s)) return st;
+  hipLaunchKernelGGL(fp8g::moe_few_down_pairs_kernel<16>, dim3(unsigned(a.hidden / 32)),
+                     dim3(fp8g::FewDownPairs<16>::kWaves * fp8g::kWave), 0, s, a);
   return launched("moe few down");
 }
 
@@ -38,7 +61,8 @@ extern "C" {
 
 size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int inter) {
   if (num_tokens <= 0 || topk <= 0 || topk > kMaxTopk || inter <= 0) return 0;
-  return size_t(std::min(num_tokens, chunk_tokens(topk))) * size_t(topk) * size_t(inter) * sizeof(uint16_t);
+  const size_t values = size_t(std::min(num_tokens, chunk_tokens(topk))) * size_t(topk) * size_t(inter);
+  return values * sizeof(uint16_t) + values / fp8g::kFewGroup;
 }
 
 int fp8_moe_few_tokens(const uint16_t* x, int64_t x_ld, const int32_t* expert_idx, const float* weights,
@@ -64,11 +88,13 @@ int fp8_moe_few_tokens(const uint16_t* x, int64_t x_ld, const int32_t* expert_id
     a.expert_idx = expert_idx + int64_t(t) * topk;
     a.weights = weights ? weights + int64_t(t) * topk : nullptr;
     a.up = up; a.up_scales = up_scales; a.down = down; a.down_scales = down_scales;
-    a.mid = static_cast<uint16_t*>(workspace); a.out = out + int64_t(t) * hidden;
+    a.mid = static_cast<uint16_t*>(workspace);
+    a.exponents = reinterpret_cast<int8_t*>(a.mid + size_t(std::min(step, num_tokens)) * topk * inter);
+    a.out = out + int64_t(t) * hidden;
     a.tokens = std::min(step, num_tokens - t); a.topk = topk; a.experts = num_experts;
     a.hidden = hidden; a.inter = inter; a.activation = activation;
     auto s = static_cast<hipStream_t>(stream);
-    if (const int st = a.tokens <= 4 ? launch<4>(a, s) : launch<16>(a, s)) return st;
+    if (const int st = launch(a, s)) return st;
   }
   return FP8G_OK;
 }

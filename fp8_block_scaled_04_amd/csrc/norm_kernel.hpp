@@ -97,10 +97,11 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Sums of up to two values over the `waves` waves of a row (one wave: no barrier).  `part`: a place of LDS of its own.
+// Sums of up to four values over the `waves` waves of a row (one wave: no barrier).  `part`: a place of LDS that no
+// other call uses until every wave has passed another barrier.
 constexpr int kNormMaxWaves = 16;
 struct NormPart {
-  float v[2][kNormMaxWaves];
+  float v[4][kNormMaxWaves];
 };
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], int waves, NormPart& part) {
@@ -240,10 +241,12 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 }
 
 // Grid: slices of rows, which a workgroup takes one after the other, each thread with its C pieces of 8 columns, whose
-// sums over the rows stay in its registers.
+// sums over the rows stay in its registers.  The next row is read while this one is worked on.  What a row needs of
+// itself takes two rounds of sums (three for layer norms, whose squares are of centred values):
+//   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
 template <typename X, typename R, bool LAYER, int C, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
-  __shared__ NormPart parts[4];
+  __shared__ NormPart parts[2][3];
   const int waves = blockDim.x >> 6, n = a.n;
   const float inv_n = 1.f / n;
   int col[C];
@@ -255,13 +258,12 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
   }
   float s_pre[C][8] = {}, s_post[C][8] = {}, s_gate[C][8] = {};
   const int first = blockIdx.x * a.rows_per_slice, last = min(a.rows, first + a.rows_per_slice);
-  for (int row = first; row < last; ++row) {
+  Raw8<X> xs[C], gys[C];
+  Raw8<R> hs[C], ghs[C];
+  auto load = [&](int row) {
     const int64_t at0 = int64_t(row) * n;
-    Raw8<X> xs[C], gys[C];
-    Raw8<R> hs[C], ghs[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      xs[c].clear(), gys[c].clear(), hs[c].clear(), ghs[c].clear();
       if (!in[c]) continue;
       if (a.x) xs[c].load(a.x, row * a.x_ld + col[c]);
       if (a.grad_y) {
@@ -270,69 +272,87 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       }
       if (a.grad_h) ghs[c].load(a.grad_h, at0 + col[c]);
     }
-    float d[C][8];
+  };
 #pragma unroll
-    for (int c = 0; c < C; ++c) ghs[c].get(d[c]);
-    if (a.grad_y) {
-      float v[C][8], m[2] = {0.f, 0.f};
+  for (int c = 0; c < C; ++c) xs[c].clear(), gys[c].clear(), hs[c].clear(), ghs[c].clear();
+  if (first < last) load(first);
+  for (int row = first; row < last; ++row) {
+    const int64_t at0 = int64_t(row) * n;
+    NormPart* part = parts[row & 1];
+    float x[C][8], h[C][8], gy[C][8], d[C][8];
 #pragma unroll
-      for (int c = 0; c < C; ++c) hs[c].get(v[c]);
-      const float r = normalise<LAYER>(v, in, n, a.eps, waves, parts);
+    for (int c = 0; c < C; ++c) xs[c].get(x[c]), hs[c].get(h[c]), gys[c].get(gy[c]), ghs[c].get(d[c]);
+    if (row + 1 < last) load(row + 1);
+    if constexpr (LAYER) {
+      float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float g[8], w[8];
-        gys[c].get(g);
-        if (in[c]) param8(a.pre_weight, a.params_bf16, col[c], w);
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[0] += h[c][i], m[1] += x[c][i];
+      row_sums(m, waves, part[0]);
+      if (!a.post_norm) m[1] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float b = in[c] ? g[i] * w[i] : 0.f;
-          m[0] = fmaf(b, v[c][i], m[0]);
-          m[1] += b;
+          h[c][i] = in[c] ? fmaf(-inv_n, m[0], h[c][i]) : 0.f;
+          x[c][i] = in[c] ? fmaf(-inv_n, m[1], x[c][i]) : 0.f;
         }
-      }
-      row_sums(m, waves, parts[2]);
-      m[0] *= inv_n;
-      m[1] = LAYER ? m[1] * inv_n : 0.f;
+    }
+    float m[4] = {0.f, 0.f, 0.f, 0.f};  // of h^2, x^2, a h, a
+    float rx = 1.f;
+    if (a.grad_y || a.post_norm) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float g[8], w[8];
-        gys[c].get(g);
         if (!in[c]) continue;
+        float w[8];
         param8(a.pre_weight, a.params_bf16, col[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s_pre[c][i] = fmaf(g[i], v[c][i], s_pre[c][i]);
-          d[c][i] = fmaf(r, fmaf(-m[0], v[c][i], g[i] * w[i]) - m[1], d[c][i]);
+          const float b = gy[c][i] * w[i];
+          m[0] = fmaf(h[c][i], h[c][i], m[0]);
+          m[1] = fmaf(x[c][i], x[c][i], m[1]);
+          m[2] = fmaf(b, h[c][i], m[2]);
+          m[3] += b;
         }
       }
+      row_sums(m, waves, part[1]);
+      if (a.post_norm) rx = 1.f / sqrtf(fmaf(m[1], inv_n, a.eps));
     }
-    if (a.grad_residual) {
+    if (a.grad_y) {
+      const float r = 1.f / sqrtf(fmaf(m[0], inv_n, a.eps));
+      const float along = m[2] * inv_n * r * r, mean = LAYER ? m[3] * inv_n : 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (!in[c]) continue;
+        float w[8];
+        param8(a.pre_weight, a.params_bf16, col[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s_pre[c][i] = fmaf(gy[c][i], h[c][i] * r, s_pre[c][i]);
+          d[c][i] = fmaf(r, fmaf(-along, h[c][i], gy[c][i] * w[i]) - mean, d[c][i]);
+        }
+      }
+    }
+    float b[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x; x becomes norm(x)
+      if (!in[c]) continue;
+      if (a.grad_residual) {
         float g[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = a.residual_scale * d[c][i];
         store8<R>(a.grad_residual, at0 + col[c], g);
       }
-    }
-    float v[C][8];
+      float w[8];
+      param8(a.post_norm ? a.post_weight : nullptr, a.params_bf16, col[c], w);
 #pragma unroll
-    for (int c = 0; c < C; ++c) xs[c].get(v[c]);
-    const float r = a.post_norm ? normalise<LAYER>(v, in, n, a.eps, waves, parts) : 1.f;
-    float m[2] = {0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x
-      if (!in[c]) continue;
-      float w[8], g[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-      if (a.post_norm) param8(a.post_weight, a.params_bf16, col[c], w);
+      for (int i = 0; i < 8; ++i) x[c][i] *= rx;
       if (a.gate) {
-        float u[8];
+        float u[8], g[8];
         param8(a.gate, a.params_bf16, (a.gate_per_row ? at0 : 0) + col[c], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (v[c][i] * w[i]);
+        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (x[c][i] * w[i]);
         if (a.gate_per_row) {
           if (a.grad_gate) store8<float>(a.grad_gate, at0 + col[c], u);
         } else {
@@ -345,21 +365,20 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       if (a.post_norm) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s_post[c][i] = fmaf(d[c][i], v[c][i], s_post[c][i]);
+          s_post[c][i] = fmaf(d[c][i], x[c][i], s_post[c][i]);
           d[c][i] *= w[i];
-          m[0] = fmaf(d[c][i], v[c][i], m[0]);
-          m[1] += d[c][i];
+          b[0] = fmaf(d[c][i], x[c][i], b[0]);
+          b[1] += d[c][i];
         }
       }
     }
     if (a.post_norm) {
-      row_sums(m, waves, parts[3]);
-      m[0] *= inv_n;
-      m[1] = LAYER ? m[1] * inv_n : 0.f;
+      row_sums(b, waves, part[2]);
+      const float along = b[0] * inv_n, mean = LAYER ? b[1] * inv_n : 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] = r * (fmaf(-m[0], v[c][i], d[c][i]) - m[1]);
+        for (int i = 0; i < 8; ++i) d[c][i] = rx * (fmaf(-along, x[c][i], d[c][i]) - mean);
     }
     if (a.grad_x) {
 #pragma unroll
