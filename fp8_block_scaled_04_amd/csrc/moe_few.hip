@@ -15,44 +15,47 @@ namespace {
 using fp8g::MoeFewArgs;
 using namespace fp8g::host;
 
-constexpr int kMaxTopk = fp8g::kFewMaxTopk, kMaxExperts = 65535, kMaxWidth = 65536;
+constexpr int kMaxTopk = fp8g::kFewMaxTopk, kMaxExperts = fp8g::kFewMaxExperts, kMaxWidth = 65536;
 
 // Tokens that one pair of launches takes.
 int chunk_tokens(int topk) { return std::min(fp8g::kFewTokens, fp8g::kFewMaxPairs / topk); }
 
-template <int TX, int R>
+template <int TX, int R, int WAVES, typename Plan>
 int launch_down(const MoeFewArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((fp8g::moe_few_down_kernel<TX, R>), dim3(unsigned(a.hidden / (16 * R))),
-                     dim3(fp8g::kFewDownWaves * fp8g::kWave), 0, s, a);
+  hipLaunchKernelGGL((fp8g::moe_few_down_kernel<TX, R, WAVES, Plan>), dim3(unsigned(a.hidden / (16 * R))),
+                     dim3(WAVES * fp8g::kWave), 0, s, a);
   return launched("moe few down");
 }
 
-template <int TX, typename Plan>
-int launch_up(const MoeFewArgs& a, int64_t tiles, hipStream_t s) {
+template <int TX, typename Plan, int DOWN2_WAVES>
+int launch_both(const MoeFewArgs& a, int64_t tiles, hipStream_t s) {
   const int64_t units = tiles * (a.inter / fp8g::kFewGroup);
-  const int64_t grid = std::min<int64_t>(units, int64_t(device_cus()) * (TX == 4 ? 2 : 1));
+  const int64_t grid = std::min<int64_t>(units, int64_t(device_cus()) * fp8g::few_up_per_cu(TX));
   hipLaunchKernelGGL((fp8g::moe_few_up_kernel<TX, Plan>), dim3(unsigned(grid)),
                      dim3(fp8g::kFewUpWaves * fp8g::kWave), 0, s, a);
-  return launched("moe few up");
+  if (const int st = launched("moe few up")) return st;
+  return a.hidden / 16 <= device_cus() ? launch_down<TX, 1, 8, Plan>(a, s) : launch_down<TX, 2, DOWN2_WAVES, Plan>(a, s);
 }
 
-// Up to TX tokens.
 template <int TX>
 int launch_tokens(const MoeFewArgs& a, hipStream_t s) {
-  const int64_t tiles = std::min(a.tokens * a.topk, a.experts);
-  if (const int st = launch_up<TX, fp8g::FewTokenPlan<TX>>(a, tiles, s)) return st;
-  return a.hidden / 16 <= device_cus() ? launch_down<TX, 1>(a, s) : launch_down<TX, 2>(a, s);
+  return launch_both<TX, fp8g::FewTokenPlan<TX>, 8>(a, std::min(a.tokens * a.topk, a.experts), s);
+}
+
+template <int TX>
+int launch_pairs(const MoeFewArgs& a, hipStream_t s) {
+  const int pairs = a.tokens * a.topk;
+  return launch_both<TX, fp8g::FewPairPlan<TX>, 4>(a, std::min(pairs, a.experts + pairs / TX), s);
 }
 
 int launch(const MoeFewArgs& a, hipStream_t s) {
+  if (a.tokens == 1) return launch_tokens<1>(a, s);
+  if (a.tokens == 2) return launch_tokens<2>(a, s);
   if (a.tokens <= 4) return launch_tokens<4>(a, s);
-  if (a.tokens <= 8) return launch_tokens<8>(a, s);
-  if (a.tokens <= 16) return launch_tokens<16>(a, s);
   const int pairs = a.tokens * a.topk;
-  if (const int st = launch_up<16, fp8g::FewPairPlan<16>>(a, std::min(pairs, a.experts + pairs / 16), s)) return st;
-  hipLaunchKernelGGL(fp8g::moe_few_down_pairs_kernel<16>, dim3(unsigned(a.hidden / 32)),
-                     dim3(fp8g::FewDownPairs<16>::kWaves * fp8g::kWave), 0, s, a);
-  return launched("moe few down");
+  if (pairs <= 2 * a.experts) return launch_pairs<4>(a, s);
+  if (pairs <= 6 * a.experts) return launch_pairs<8>(a, s);
+  return launch_pairs<16>(a, s);
 }
 
 }  // namespace

@@ -26,6 +26,8 @@
 // What bounds it: the matrices are read once, a byte a weight.
 #pragma once
 
+#include <type_traits>
+
 #include "activation.hpp"
 #include "gemm_kernel.hpp"  // the operand tiles' layout
 
@@ -34,6 +36,7 @@ namespace fp8g {
 constexpr int kFewTokens = 64;  // of a launch, at most
 constexpr int kFewMaxPairs = 1024;
 constexpr int kFewMaxTopk = 32;
+constexpr int kFewMaxExperts = 4096;  // a table of them takes the rings' place in LDS
 constexpr int kFewGroup = 16;  // columns of mid that share an exponent
 
 struct MoeFewArgs {
@@ -92,12 +95,12 @@ __device__ __forceinline__ void few_copy4(const void* src, uint32_t lds) {
 }
 
 // ---- which expert has which tokens ----------------------------------------------
-// Pairs whose index is no expert's are in no plan.
+// A pair whose index is no expert's is in no plan, and of a token's pairs with
+// one expert only the first, which has the sum of their weights.
 //
 // For up to TX tokens: a tile is one expert, in the order of the first pairs,
 // and its column t is token t.  pair[tile][t]: the pair, or kFewNone where the
-// token has not picked the expert.  A token that names an expert twice has the
-// first of those pairs there, with the sum of their weights.
+// token has not picked the expert.
 constexpr unsigned kFewNone = 0xffff;
 template <int TX>
 struct FewTokenPlan {
@@ -108,179 +111,194 @@ struct FewTokenPlan {
   int tiles;
 };
 
-// For any number of tokens: tiles of up to TX pairs of one expert, which follow
-// one another; tiles in the order of their first pairs.
+// For any number of tokens: a tile is up to TX pairs of one expert; an expert's
+// tiles follow one another, the experts in the order of their first pairs, and
+// an expert's pairs go to its tiles in order.  (Which column of its tile a pair
+// has may change from run to run; nothing that is computed depends on it.)
 template <int TX>
 struct FewPairPlan {
   static constexpr int kPairs = kFewMaxPairs;
-  uint16_t pair[kPairs];       // by tile, in a tile in order
+  uint16_t pair[kPairs];       // by tile
   uint16_t start[kPairs + 1];  // tile t's pairs are pair[start[t]] .. pair[start[t + 1] - 1]
   uint16_t expert[kPairs];
+  uint16_t first[kPairs], number[kPairs];  // the first of its expert's tiles, and how many there are
+  float weight[kPairs];
   int tiles;
 };
 
 constexpr int kFewMaxWaves = 8;
 template <int PAIRS>
 struct FewPlanScratch {
-  __attribute__((aligned(16))) int expert[PAIRS];
-  int count[PAIRS];
+  __attribute__((aligned(16))) int first[kFewMaxExperts];  // an expert's first pair
+  int count[kFewMaxExperts];  // and its pairs; then where its tile, or its first pair, is
+  int expert[PAIRS];
   int sums[kFewMaxWaves];
 };
 
-// The pairs' experts (-1: none), and four more.
-template <int PAIRS>
-__device__ __forceinline__ void few_load_experts(const MoeFewArgs& a, int pairs, FewPlanScratch<PAIRS>& s) {
-  const int padded = (pairs + 3) & ~3;
-  for (int p = threadIdx.x; p < padded; p += blockDim.x) {
-    const int e = p < pairs ? a.expert_idx[p] : -1;
+// What a plan begins with: the table of the experts; for every pair p = j THREADS + tid its expert (-1: it is in no
+// plan), its place among the expert's, and in plan.weight its weight.
+template <int WAVES, int ROUNDS, typename Plan>
+__device__ __forceinline__ void few_count(const MoeFewArgs& a, Plan& plan, FewPlanScratch<Plan::kPairs>& s,
+                                          int (&mine)[ROUNDS], int (&rank)[ROUNDS]) {
+  constexpr int THREADS = WAVES * kWave;
+  const int tid = threadIdx.x, pairs = a.tokens * a.topk;
+  for (int p = tid; p < pairs; p += THREADS) {
+    const int e = a.expert_idx[p];
+    const float w = a.weights ? a.weights[p] : 1.f;
     s.expert[p] = e >= 0 && e < a.experts ? e : -1;
-    s.count[p] = 0;
+    plan.weight[p] = w;
   }
+  for (int e = tid; e < a.experts; e += THREADS) s.first[e] = INT32_MAX, s.count[e] = 0;
+  __syncthreads();
+  float sum[ROUNDS];
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {
+    const int p = j * THREADS + tid;
+    mine[j] = -1, rank[j] = 0, sum[j] = 0.f;
+    if (p >= pairs) continue;
+    mine[j] = s.expert[p];
+    const int from = p / a.topk * a.topk;
+    bool again = false;
+    sum[j] = plan.weight[p];
+    for (int q = from; q < from + a.topk; ++q) {
+      const bool same = s.expert[q] == mine[j];
+      again |= same && q < p;
+      sum[j] += same && q > p ? plan.weight[q] : 0.f;
+    }
+    if (again) mine[j] = -1;
+    if (mine[j] < 0) continue;
+    atomicMin(&s.first[mine[j]], p);
+    rank[j] = atomicAdd(&s.count[mine[j]], 1);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j)
+    if (mine[j] >= 0) plan.weight[j * THREADS + tid] = sum[j];
 }
 
-// f(q, same) for the pairs q before p, and some after it in the same wave: whether q's expert is `mine`.
-template <int PAIRS, typename F>
-__device__ __forceinline__ void few_pairs_before(const FewPlanScratch<PAIRS>& s, int p, int mine, int pairs, F&& f) {
-  const int end = min(pairs, uniform(p) + kWave);  // the wave's last pair
-  for (int q0 = 0; q0 < end; q0 += 4) {
-    const v4i e = *reinterpret_cast<const v4i*>(s.expert + q0);
+// Sums of v over the lanes and waves before this one, and (`all` added to) over all.
+template <int WAVES>
+__device__ __forceinline__ int few_sum_before(int v, int& all, int (&sums)[kFewMaxWaves]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
+  int upto = v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f(q0 + i, e[i] == mine && q0 + i < p);
+  for (int d = 1; d < kWave; d *= 2) {
+    const int o = __shfl_up(upto, d, kWave);
+    upto += lane >= d ? o : 0;
   }
+  if (lane == kWave - 1) sums[wave] = upto;
+  __syncthreads();
+  int before = all + upto - v;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    before += w < wave ? sums[w] : 0;
+    all += sums[w];
+  }
+  __syncthreads();
+  return before;
 }
 
 template <int TX, int WAVES>
 __device__ __forceinline__ void few_plan(const MoeFewArgs& a, FewTokenPlan<TX>& plan,
                                          FewPlanScratch<FewTokenPlan<TX>::kPairs>& s) {
-  constexpr int THREADS = WAVES * kWave, ROUNDS = (FewTokenPlan<TX>::kPairs + THREADS - 1) / THREADS;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), pairs = a.tokens * a.topk;
-  for (int p = tid; p < pairs; p += THREADS) plan.weight[p] = a.weights ? a.weights[p] : 1.f;
-  few_load_experts(a, pairs, s);
-  for (int i = tid; i < pairs * (TX / 2); i += THREADS) reinterpret_cast<uint32_t*>(plan.pair)[i] = ~0u;
+  static_assert(FewTokenPlan<TX>::kPairs <= WAVES * kWave, "a thread for every pair");
+  const int p = threadIdx.x, pairs = a.tokens * a.topk;
+  for (int i = p; i < pairs * TX; i += WAVES * kWave) plan.pair[i / TX][i % TX] = uint16_t(kFewNone);
+  int mine[1], rank[1], tiles = 0;
+  few_count<WAVES>(a, plan, s, mine, rank);
+  const bool head = mine[0] >= 0 && s.first[mine[0]] == p;
+  const int at = few_sum_before<WAVES>(head, tiles, s.sums);
+  if (head) {
+    s.count[mine[0]] = at;
+    plan.expert[at] = uint16_t(mine[0]);
+  }
+  if (p == 0) plan.tiles = tiles;
   __syncthreads();
-  int head[ROUNDS], mine[ROUNDS], tiles = 0;
-  float sum[ROUNDS];
-  bool again[ROUNDS];
-#pragma unroll
-  for (int j = 0; j < ROUNDS; ++j) {
-    const int p = j * THREADS + tid;
-    head[j] = p, mine[j] = -1, again[j] = false, sum[j] = 0.f;
-    if (j * THREADS >= pairs) continue;
-    mine[j] = p < pairs ? s.expert[p] : -1;
-    const int token = p / a.topk, from = token * a.topk;
-    few_pairs_before(s, p, mine[j], pairs, [&](int q, bool same) {
-      head[j] = same && head[j] == p ? q : head[j];
-      again[j] |= same && q >= from;
-    });
-    if (mine[j] >= 0 && !again[j]) {
-      sum[j] = plan.weight[p];
-      for (int q = p + 1; q < from + a.topk; ++q) sum[j] += s.expert[q] == mine[j] ? plan.weight[q] : 0.f;
-    }
-    // the tile of a pair that begins one: how many begin before
-    const uint64_t first = __ballot(mine[j] >= 0 && head[j] == p);
-    if (lane == 0) s.sums[wave] = __popcll(first);
-    __syncthreads();
-    int at = tiles + __popcll(first & ((uint64_t(1) << lane) - 1));
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      at += w < wave ? s.sums[w] : 0;
-      tiles += s.sums[w];
-    }
-    if (mine[j] >= 0 && head[j] == p) {
-      s.count[p] = at;
-      plan.expert[at] = uint16_t(mine[j]);
-    }
-    __syncthreads();
-  }
-  if (tid == 0) plan.tiles = tiles;
-#pragma unroll
-  for (int j = 0; j < ROUNDS; ++j) {
-    const int p = j * THREADS + tid;
-    if (mine[j] < 0 || again[j]) continue;
-    plan.pair[s.count[head[j]]][p / a.topk] = uint16_t(p);
-    plan.weight[p] = sum[j];
-  }
+  if (mine[0] >= 0) plan.pair[s.count[mine[0]]][p / a.topk] = uint16_t(p);
   __syncthreads();
 }
 
-// Every pair finds its rank among its expert's and the pair that begins its
-// tile; a scan over the tiles' first pairs then places the tiles.
 template <int TX, int WAVES>
 __device__ __forceinline__ void few_plan(const MoeFewArgs& a, FewPairPlan<TX>& plan,
                                          FewPlanScratch<FewPairPlan<TX>::kPairs>& s) {
-  constexpr int THREADS = WAVES * kWave, ROUNDS = (FewPairPlan<TX>::kPairs + THREADS - 1) / THREADS;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6), pairs = a.tokens * a.topk;
-  few_load_experts(a, pairs, s);
-  __syncthreads();
-  int rank[ROUNDS], head[ROUNDS], mine[ROUNDS];
+  constexpr int THREADS = WAVES * kWave, ROUNDS = FewPairPlan<TX>::kPairs / THREADS;
+  const int tid = threadIdx.x, pairs = a.tokens * a.topk;
+  int mine[ROUNDS], rank[ROUNDS], heads[ROUNDS] = {}, all = 0;  // tiles << 16 | pairs
+  few_count<WAVES>(a, plan, s, mine, rank);
 #pragma unroll
   for (int j = 0; j < ROUNDS; ++j) {
-    const int p = j * THREADS + tid;
-    rank[j] = 0, head[j] = p, mine[j] = -1;
     if (j * THREADS >= pairs) continue;
-    mine[j] = p < pairs ? s.expert[p] : -1;
-    few_pairs_before(s, p, mine[j], pairs, [&](int q, bool same) {
-      head[j] = same && rank[j] % TX == 0 ? q : head[j];
-      rank[j] += same;
-    });
-    if (rank[j] % TX == 0) head[j] = p;
-    if (mine[j] >= 0) atomicAdd(&s.count[head[j]], 1);
-  }
-  __syncthreads();
-  int before = 0;  // tiles << 16 | pairs of the rounds before
-#pragma unroll
-  for (int j = 0; j < ROUNDS; ++j) {
-    const int p = j * THREADS + tid;
-    if (j * THREADS >= pairs) continue;
-    const bool first = mine[j] >= 0 && head[j] == p;
-    const int own = first ? 1 << 16 | s.count[p] : 0;
-    int upto = own;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-      const int v = __shfl_up(upto, d, kWave);
-      upto += lane >= d ? v : 0;
+    const bool head = mine[j] >= 0 && s.first[mine[j]] == j * THREADS + tid;
+    const int count = head ? s.count[mine[j]] : 0, number = (count + TX - 1) / TX;
+    const int at = few_sum_before<WAVES>(number << 16 | count, all, s.sums), tile = at >> 16, pos = at & 0xffff;
+    for (int i = 0; i < number; ++i) {
+      plan.start[tile + i] = uint16_t(pos + i * TX);
+      plan.expert[tile + i] = uint16_t(mine[j]);
+      plan.first[tile + i] = uint16_t(tile);
+      plan.number[tile + i] = uint16_t(number);
     }
-    if (lane == kWave - 1) s.sums[wave] = upto;
-    __syncthreads();
-    int at = before + upto - own;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      at += w < wave ? s.sums[w] : 0;
-      before += s.sums[w];
-    }
-    if (first) {
-      plan.start[at >> 16] = uint16_t(at & 0xffff);
-      plan.expert[at >> 16] = uint16_t(mine[j]);
-      s.count[p] = at & 0xffff;
-    }
-    __syncthreads();
+    if (head) s.count[mine[j]] = pos, heads[j] = count;
   }
   if (tid == 0) {
-    plan.tiles = before >> 16;
-    plan.start[before >> 16] = uint16_t(before & 0xffff);
+    plan.tiles = all >> 16;
+    plan.start[all >> 16] = uint16_t(all & 0xffff);
   }
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < ROUNDS; ++j)
-    if (mine[j] >= 0) plan.pair[s.count[head[j]] + rank[j] % TX] = uint16_t(j * THREADS + tid);
+  for (int j = 0; j < ROUNDS; ++j) {
+    if (mine[j] >= 0) s.expert[s.count[mine[j]] + rank[j]] = j * THREADS + tid;  // the pairs by expert, in any order
+    if (heads[j]) s.first[mine[j]] = heads[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ROUNDS; ++j) {
+    if (mine[j] < 0) continue;
+    const int pos = s.count[mine[j]], count = s.first[mine[j]], p = j * THREADS + tid;
+    if (count > TX) {  // by tile: in order
+      rank[j] = 0;
+      for (int i = 0; i < count; ++i) rank[j] += s.expert[pos + i] < p;
+    }
+    plan.pair[pos + rank[j]] = uint16_t(p);
+  }
   __syncthreads();
 }
 
-// What the kernels ask a plan: the row of x or mid of column t of a tile (of a
-// column without a pair: some other's), and its pair (kFewNone: none).
+// What the kernels ask a plan: the pair of column t of a tile (kFewNone: none) and, for a column that has none, a pair
+// to read in its place; the row of x for column t; and the tile and row set of a unit, the tiles of one expert next to
+// one another (the second then finds the rows in the cache).
 template <int TX>
 __device__ __forceinline__ unsigned few_pair(const FewTokenPlan<TX>& p, int tile, int t) { return p.pair[tile][t]; }
 template <int TX>
-__device__ __forceinline__ unsigned few_pair(const FewPairPlan<TX>& p, int tile, int t) {
-  const int at = p.start[tile] + t;
-  return at < p.start[tile + 1] ? p.pair[at] : kFewNone;
+__device__ __forceinline__ unsigned few_any_pair(const FewTokenPlan<TX>& p, int tile, int t) {
+  unsigned pair = p.pair[tile][t];
+  for (int i = 0; pair == kFewNone; ++i) pair = p.pair[tile][i];  // (a tile has one)
+  return pair;
 }
 template <int TX>
 __device__ __forceinline__ const uint16_t* few_x(const MoeFewArgs& a, const FewTokenPlan<TX>&, int, int t) {
   return a.x + min(t, a.tokens - 1) * a.x_ld;
 }
 template <int TX>
+__device__ __forceinline__ void few_unit(const FewTokenPlan<TX>&, int u, int sets, int& tile, int& set) {
+  tile = u / sets, set = u % sets;
+}
+template <int TX>
+__device__ __forceinline__ unsigned few_pair(const FewPairPlan<TX>& p, int tile, int t) {
+  const int at = p.start[tile] + t;
+  return at < p.start[tile + 1] ? p.pair[at] : kFewNone;
+}
+template <int TX>
+__device__ __forceinline__ unsigned few_any_pair(const FewPairPlan<TX>& p, int tile, int t) {
+  return p.pair[min(p.start[tile] + t, p.start[tile + 1] - 1)];
+}
+template <int TX>
 __device__ __forceinline__ const uint16_t* few_x(const MoeFewArgs& a, const FewPairPlan<TX>& p, int tile, int t) {
-  return a.x + p.pair[min(p.start[tile] + t, p.start[tile + 1] - 1)] / a.topk * a.x_ld;
+  return a.x + few_any_pair(p, tile, t) / a.topk * a.x_ld;
+}
+template <int TX>
+__device__ __forceinline__ void few_unit(const FewPairPlan<TX>& p, int u, int sets, int& tile, int& set) {
+  const int first = uniform(p.first[u / sets]), number = uniform(p.number[u / sets]), r = u - first * sets;
+  tile = first + r % number, set = r / number;
 }
 
 // ---- the stream ------------------------------------------------------------------
@@ -291,7 +309,7 @@ __device__ __forceinline__ const uint16_t* few_x(const MoeFewArgs& a, const FewP
 template <int TX, int R, int WAVES, int LDS_BYTES, bool MID>
 struct FewRing {
   static constexpr int kX = R * 2048, kMore = kX + TX * 256, kSlot = kMore + 256;
-  static constexpr int kXCopies = TX * 256 / 1024, kCopies = 2 * R + kXCopies + 1;
+  static constexpr int kXCopies = (TX * 256 + 1023) / 1024, kCopies = 2 * R + kXCopies + 1;
   static constexpr int kFit = LDS_BYTES / (WAVES * kSlot), kBlocks = kFit > 6 ? 6 : kFit;
   static constexpr int kWaveBytes = kBlocks * kSlot, kBytes = WAVES * kWaveBytes;
   static_assert(kBlocks >= 2 && (kBlocks - 1) * kCopies < 64, "LDS and vmcnt");
@@ -356,7 +374,8 @@ struct FewStream {
       for (int h = 0; h < 2; ++h)
         copy16_to_lds(src.codes[s] + g * kGroupK, row_off[h], at + s * 2048 + h * 1024);
 #pragma unroll
-    for (int c = 0; c < L::kXCopies; ++c) few_copy16(xsrc[c] + g * kGroupK, at + L::kX + c * 1024);
+    for (int c = 0; c < L::kXCopies; ++c)
+      if (TX >= 4 || lane < TX * 16) few_copy16(xsrc[c] + g * kGroupK, at + L::kX + c * 1024);
     const int step = MID && lane < 32 ? kGroupK / kFewGroup : 4;
     few_copy4(static_cast<const char*>(src.more) + g * step, at + L::kMore);
     issue_slot = issue_slot + 1 == L::kBlocks ? 0 : issue_slot + 1;
@@ -439,12 +458,15 @@ struct FewStream {
 template <int TX, int R, int WAVES>
 struct FewSums {
   float v[WAVES][TX][16 * R];
+  // This lane's four rows of row set s.
+  __device__ __forceinline__ v4f* at(int wave, int t, int s) {
+    return reinterpret_cast<v4f*>(&v[wave][t][((4 * s + (threadIdx.x >> 4 & 3)) ^ (t & (4 * R - 1))) * 4]);
+  }
   __device__ __forceinline__ void put(const v4f (&acc)[R]) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6, t = lane & 15, q = lane >> 4;
+    const int t = threadIdx.x & 15;
     if (t >= TX) return;
 #pragma unroll
-    for (int s = 0; s < R; ++s)
-      *reinterpret_cast<v4f*>(&v[wave][t][((4 * s + q) ^ (t & (4 * R - 1))) * 4]) = acc[s];
+    for (int s = 0; s < R; ++s) *at(threadIdx.x >> 6, t, s) = acc[s];
   }
   __device__ __forceinline__ float get(int t, int row) const {
     const int at = ((row >> 2) ^ (t & (4 * R - 1))) * 4 + (row & 3);
@@ -459,11 +481,13 @@ struct FewSums {
 // A unit is 16 rows of G and the 16 of U of one tile; a workgroup takes a run of
 // units, its waves every fourth block of each.  Grid: any number of workgroups.
 constexpr int kFewUpWaves = 4;
+constexpr int kFewLds = 160 * 1024;
+// Two workgroups fit a CU with a few tokens (their waits then overlap), one with more.
+constexpr int few_up_per_cu(int tx) { return tx <= 4 ? 2 : 1; }
 template <int TX, typename Plan>
 struct FewUp {
-  static constexpr int kLds = 160 * 1024 - int(sizeof(Plan) + sizeof(FewSums<TX, 2, kFewUpWaves>)) - 256;
-  // Two workgroups fit a CU with a few tokens (their waits then overlap), one with more.
-  using Ring = FewRing<TX, 2, kFewUpWaves, (TX == 4 ? 64 * 1024 : kLds), false>;
+  static constexpr int kRest = int(sizeof(Plan) + sizeof(FewSums<TX, 2, kFewUpWaves>)) + 1024;
+  using Ring = FewRing<TX, 2, kFewUpWaves, kFewLds / few_up_per_cu(TX) - kRest, false>;
   __attribute__((aligned(1024))) char ring[Ring::kBytes];
   FewSums<TX, 2, kFewUpWaves> sums;
   Plan plan;
@@ -481,7 +505,9 @@ __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const Mo
   const int u0 = int(units * blockIdx.x / gridDim.x), u1 = int(units * (blockIdx.x + 1) / gridDim.x);
   if (u0 == u1) return;
   auto source = [&](int u) {
-    const int e = uniform(plan.expert[u / sets]), row = u % sets * kFewGroup;
+    int tile, set;
+    few_unit(plan, u, sets, tile, set);
+    const int e = uniform(plan.expert[tile]), row = set * kFewGroup;
     FewSource<2> s;
     s.codes[0] = a.up + (int64_t(e) * 2 * a.inter + row) * a.hidden;
     s.codes[1] = s.codes[0] + int64_t(a.inter) * a.hidden;
@@ -489,7 +515,11 @@ __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const Mo
                             ((tid & 1) ? a.inter / kGroupK : 0)) * kg;
     return s;
   };
-  auto x_row = [&](int u, int t) { return few_x(a, plan, u / sets, t); };
+  auto x_row = [&](int u, int t) {
+    int tile, set;
+    few_unit(plan, u, sets, tile, set);
+    return few_x(a, plan, tile, t & (TX - 1));
+  };
   FewStream<typename Lds::Ring, TX, 2, kFewUpWaves, false> stream;
   const int blocks = (kg - wave + kFewUpWaves - 1) / kFewUpWaves;
   stream.start(lds.ring, a.hidden, u0, wave, wave, kFewUpWaves, (u1 - u0) * blocks, source, x_row);
@@ -505,7 +535,9 @@ __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const Mo
     few_barrier();  // the sums of the unit before are read
     lds.sums.put(acc);
     few_barrier();
-    const int tile = u / sets, set = u % sets, row = tid & 15, t = tid >> 4;
+    int tile, set;
+    few_unit(plan, u, sets, tile, set);
+    const int row = tid & 15, t = tid >> 4;
     const unsigned p = t < TX ? few_pair(plan, tile, t) : kFewNone;
     if (p == kFewNone) continue;  // (16 lanes together)
     const float v = activate(a.activation, lds.sums.get(t, row)) * lds.sums.get(t, 16 + row);
@@ -524,152 +556,88 @@ __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const Mo
   }
 }
 
-// ---- second kernel, any number of tokens -------------------------------------------
-// A workgroup has 32 rows of the output, of all tokens, in LDS and takes the tiles
-// one after the other, its waves every fourth block of each.  Grid: hidden / 32.
-template <int TX>
-struct FewDownPairs {
-  static constexpr int kWaves = 4;
-  using Plan = FewPairPlan<TX>;
-  using Ring = FewRing<TX, 2, kWaves, 132 * 1024, true>;
-  __attribute__((aligned(1024))) char ring[Ring::kBytes];
-  FewSums<TX, 2, kWaves> sums;
-  float out[kFewTokens][32];
-  float weight[kFewMaxPairs];
+// ---- second kernel -----------------------------------------------------------------
+// A workgroup has 16 R rows of the output; its waves take equal runs of the
+// tiles' blocks and meet once, at the end.  With a column for each token (a
+// FewTokenPlan) a wave's sums over all experts, weighted, stay in registers;
+// else they are added, at the end of each of its tiles, to the wave's own sums
+// of every token in LDS.  Grid: hidden / (16 R).
+template <int TX, int R, int WAVES, typename Plan>
+struct FewDown {
+  static constexpr bool kTokens = std::is_same_v<Plan, FewTokenPlan<TX>>;
+  static constexpr int kSums = kTokens ? TX : kFewTokens;  // tokens
+  static constexpr int kApart = kTokens ? 0 : int(sizeof(FewSums<kSums, R, WAVES>));
+  using Ring = FewRing<TX, R, WAVES, kFewLds - int(sizeof(Plan)) - kApart - 1024, true>;
+  using Sums = FewSums<kSums, R, WAVES>;
+  __attribute__((aligned(1024))) char ring[Ring::kBytes + kApart];  // the tokens' sums lie behind it, or take its place
   Plan plan;
+  static_assert(sizeof(Sums) <= sizeof(ring) && sizeof(FewPlanScratch<Plan::kPairs>) <= Ring::kBytes, "places");
 };
 
-template <int TX>
-__global__ void __launch_bounds__(FewDownPairs<TX>::kWaves* kWave) moe_few_down_pairs_kernel(const MoeFewArgs a) {
-  using Lds = FewDownPairs<TX>;
-  constexpr int kWaves = Lds::kWaves, kThreads = kWaves * kWave, kRows = 32;
+template <int TX, int R, int WAVES, typename Plan>
+__global__ void __launch_bounds__(WAVES* kWave) moe_few_down_kernel(const MoeFewArgs a) {
+  using Lds = FewDown<TX, R, WAVES, Plan>;
+  constexpr int kRows = 16 * R;
   __shared__ Lds lds;
-  const auto& plan = lds.plan;
-  const int tid = threadIdx.x, wave = uniform(tid >> 6), row0 = blockIdx.x * kRows, kg = a.inter / kGroupK;
-  for (int p = tid; p < a.tokens * a.topk; p += kThreads) lds.weight[p] = a.weights ? a.weights[p] : 1.f;
-  for (int o = tid; o < a.tokens * kRows; o += kThreads) lds.out[o / kRows][o % kRows] = 0.f;
-  few_plan<TX, kWaves>(a, lds.plan, *reinterpret_cast<FewPlanScratch<kFewMaxPairs>*>(lds.ring));
-  const int tiles = uniform(plan.tiles);
-  const auto row_pair = [&](int u, int t) { return plan.pair[min(plan.start[u] + t, plan.start[u + 1] - 1)]; };
-  auto source = [&](int u) {
-    const int e = uniform(plan.expert[u]), lane = tid & (kWave - 1);
-    FewSource<2> s;
-    s.codes[0] = a.down + (int64_t(e) * a.hidden + row0) * a.inter;
-    s.codes[1] = s.codes[0] + int64_t(16) * a.inter;
-    const float* scales = a.down_scales + (int64_t(e) * (a.hidden / kGroupK) + row0 / kGroupK) * kg;
-    s.more = lane < 32 ? static_cast<const void*>(a.exponents + int64_t(row_pair(u, lane >> 1 & (TX - 1))) *
-                                                                    (a.inter / kFewGroup) + 4 * (lane & 1))
-                       : scales;
-    return s;
-  };
-  auto x_row = [&](int u, int t) { return a.mid + int64_t(row_pair(u, t)) * a.inter; };
-  FewStream<typename Lds::Ring, TX, 2, kWaves, true> stream;
-  const int blocks = (kg - wave + kWaves - 1) / kWaves;
-  stream.start(lds.ring, a.inter, 0, wave, wave, kWaves, tiles * blocks, source, x_row);
-  for (int u = 0; u < tiles; ++u) {
-    v4f acc[2] = {};
-    for (int i = 0; i < blocks; ++i) {
-      const FewBlock<2> b = stream.next(source, x_row);
-      const float scale = ldexpf(b.scale[0], b.exponent);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[s][r] = fmaf(scale, b.part[s][r], acc[s][r]);
-    }
-    few_barrier();  // the sums of the unit before are read
-    lds.sums.put(acc);
-    few_barrier();
-    const int first = plan.start[u], count = plan.start[u + 1] - first;
-    for (int o = tid; o < count * kRows; o += kThreads) {
-      const int row = o % kRows;
-      int t = o / kRows;
-      const int token = plan.pair[first + t] / a.topk;
-      // pairs of one token (an expert picked twice) follow one another; the first one's thread adds them all
-      if (t > 0 && plan.pair[first + t - 1] / a.topk == token) continue;
-      float sum = lds.out[token][row];
-      for (; t < count && plan.pair[first + t] / a.topk == token; ++t)
-        sum = fmaf(lds.weight[plan.pair[first + t]], lds.sums.get(t, row), sum);
-      lds.out[token][row] = sum;
-    }
-  }
-  __syncthreads();
-  for (int o = tid; o < a.tokens * (kRows / 2); o += kThreads) {
-    const int t = o / (kRows / 2), c = 2 * (o % (kRows / 2));
-    *reinterpret_cast<uint32_t*>(a.out + int64_t(t) * a.hidden + row0 + c) =
-        pack_bf16x2(lds.out[t][c], lds.out[t][c + 1]);
-  }
-}
-
-// ---- second kernel, up to TX tokens ------------------------------------------------
-// A lane's column is a token, so its sums over all experts, weighted, stay in
-// its registers.  A workgroup has 16 R rows of the output; its waves take equal
-// runs of the experts' blocks and meet once, at the end.  Grid: hidden / (16 R).
-constexpr int kFewDownWaves = 8;
-template <int TX, int R>
-struct FewDownTokens {
-  static constexpr int kWaves = kFewDownWaves;
-  using Plan = FewTokenPlan<TX>;
-  using Ring = FewRing<TX, R, kWaves, 160 * 1024 - int(sizeof(Plan)) - 1024, true>;
-  __attribute__((aligned(1024))) char ring[Ring::kBytes];
-  Plan plan;
-  static_assert(sizeof(FewSums<TX, R, kWaves>) <= Ring::kBytes, "the sums take the ring's place");
-  static_assert(sizeof(FewPlanScratch<Plan::kPairs>) <= Ring::kBytes, "the plan's scratch takes the ring's place");
-};
-
-template <int TX, int R>
-__global__ void __launch_bounds__(kFewDownWaves* kWave) moe_few_down_kernel(const MoeFewArgs a) {
-  using Lds = FewDownTokens<TX, R>;
-  constexpr int kWaves = Lds::kWaves, kRows = 16 * R;
-  __shared__ Lds lds;
-  const auto& plan = lds.plan;
-  few_plan<TX, kWaves>(a, lds.plan, *reinterpret_cast<FewPlanScratch<Lds::Plan::kPairs>*>(lds.ring));
+  const Plan& plan = lds.plan;
+  auto& sums = *reinterpret_cast<typename Lds::Sums*>(lds.ring + (Lds::kTokens ? 0 : Lds::Ring::kBytes));
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = uniform(tid >> 6);
+  if constexpr (!Lds::kTokens)
+    for (int i = lane; i < a.tokens * kRows; i += kWave) sums.v[wave][i / kRows][i % kRows] = 0.f;
+  few_plan<TX, WAVES>(a, lds.plan, *reinterpret_cast<FewPlanScratch<Plan::kPairs>*>(lds.ring));
   const int row0 = blockIdx.x * kRows, kg = a.inter / kGroupK, sets = a.inter / kFewGroup;
-  const int all = uniform(plan.tiles) * kg;  // (at most 512 experts' 512 blocks)
-  const int f0 = all * wave / kWaves, f1 = all * (wave + 1) / kWaves;
-  // a column without a pair: the tile's first one's (there is one)
-  auto row_pair = [&](int u, int t) {
-    unsigned p = plan.pair[u][t];
-    for (int i = 0; p == kFewNone; ++i) p = plan.pair[u][i];
-    return p;
-  };
+  const int all = uniform(plan.tiles) * kg;  // (at most 1024 tiles of 512 blocks)
+  const int f0 = int(int64_t(all) * wave / WAVES), f1 = int(int64_t(all) * (wave + 1) / WAVES);
   auto source = [&](int u) {
     const int e = uniform(plan.expert[u]);
     FewSource<R> s;
 #pragma unroll
     for (int r = 0; r < R; ++r) s.codes[r] = a.down + (int64_t(e) * a.hidden + row0 + 16 * r) * a.inter;
     const float* scales = a.down_scales + (int64_t(e) * (a.hidden / kGroupK) + row0 / kGroupK) * kg;
-    s.more = lane < 32 ? static_cast<const void*>(a.exponents + int64_t(row_pair(u, lane >> 1 & (TX - 1))) * sets +
+    s.more = lane < 32 ? static_cast<const void*>(a.exponents +
+                                                  int64_t(few_any_pair(plan, u, (lane >> 1) & (TX - 1))) * sets +
                                                   4 * (lane & 1))
                        : scales;
     return s;
   };
-  auto x_row = [&](int u, int t) { return a.mid + int64_t(row_pair(u, t)) * a.inter; };
-  FewStream<typename Lds::Ring, TX, R, kWaves, true> stream;
+  auto x_row = [&](int u, int t) { return a.mid + int64_t(few_any_pair(plan, u, t & (TX - 1))) * a.inter; };
+  FewStream<typename Lds::Ring, TX, R, WAVES, true> stream;
   stream.start(lds.ring, a.inter, f0 / kg, f0 % kg, 0, 1, f1 - f0, source, x_row);
   v4f acc[R] = {};
-  int unit = -1;
-  bool live = false;
-  float weight = 0.f;
-  for (int f = f0; f < f1; ++f) {
-    if (f / kg != unit) {
-      unit = f / kg;
-      const unsigned p = plan.pair[unit][lane & (TX - 1)];
-      live = p != kFewNone;
-      weight = live ? plan.weight[p] : 0.f;
+  for (int f = f0, unit = f0 / kg; f < f1; ++unit) {
+    const unsigned p = few_pair(plan, unit, lane & (TX - 1));
+    const bool live = p != kFewNone;
+    const float weight = live ? plan.weight[p] : 0.f;
+    for (const int end = min(f1, (unit + 1) * kg); f < end; ++f) {
+      const FewBlock<R> b = stream.next(source, x_row);
+      float scale = ldexpf(b.scale[0], b.exponent);
+      if constexpr (Lds::kTokens) scale *= weight;
+#pragma unroll
+      for (int s = 0; s < R; ++s)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[s][r] = live ? fmaf(scale, b.part[s][r], acc[s][r]) : acc[s][r];
     }
-    const FewBlock<R> b = stream.next(source, x_row);
-    const float scale = weight * ldexpf(b.scale[0], b.exponent);
+    if constexpr (!Lds::kTokens) {
+      const int token = live ? int(p) / a.topk : 0;
 #pragma unroll
-    for (int s = 0; s < R; ++s)
+      for (int s = 0; s < R; ++s) {
+        v4f* to = sums.at(wave, token, s);
+        if (live && (lane & 15) < TX) {  // a tile has a token once
+          v4f v = *to;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[s][r] = live ? fmaf(scale, b.part[s][r], acc[s][r]) : acc[s][r];
+          for (int r = 0; r < 4; ++r) v[r] = fmaf(weight, acc[s][r], v[r]);
+          *to = v;
+        }
+        acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+    }
   }
-  auto& sums = *reinterpret_cast<FewSums<TX, R, kWaves>*>(lds.ring);
   __syncthreads();  // every wave is done with its ring
-  sums.put(acc);
-  __syncthreads();
-  for (int o = tid; o < a.tokens * (kRows / 2); o += kWaves * kWave) {
+  if constexpr (Lds::kTokens) {
+    sums.put(acc);
+    __syncthreads();
+  }
+  for (int o = tid; o < a.tokens * (kRows / 2); o += WAVES * kWave) {
     const int t = o / (kRows / 2), c = 2 * (o % (kRows / 2));
     *reinterpret_cast<uint32_t*>(a.out + int64_t(t) * a.hidden + row0 + c) =
         pack_bf16x2(sums.get(t, c), sums.get(t, c + 1));

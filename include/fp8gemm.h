@@ -602,7 +602,7 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
  * Any number of tokens, min(64, 1024 / topk) at a time: an expert's matrices are
  * read once for up to 16 of its pairs, so beyond a few hundred pairs the grouped
  * GEMMs are the way.  hidden % 128 == 0 and inter % 128 == 0, both <= 65536, inter
- * > 0, topk <= 32, num_experts <= 65535 (FP8G_EUNSUPPORTED otherwise).  Tensors
+ * > 0, topk <= 32, num_experts <= 4096 (FP8G_EUNSUPPORTED otherwise).  Tensors
  * 16-byte aligned (expert_idx, weights 4).  A token's sum goes over its experts in a
  * fixed order: equal calls give equal bits. */
 size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int inter);
