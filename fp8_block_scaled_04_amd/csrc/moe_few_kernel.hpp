@@ -34,7 +34,7 @@
 namespace fp8g {
 
 constexpr int kFewTokens = 64;  // of a launch, at most
-constexpr int kFewMaxPairs = 1024;
+constexpr int kFewMaxPairs = 512;
 constexpr int kFewMaxTopk = 32;
 constexpr int kFewMaxExperts = 4096;  // a table of them takes the rings' place in LDS
 constexpr int kFewGroup = 16;  // columns of mid that share an exponent
@@ -48,7 +48,10 @@ struct MoeFewArgs {
   const float *up_scales, *down_scales;
   uint16_t* mid;      // [pairs][inter] FP16
   int8_t* exponents;  // [pairs][inter / 16]
+  float* partial;     // [slices][tokens][hidden], where the second kernel has slices
+  unsigned long long* counters;  // arrivals, one for each workgroup of a slice
   uint16_t* out;
+  unsigned tag;  // of the counters
   int tokens, topk, experts, hidden, inter, activation;
 };
 
@@ -122,6 +125,7 @@ struct FewPairPlan {
   uint16_t start[kPairs + 1];  // tile t's pairs are pair[start[t]] .. pair[start[t + 1] - 1]
   uint16_t expert[kPairs];
   uint16_t first[kPairs], number[kPairs];  // the first of its expert's tiles, and how many there are
+  uint16_t token[kPairs];                  // of a pair
   float weight[kPairs];
   int tiles;
 };
@@ -259,13 +263,14 @@ __device__ __forceinline__ void few_plan(const MoeFewArgs& a, FewPairPlan<TX>& p
       for (int i = 0; i < count; ++i) rank[j] += s.expert[pos + i] < p;
     }
     plan.pair[pos + rank[j]] = uint16_t(p);
+    plan.token[p] = uint16_t(p / a.topk);
   }
   __syncthreads();
 }
 
 // What the kernels ask a plan: the pair of column t of a tile (kFewNone: none) and, for a column that has none, a pair
-// to read in its place; the row of x for column t; and the tile and row set of a unit, the tiles of one expert next to
-// one another (the second then finds the rows in the cache).
+// to read in its place; the row of x for column t; and how many tiles of the same expert there are from a tile on that
+// is its first.
 template <int TX>
 __device__ __forceinline__ unsigned few_pair(const FewTokenPlan<TX>& p, int tile, int t) { return p.pair[tile][t]; }
 template <int TX>
@@ -279,9 +284,9 @@ __device__ __forceinline__ const uint16_t* few_x(const MoeFewArgs& a, const FewT
   return a.x + min(t, a.tokens - 1) * a.x_ld;
 }
 template <int TX>
-__device__ __forceinline__ void few_unit(const FewTokenPlan<TX>&, int u, int sets, int& tile, int& set) {
-  tile = u / sets, set = u % sets;
-}
+__device__ __forceinline__ int few_first(const FewTokenPlan<TX>&, int tile) { return tile; }
+template <int TX>
+__device__ __forceinline__ int few_number(const FewTokenPlan<TX>&, int) { return 1; }
 template <int TX>
 __device__ __forceinline__ unsigned few_pair(const FewPairPlan<TX>& p, int tile, int t) {
   const int at = p.start[tile] + t;
@@ -293,13 +298,33 @@ __device__ __forceinline__ unsigned few_any_pair(const FewPairPlan<TX>& p, int t
 }
 template <int TX>
 __device__ __forceinline__ const uint16_t* few_x(const MoeFewArgs& a, const FewPairPlan<TX>& p, int tile, int t) {
-  return a.x + few_any_pair(p, tile, t) / a.topk * a.x_ld;
+  return a.x + p.token[few_any_pair(p, tile, t)] * a.x_ld;
 }
 template <int TX>
-__device__ __forceinline__ void few_unit(const FewPairPlan<TX>& p, int u, int sets, int& tile, int& set) {
-  const int first = uniform(p.first[u / sets]), number = uniform(p.number[u / sets]), r = u - first * sets;
-  tile = first + r % number, set = r / number;
-}
+__device__ __forceinline__ int few_first(const FewPairPlan<TX>& p, int tile) { return uniform(p.first[tile]); }
+template <int TX>
+__device__ __forceinline__ int few_number(const FewPairPlan<TX>& p, int tile) { return uniform(p.number[tile]); }
+
+// The first kernel's units in order: experts, row sets of each, and next to one another the tiles of the expert, of
+// which the second then finds the rows in the cache.
+template <typename Plan>
+struct FewUnits {
+  const Plan& plan;
+  int sets, first, number, set, i;
+  __device__ __forceinline__ FewUnits(const Plan& plan_, int sets_, int u) : plan(plan_), sets(sets_) {
+    first = few_first(plan, u / sets), number = few_number(plan, first);
+    const int r = u - first * sets;
+    set = r / number, i = r % number;
+  }
+  __device__ __forceinline__ int tile() const { return first + i; }
+  __device__ __forceinline__ void next() {
+    if (++i < number) return;
+    i = 0;
+    if (++set < sets) return;
+    set = 0, first += number;
+    number = few_number(plan, min(first, plan.tiles - 1));
+  }
+};
 
 // ---- the stream ------------------------------------------------------------------
 // A block in LDS: 16 R rows of 128 codes (operand tiles, laid out as tile_byte
@@ -334,39 +359,38 @@ template <typename L, int TX, int R, int WAVES, bool MID>
 struct FewStream {
   const char* ring;
   uint32_t ring_at;
-  int lane, groups, g, g_restart, g_step, unit, total, issued = 0, taken = 0, issue_slot = 0, read_slot = 0;
+  int lane, groups, g, g_restart, g_step, total, issued = 0, taken = 0, issue_slot = 0, read_slot = 0;
   FewSource<R> src;
   const uint16_t* xsrc[L::kXCopies];
   unsigned row_off[2];
 
-  // `source(unit)`: the data of a unit; `x_row(unit, t)`: its t-th token's activations.
-  template <typename S, typename X>
-  __device__ __forceinline__ void begin_unit(S&& source, X&& x_row) {
-    src = source(unit);
+  // `units`: source() the data of the unit it is at, x_row(t) its t-th token's activations, next() goes on.
+  template <typename U>
+  __device__ __forceinline__ void begin_unit(U& units) {
+    src = units.source();
 #pragma unroll
     for (int c = 0; c < L::kXCopies; ++c) {
       const int t = (c * 64 + lane) / 16;
-      xsrc[c] = x_row(unit, t) + (((lane & 15) ^ t) & 15) * 8;
+      xsrc[c] = units.x_row(t & (TX - 1)) + (((lane & 15) ^ t) & 15) * 8;
     }
   }
-  // Blocks of this wave: `total` of them, from block g_ of unit `unit_` on every step-th, in further units from block
+  // Blocks of this wave: `total` of them, from block g_ of the first unit on every step-th, in further units from block
   // `restart` on.
-  template <typename S, typename X>
-  __device__ __forceinline__ void start(char* lds, int k, int unit_, int g_, int restart, int step, int total_,
-                                        S&& source, X&& x_row) {
+  template <typename U>
+  __device__ __forceinline__ void start(char* lds, int k, int g_, int restart, int step, int total_, U& units) {
     const int wave = uniform(threadIdx.x >> 6);
     lane = threadIdx.x & (kWave - 1);
     ring = lds + wave * L::kWaveBytes;
     ring_at = lds_addr(lds) + wave * L::kWaveBytes;
     groups = k / kGroupK;
-    unit = unit_, g = g_, g_restart = restart, g_step = step, total = total_;
+    g = g_, g_restart = restart, g_step = step, total = total_;
 #pragma unroll
     for (int h = 0; h < 2; ++h) row_off[h] = unsigned(tile_row(h, lane)) * unsigned(k) + 16u * tile_chunk(h, lane);
-    if (total > 0) begin_unit(source, x_row);
-    for (int i = 0; i < L::kBlocks && i < total; ++i) copy_next(source, x_row);
+    if (total > 0) begin_unit(units);
+    for (int i = 0; i < L::kBlocks && i < total; ++i) copy_next(units);
   }
-  template <typename S, typename X>
-  __device__ __forceinline__ void copy_next(S&& source, X&& x_row) {
+  template <typename U>
+  __device__ __forceinline__ void copy_next(U& units) {
     const uint32_t at = ring_at + unsigned(issue_slot) * L::kSlot;
 #pragma unroll
     for (int s = 0; s < R; ++s)
@@ -382,8 +406,8 @@ struct FewStream {
     g += g_step;
     if (++issued < total && g >= groups) {
       g = g_restart;
-      ++unit;
-      begin_unit(source, x_row);
+      units.next();
+      begin_unit(units);
     }
   }
   template <int N = L::kBlocks - 1>
@@ -391,8 +415,8 @@ struct FewStream {
     if (N == 0 || newer >= N) few_copies_left<N * L::kCopies>();
     else if constexpr (N > 0) wait<N - 1>(newer);
   }
-  template <typename S, typename X>
-  __device__ __forceinline__ FewBlock<R> next(S&& source, X&& x_row) {
+  template <typename U>
+  __device__ __forceinline__ FewBlock<R> next(U& units) {
     wait(min(total - 1 - taken, L::kBlocks - 1));  // blocks in flight after this one
     ++taken;
     const char* at = ring + read_slot * L::kSlot;
@@ -418,7 +442,7 @@ struct FewStream {
       for (int s = 0; s < R; ++s) b.scale[s] = *reinterpret_cast<const float*>(at + L::kMore + 4 * s) * 65536.f;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the block has been read
-    if (issued < total) copy_next(source, x_row);
+    if (issued < total) copy_next(units);
     b.exponent = 0;
     if constexpr (MID) {
       // The lane's activations, 32 columns from 32 q on, are of the groups 2 q and 2 q + 1: brought to the token's
@@ -478,81 +502,87 @@ struct FewSums {
 };
 
 // ---- first kernel ------------------------------------------------------------------
-// A unit is 16 rows of G and the 16 of U of one tile; a workgroup takes a run of
+// A unit is 8 R rows of G and the 8 R of U of one tile; a workgroup takes a run of
 // units, its waves every fourth block of each.  Grid: any number of workgroups.
 constexpr int kFewUpWaves = 4;
 constexpr int kFewLds = 160 * 1024;
 // Two workgroups fit a CU with a few tokens (their waits then overlap), one with more.
-constexpr int few_up_per_cu(int tx) { return tx <= 4 ? 2 : 1; }
-template <int TX, typename Plan>
+template <int TX>
+constexpr int kFewUpPerCu = TX <= 4 ? 2 : 1;
+template <int TX, int R, typename Plan>
 struct FewUp {
-  static constexpr int kRest = int(sizeof(Plan) + sizeof(FewSums<TX, 2, kFewUpWaves>)) + 1024;
-  using Ring = FewRing<TX, 2, kFewUpWaves, kFewLds / few_up_per_cu(TX) - kRest, false>;
+  static constexpr int kRest = int(sizeof(Plan) + sizeof(FewSums<TX, R, kFewUpWaves>)) + 1024;
+  using Ring = FewRing<TX, R, kFewUpWaves, kFewLds / kFewUpPerCu<TX> - kRest, false>;
   __attribute__((aligned(1024))) char ring[Ring::kBytes];
-  FewSums<TX, 2, kFewUpWaves> sums;
+  FewSums<TX, R, kFewUpWaves> sums;
   Plan plan;
   static_assert(sizeof(FewPlanScratch<Plan::kPairs>) <= Ring::kBytes, "the plan's scratch takes the ring's place");
 };
 
-template <int TX, typename Plan>
+template <int TX, int R, typename Plan>
 __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const MoeFewArgs a) {
-  using Lds = FewUp<TX, Plan>;
+  using Lds = FewUp<TX, R, Plan>;
+  constexpr int kRows = 8 * R;  // of G, and of U
   __shared__ Lds lds;
   const Plan& plan = lds.plan;
   few_plan<TX, kFewUpWaves>(a, lds.plan, *reinterpret_cast<FewPlanScratch<Plan::kPairs>*>(lds.ring));
-  const int sets = a.inter / kFewGroup, kg = a.hidden / kGroupK, tid = threadIdx.x, wave = uniform(tid >> 6);
+  const int sets = a.inter / kRows, tid = threadIdx.x, wave = uniform(tid >> 6);
   const int64_t units = int64_t(uniform(plan.tiles)) * sets;
   const int u0 = int(units * blockIdx.x / gridDim.x), u1 = int(units * (blockIdx.x + 1) / gridDim.x);
   if (u0 == u1) return;
-  auto source = [&](int u) {
-    int tile, set;
-    few_unit(plan, u, sets, tile, set);
-    const int e = uniform(plan.expert[tile]), row = set * kFewGroup;
-    FewSource<2> s;
-    s.codes[0] = a.up + (int64_t(e) * 2 * a.inter + row) * a.hidden;
-    s.codes[1] = s.codes[0] + int64_t(a.inter) * a.hidden;
-    s.more = a.up_scales + (int64_t(e) * 2 * (a.inter / kGroupK) + row / kGroupK +
-                            ((tid & 1) ? a.inter / kGroupK : 0)) * kg;
-    return s;
-  };
-  auto x_row = [&](int u, int t) {
-    int tile, set;
-    few_unit(plan, u, sets, tile, set);
-    return few_x(a, plan, tile, t & (TX - 1));
-  };
-  FewStream<typename Lds::Ring, TX, 2, kFewUpWaves, false> stream;
-  const int blocks = (kg - wave + kFewUpWaves - 1) / kFewUpWaves;
-  stream.start(lds.ring, a.hidden, u0, wave, wave, kFewUpWaves, (u1 - u0) * blocks, source, x_row);
-  for (int u = u0; u < u1; ++u) {
-    v4f acc[2] = {};
-    for (int i = 0; i < blocks; ++i) {
-      const FewBlock<2> b = stream.next(source, x_row);
+  struct Units : FewUnits<Plan> {
+    const MoeFewArgs& a;
+    int kg;
+    __device__ __forceinline__ Units(const MoeFewArgs& a_, const Plan& plan_, int sets_, int u)
+        : FewUnits<Plan>(plan_, sets_, u), a(a_), kg(a_.hidden / kGroupK) {}
+    __device__ __forceinline__ FewSource<R> source() const {
+      const int e = uniform(this->plan.expert[this->tile()]), row = this->set * kRows;
+      FewSource<R> s;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int r = 0; r < R; ++r)
+        s.codes[r] = a.up + (int64_t(e) * 2 * a.inter + (r < R / 2 ? 0 : a.inter) + row + 16 * (r % (R / 2))) * a.hidden;
+      s.more = a.up_scales + (int64_t(e) * 2 * (a.inter / kGroupK) + row / kGroupK +
+                              ((threadIdx.x & (R - 1)) < R / 2 ? 0 : a.inter / kGroupK)) * kg;
+      return s;
+    }
+    __device__ __forceinline__ const uint16_t* x_row(int t) const { return few_x(a, this->plan, this->tile(), t); }
+  };
+  Units copied(a, plan, sets, u0);
+  FewUnits<Plan> at(plan, sets, u0);
+  FewStream<typename Lds::Ring, TX, R, kFewUpWaves, false> stream;
+  const int blocks = (a.hidden / kGroupK - wave + kFewUpWaves - 1) / kFewUpWaves;
+  stream.start(lds.ring, a.hidden, wave, wave, kFewUpWaves, (u1 - u0) * blocks, copied);
+  for (int u = u0; u < u1; ++u, at.next()) {
+    v4f acc[R] = {};
+    for (int i = 0; i < blocks; ++i) {
+      const FewBlock<R> b = stream.next(copied);
+#pragma unroll
+      for (int s = 0; s < R; ++s)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[s][r] = fmaf(b.scale[s], b.part[s][r], acc[s][r]);
     }
     few_barrier();  // the sums of the unit before are read
     lds.sums.put(acc);
     few_barrier();
-    int tile, set;
-    few_unit(plan, u, sets, tile, set);
-    const int row = tid & 15, t = tid >> 4;
-    const unsigned p = t < TX ? few_pair(plan, tile, t) : kFewNone;
-    if (p == kFewNone) continue;  // (16 lanes together)
-    const float v = activate(a.activation, lds.sums.get(t, row)) * lds.sums.get(t, 16 + row);
-    // FP16 with the exponent that takes the largest of the 16 to 2^14 .. 2^15; with an infinity or a NaN the largest
-    // exponent, which leaves it what it is.
-    float top = fabsf(v);
+    for (int o = tid; o < TX * kRows; o += kFewUpWaves * kWave) {
+      const int row = o % kRows, t = o / kRows;
+      const unsigned p = few_pair(plan, at.tile(), t);
+      if (p == kFewNone) continue;  // (16 lanes together)
+      const float v = activate(a.activation, lds.sums.get(t, row)) * lds.sums.get(t, kRows + row);
+      // FP16 with the exponent that takes the largest of the 16 to 2^14 .. 2^15; with an infinity or a NaN the largest
+      // exponent, which leaves it what it is.
+      float top = fabsf(v);
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-      const float o = __shfl_xor(top, d, 16);
-      top = o > top || o != o ? o : top;
+      for (int d = 1; d < 16; d *= 2) {
+        const float other = __shfl_xor(top, d, 16);
+        top = other > top || other != other ? other : top;
+      }
+      const int e = top < __builtin_inff() ? max(-128, (top > 0.f ? ilogbf(top) : -128) - 14) : 113;
+      const _Float16 h = _Float16(ldexpf(v, -e));
+      const int64_t to = int64_t(p) * a.inter + at.set * kRows + row;
+      a.mid[to] = __builtin_bit_cast(uint16_t, h);
+      if (row % kFewGroup == 0) a.exponents[to / kFewGroup] = int8_t(e);
     }
-    const int e = top < __builtin_inff() ? max(-128, (top > 0.f ? ilogbf(top) : -128) - 14) : 113;
-    const _Float16 h = _Float16(ldexpf(v, -e));
-    a.mid[int64_t(p) * a.inter + set * kFewGroup + row] = __builtin_bit_cast(uint16_t, h);
-    if (row == 0) a.exponents[int64_t(p) * sets + set] = int8_t(e);
   }
 }
 
@@ -561,7 +591,44 @@ __global__ void __launch_bounds__(kFewUpWaves* kWave) moe_few_up_kernel(const Mo
 // tiles' blocks and meet once, at the end.  With a column for each token (a
 // FewTokenPlan) a wave's sums over all experts, weighted, stay in registers;
 // else they are added, at the end of each of its tiles, to the wave's own sums
-// of every token in LDS.  Grid: hidden / (16 R).
+// of every token in LDS.  Where there are few rows, slices of the tiles' blocks
+// have workgroups of their own; their sums go past the caches to `partial`, and the
+// last of them to arrive adds them in order (the counters are those of the
+// split-K GEMM: a word that does not carry the call's tag is restarted, and the
+// last arrival leaves it at zero).  Grid: x hidden / (16 R), y slices.
+constexpr int kFewMaxSlices = 8;
+
+// Counts an arrival; whether it is the last of `all`.
+__device__ __forceinline__ bool few_arrive(unsigned long long* counter, unsigned tag, int all) {
+  unsigned long long old = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), now;
+  for (;;) {
+    if (unsigned(old >> 32) == tag) {
+      now = __hip_atomic_fetch_add(counter, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+      break;
+    }
+    now = (unsigned long long)tag << 32 | 1ull;
+    if (__hip_atomic_compare_exchange_strong(counter, &old, now, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT))
+      break;
+  }
+  const bool last = unsigned(now) == unsigned(all);
+  if (last) __hip_atomic_store(counter, (unsigned long long)tag << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return last;
+}
+
+// The sum of S slices' partial sums, in order.
+template <int S>
+__device__ __forceinline__ v4f few_add(const float* partial, int64_t size) {
+  const float* at[S];
+  v4f v[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) at[s] = partial + s * size;
+  load16_coherent<S>(at, v);
+#pragma unroll
+  for (int s = 1; s < S; ++s) v[0] += v[s];
+  return v[0];
+}
+
 template <int TX, int R, int WAVES, typename Plan>
 struct FewDown {
   static constexpr bool kTokens = std::is_same_v<Plan, FewTokenPlan<TX>>;
@@ -587,29 +654,37 @@ __global__ void __launch_bounds__(WAVES* kWave) moe_few_down_kernel(const MoeFew
   few_plan<TX, WAVES>(a, lds.plan, *reinterpret_cast<FewPlanScratch<Plan::kPairs>*>(lds.ring));
   const int row0 = blockIdx.x * kRows, kg = a.inter / kGroupK, sets = a.inter / kFewGroup;
   const int all = uniform(plan.tiles) * kg;  // (at most 1024 tiles of 512 blocks)
-  const int f0 = int(int64_t(all) * wave / WAVES), f1 = int(int64_t(all) * (wave + 1) / WAVES);
-  auto source = [&](int u) {
-    const int e = uniform(plan.expert[u]);
-    FewSource<R> s;
+  const int slices = gridDim.y, run = blockIdx.y * WAVES + wave;
+  const int f0 = int(int64_t(all) * run / (slices * WAVES)), f1 = int(int64_t(all) * (run + 1) / (slices * WAVES));
+  struct Units {
+    const MoeFewArgs& a;
+    const Plan& plan;
+    int tile, row0, kg, sets;
+    __device__ __forceinline__ void next() { ++tile; }
+    __device__ __forceinline__ FewSource<R> source() const {
+      const int e = uniform(plan.expert[tile]), lane = threadIdx.x & (kWave - 1);
+      FewSource<R> s;
 #pragma unroll
-    for (int r = 0; r < R; ++r) s.codes[r] = a.down + (int64_t(e) * a.hidden + row0 + 16 * r) * a.inter;
-    const float* scales = a.down_scales + (int64_t(e) * (a.hidden / kGroupK) + row0 / kGroupK) * kg;
-    s.more = lane < 32 ? static_cast<const void*>(a.exponents +
-                                                  int64_t(few_any_pair(plan, u, (lane >> 1) & (TX - 1))) * sets +
-                                                  4 * (lane & 1))
-                       : scales;
-    return s;
+      for (int r = 0; r < R; ++r) s.codes[r] = a.down + (int64_t(e) * a.hidden + row0 + 16 * r) * a.inter;
+      const float* scales = a.down_scales + (int64_t(e) * (a.hidden / kGroupK) + row0 / kGroupK) * kg;
+      const int64_t p = few_any_pair(plan, tile, (lane >> 1) & (TX - 1));
+      s.more = lane < 32 ? static_cast<const void*>(a.exponents + p * sets + 4 * (lane & 1)) : scales;
+      return s;
+    }
+    __device__ __forceinline__ const uint16_t* x_row(int t) const {
+      return a.mid + int64_t(few_any_pair(plan, tile, t)) * a.inter;
+    }
   };
-  auto x_row = [&](int u, int t) { return a.mid + int64_t(few_any_pair(plan, u, t & (TX - 1))) * a.inter; };
+  Units copied{a, plan, f0 / kg, row0, kg, sets};
   FewStream<typename Lds::Ring, TX, R, WAVES, true> stream;
-  stream.start(lds.ring, a.inter, f0 / kg, f0 % kg, 0, 1, f1 - f0, source, x_row);
+  stream.start(lds.ring, a.inter, f0 % kg, 0, 1, f1 - f0, copied);
   v4f acc[R] = {};
   for (int f = f0, unit = f0 / kg; f < f1; ++unit) {
     const unsigned p = few_pair(plan, unit, lane & (TX - 1));
     const bool live = p != kFewNone;
     const float weight = live ? plan.weight[p] : 0.f;
     for (const int end = min(f1, (unit + 1) * kg); f < end; ++f) {
-      const FewBlock<R> b = stream.next(source, x_row);
+      const FewBlock<R> b = stream.next(copied);
       float scale = ldexpf(b.scale[0], b.exponent);
       if constexpr (Lds::kTokens) scale *= weight;
 #pragma unroll
@@ -618,7 +693,7 @@ __global__ void __launch_bounds__(WAVES* kWave) moe_few_down_kernel(const MoeFew
         for (int r = 0; r < 4; ++r) acc[s][r] = live ? fmaf(scale, b.part[s][r], acc[s][r]) : acc[s][r];
     }
     if constexpr (!Lds::kTokens) {
-      const int token = live ? int(p) / a.topk : 0;
+      const int token = live ? plan.token[p] : 0;
 #pragma unroll
       for (int s = 0; s < R; ++s) {
         v4f* to = sums.at(wave, token, s);
@@ -636,6 +711,30 @@ __global__ void __launch_bounds__(WAVES* kWave) moe_few_down_kernel(const MoeFew
   if constexpr (Lds::kTokens) {
     sums.put(acc);
     __syncthreads();
+  }
+  if (slices > 1) {
+    const int64_t size = int64_t(a.tokens) * a.hidden;
+    constexpr int kPieces = kRows / 4;
+    for (int o = tid; o < a.tokens * kPieces; o += WAVES * kWave) {
+      const int t = o / kPieces, c = 4 * (o % kPieces);
+      store16_coherent(a.partial + blockIdx.y * size + int64_t(t) * a.hidden + row0 + c,
+                       v4f{sums.get(t, c), sums.get(t, c + 1), sums.get(t, c + 2), sums.get(t, c + 3)});
+    }
+    __shared__ int last;
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (tid == 0) last = few_arrive(a.counters + blockIdx.x, a.tag, slices);
+    __syncthreads();
+    if (!last) return;
+    for (int o = tid; o < a.tokens * kPieces; o += WAVES * kWave) {
+      const int64_t at = int64_t(o / kPieces) * a.hidden + row0 + 4 * (o % kPieces);
+      v4f sum;
+      if (slices == 2) sum = few_add<2>(a.partial + at, size);
+      else if (slices == 4) sum = few_add<4>(a.partial + at, size);
+      else sum = few_add<8>(a.partial + at, size);
+      *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+    }
+    return;
   }
   for (int o = tid; o < a.tokens * (kRows / 2); o += WAVES * kWave) {
     const int t = o / (kRows / 2), c = 2 * (o % (kRows / 2));

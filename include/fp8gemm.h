@@ -599,13 +599,13 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
  *   out        [num_tokens][hidden] BF16 (written in full)
  *   workspace  fp8_moe_few_tokens_workspace_bytes() bytes, uninitialised, not shared
  *              by concurrent calls; FP8G_EINVAL without it
- * Any number of tokens, min(64, 1024 / topk) at a time: an expert's matrices are
+ * Any number of tokens, min(64, 512 / topk) at a time: an expert's matrices are
  * read once for up to 16 of its pairs, so beyond a few hundred pairs the grouped
  * GEMMs are the way.  hidden % 128 == 0 and inter % 128 == 0, both <= 65536, inter
  * > 0, topk <= 32, num_experts <= 4096 (FP8G_EUNSUPPORTED otherwise).  Tensors
  * 16-byte aligned (expert_idx, weights 4).  A token's sum goes over its experts in a
  * fixed order: equal calls give equal bits. */
-size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int inter);
+size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int hidden, int inter);
 int fp8_moe_few_tokens(const uint16_t* x, int64_t x_ld, const int32_t* expert_idx, const float* weights,
                        int num_tokens, int topk, const uint8_t* up, const float* up_scales, const uint8_t* down,
                        const float* down_scales, int num_experts, int hidden, int inter, int activation,
