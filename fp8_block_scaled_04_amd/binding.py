@@ -106,7 +106,7 @@ _SIGNATURES = {
     "fp8_norm_residual_backward_workspace_bytes": ([_i32, _i32], _sz),
     "fp8_norm_residual_backward": ([_vp, _vp, _vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _f32c, _i32, _vp, _vp,
                                     _i32, _f32c, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
-    "fp8_moe_few_tokens_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "fp8_moe_few_tokens_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
     "fp8_moe_few_tokens": ([_vp, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp,
                             _sz, _vp], _i32),
 }
@@ -1147,8 +1147,8 @@ def fp8_norm_residual_backward(grad_h, grad_y, x, h, grad_x=None, grad_residual=
     return grad_x, grad_residual, grad_pre_weight, grad_post_weight, grad_gate
 
 
-def fp8_moe_few_tokens_workspace_bytes(num_tokens: int, topk: int, inter: int) -> int:
-    return int(lib().fp8_moe_few_tokens_workspace_bytes(int(num_tokens), int(topk), int(inter)))
+def fp8_moe_few_tokens_workspace_bytes(num_tokens: int, topk: int, hidden: int, inter: int) -> int:
+    return int(lib().fp8_moe_few_tokens_workspace_bytes(int(num_tokens), int(topk), int(hidden), int(inter)))
 
 
 def fp8_moe_few_tokens(x, expert_idx, weights, up, up_scales, down, down_scales, out, activation=FP8G_ACT_SILU,
@@ -1181,7 +1181,7 @@ def fp8_moe_few_tokens(x, expert_idx, weights, up, up_scales, down, down_scales,
            _tensor(down_scales, "down_scales", f32, (E, _kg(hidden), _kg(inter)), dev))
     out_at = _tensor(out, "out", torch.bfloat16, (T, hidden), dev)
     s = _on(stream, dev)
-    needed = fp8_moe_few_tokens_workspace_bytes(T, topk, inter) if workspace is None else 0
+    needed = fp8_moe_few_tokens_workspace_bytes(T, topk, hidden, inter) if workspace is None else 0
     with _allocating(stream):
         ws_at, ws_bytes, _keep = _ws(workspace, needed, x.device)
     st = lib().fp8_moe_few_tokens(x.data_ptr(), x_ld, *ats, E, hidden, inter, activation, out_at, ws_at, ws_bytes, s)

@@ -91,10 +91,55 @@ __device__ __forceinline__ void param8(const void* p, bool bf16, int64_t at, flo
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// The same, loaded early and used late.
+struct RawParam {
+  uint4 w[2];
+  __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at) {
+    if (!p) return;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (bf16 ? 2 : 4));
+    w[0] = q[0];
+    if (!bf16) w[1] = q[1];
+  }
+  __device__ __forceinline__ void get(const void* p, bool bf16, float v[8]) const {
 #pragma unroll
-  for (int s = 32; s; s >>= 1) v += __shfl_xor(v, s, kWave);
-  return v;
+    for (int i = 0; i < 8; ++i) {
+      const uint4& f = w[i / 4];
+      const uint32_t f32 = (i & 3) == 0 ? f.x : (i & 3) == 1 ? f.y : (i & 3) == 2 ? f.z : f.w;
+      const uint32_t h = (i >> 1) == 0 ? w[0].x : (i >> 1) == 1 ? w[0].y : (i >> 1) == 2 ? w[0].z : w[0].w;
+      v[i] = !p ? 1.f : __uint_as_float(!bf16 ? f32 : i & 1 ? h & 0xffff0000u : h << 16);
+    }
+  }
+};
+
+// v of the lane that a DPP pattern names, within rows of 16 lanes (a few cycles; a shuffle goes through LDS).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kSwapPairs = 0xB1, kSwapHalves = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+// f over the 16 lanes of a row, over the wave: in every lane.
+template <typename F>
+__device__ __forceinline__ float row16(float v, F&& f) {
+  v = f(v, dpp<kSwapPairs>(v));
+  v = f(v, dpp<kSwapHalves>(v));
+  v = f(v, dpp<kMirror8>(v));
+  return f(v, dpp<kMirror16>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+  return row16(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float max16(float v) {
+  return row16(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  const int a = __float_as_int(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);  // the rows of each pair apart
+  v = __int_as_float(r[0]) + __int_as_float(r[1]);
+  const int b = __float_as_int(v);
+  const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);  // the halves apart
+  return __int_as_float(h[0]) + __int_as_float(h[1]);
 }
 
 // Sums of up to four values over the `waves` waves of a row (one wave: no barrier).  `part`: a place of LDS that no
@@ -116,10 +161,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int waves, NormPart& par
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float t = (lane & 15) < waves ? part.v[i][lane & 15] : 0.f;
-#pragma unroll
-    for (int s = 8; s; s >>= 1) t += __shfl_xor(t, s, 16);
-    v[i] = t;
+    v[i] = sum16((lane & 15) < waves ? part.v[i][lane & 15] : 0.f);
   }
 }
 
@@ -168,6 +210,10 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
   float v[C][8];
   Raw8<X> xs[C];
   Raw8<R> rs[C];
+  // Few rows, a piece each: the parameters are on their way with the row.  Else they are read where they are used (from
+  // the cache; the registers are worth more to the rows that run beside this one).
+  constexpr bool EARLY = C == 1;
+  RawParam post = {}, gate = {}, pre = {};
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     col[c] = 8 * int(threadIdx.x + c * blockDim.x);
@@ -177,6 +223,11 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
     if (in[c]) {
       xs[c].load(a.x, row * a.x_ld + col[c]);
       if (a.residual) rs[c].load(a.residual, row * a.residual_ld + col[c]);
+      if (EARLY) {
+        post.load(a.post_weight, a.params_bf16, col[c]);
+        gate.load(a.gate, a.params_bf16, (a.gate_per_row ? int64_t(row) * a.n : 0) + col[c]);
+        pre.load(a.pre_weight, a.params_bf16, col[c]);
+      }
     }
   }
 #pragma unroll
@@ -187,12 +238,14 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
     if (!in[c]) continue;
     float w[8], r[8];
     if (a.post_norm && a.post_weight) {
-      param8(a.post_weight, a.params_bf16, col[c], w);
+      if (EARLY) post.get(a.post_weight, a.params_bf16, w);
+      else param8(a.post_weight, a.params_bf16, col[c], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
     }
     if (a.gate) {
-      param8(a.gate, a.params_bf16, (a.gate_per_row ? int64_t(row) * a.n : 0) + col[c], w);
+      if (EARLY) gate.get(a.gate, a.params_bf16, w);
+      else param8(a.gate, a.params_bf16, (a.gate_per_row ? int64_t(row) * a.n : 0) + col[c], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
     }
@@ -209,7 +262,8 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
   for (int c = 0; c < C; ++c) {
     if (in[c]) {
       float w[8];
-      param8(a.pre_weight, a.params_bf16, col[c], w);
+      if (EARLY) pre.get(a.pre_weight, a.params_bf16, w);
+      else param8(a.pre_weight, a.params_bf16, col[c], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
       if (a.y) store8<X>(a.y, int64_t(row) * a.n + col[c], v[c]);
@@ -218,8 +272,7 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[c][i]));
-#pragma unroll
-      for (int s = 1; s < 16; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, 16));
+      top = max16(top);
       const float s = a.q_e5m2 ? group_scale<kFmtE5M2>(top) : group_scale<kFmtE4M3>(top);
       float d[8];
 #pragma unroll
