@@ -170,7 +170,7 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
   if (int st = check_norm(num_rows, n, kind, x_dtype, stream_dtype, param_dtype, gate_rows, gate, eps)) return st;
   if (x_ld < n) return FP8G_EINVAL;
   if (x_ld % 8 != 0) return FP8G_EUNSUPPORTED;
-  if ((grad_post_weight && !post_norm) || (grad_gate && !gate) || (grad_pre_weight && !grad_y)) return FP8G_EINVAL;
+  if ((grad_post_weight && !post_norm) || (grad_gate && !gate)) return FP8G_EINVAL;
   if (n == 0) return FP8G_OK;
   if (!all_aligned16(grad_h, grad_y, x, h, post_weight, gate, pre_weight, grad_x, grad_residual, grad_pre_weight,
                      grad_post_weight, grad_gate, workspace))
@@ -183,7 +183,8 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
     launch_column_sums(nullptr, 0, 3, n, grad_pre_weight, grad_post_weight, shared_gate, s);  // sums of nothing
     return launched();
   }
-  if ((!grad_h && !grad_y) || (grad_y && !h) || (!x && (post_norm || grad_gate))) return FP8G_EINVAL;
+  if ((!grad_h && !grad_y) || (grad_y && !h) || (!x && (post_norm || gate)) || (grad_pre_weight && !grad_y))
+    return FP8G_EINVAL;
   if (!grad_x && !grad_residual && !grad_gate && !sums) return FP8G_EINVAL;
   if (sums && (!workspace || workspace_bytes < fp8_norm_residual_backward_workspace_bytes(num_rows, n)))
     return FP8G_EINVAL;
