@@ -18,16 +18,12 @@ namespace fp8g {
 namespace host {
 namespace {
 
-constexpr bool kEpilogue = FP8G_DENSE_EPI != 0;
+constexpr int kMode = FP8G_DENSE_EPI ? kDenseEpilogue : kDense;
 
 template <int BM, int BN, int WMW, int WNW, int ST, bool SPLIT, int KU, int WK, int FMT>
 void launch(const GemmParams& p, int64_t grid, hipStream_t s) {
-  if constexpr (kEpilogue)
-    hipLaunchKernelGGL((gemm_epilogue_kernel<BM, BN, WMW, WNW, ST, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
-                       dim3(64 * WMW * WNW * WK), 0, s, p);
-  else
-    hipLaunchKernelGGL((gemm_kernel<BM, BN, WMW, WNW, ST, kDense, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
-                       dim3(64 * WMW * WNW * WK), 0, s, p);
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WMW, WNW, ST, kMode, SPLIT, KU, WK, FMT>), dim3(unsigned(grid)),
+                     dim3(64 * WMW * WNW * WK), 0, s, p);
 }
 
 template <bool SPLIT, int FMT>
@@ -48,12 +44,12 @@ int launch_kind(int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
 
 }  // namespace
 
-template <int FMT, bool>
+template <int FMT, int MODE>
 int launch_dense_kind(bool split, int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
   return split ? launch_kind<true, FMT>(kind, p, grid, s) : launch_kind<false, FMT>(kind, p, grid, s);
 }
 
-template int launch_dense_kind<FP8G_DENSE_FMT, kEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
+template int launch_dense_kind<FP8G_DENSE_FMT, kMode>(bool, int, const GemmParams&, int64_t, hipStream_t);
 
 }  // namespace host
 }  // namespace fp8g

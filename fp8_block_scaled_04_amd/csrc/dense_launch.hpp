@@ -14,20 +14,20 @@ namespace host {
 
 // Launches the kernel of dense configuration `kind` (a DenseKind) with
 // operand formats FMT (bit 0: LHS E5M2, bit 1: RHS E5M2), split-K or not,
-// with the epilogue of p or without one.
+// MODE kDense or kDenseEpilogue.
 // Returns FP8G_OK, or FP8G_EUNSUPPORTED (launching nothing) for a (kind,
 // split) pair that has no kernel.
-template <int FMT, bool EPI>
+template <int FMT, int MODE>
 int launch_dense_kind(bool split, int kind, const GemmParams& p, int64_t grid, hipStream_t s);
 
-extern template int launch_dense_kind<0, false>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<1, false>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<2, false>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<3, false>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<0, true>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<1, true>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<2, true>(bool, int, const GemmParams&, int64_t, hipStream_t);
-extern template int launch_dense_kind<3, true>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<0, kDense>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<1, kDense>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<2, kDense>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<3, kDense>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<0, kDenseEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<1, kDenseEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<2, kDenseEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
+extern template int launch_dense_kind<3, kDenseEpilogue>(bool, int, const GemmParams&, int64_t, hipStream_t);
 
 }  // namespace host
 }  // namespace fp8g

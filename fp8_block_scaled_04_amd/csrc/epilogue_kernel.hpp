@@ -29,9 +29,8 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float v[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-struct Epilogue {
-  static constexpr bool kActive = true;
-
+template <>
+struct EpilogueOf<kDenseEpilogue> {
   // N (4 or 8) consecutive values of the bias, from column `col` on.
   template <int N>
   static __device__ __forceinline__ void load_bias(const GemmParams& p, int col, float (&b)[N]) {
@@ -128,10 +127,5 @@ struct Epilogue {
     }
   }
 };
-
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, bool SPLIT, int KU, int WK, int FMT>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N * WK, 1) gemm_epilogue_kernel(const GemmParams p) {
-  gemm_body<BM, BN, WAVES_M, WAVES_N, STAGES, kDense, SPLIT, KU, WK, FMT, 0, 0, Epilogue>(p);
-}
 
 }  // namespace fp8g

@@ -39,13 +39,13 @@ void launch_gemm(const GemmParams& p, int64_t grid, hipStream_t s) {
 // The dense GEMM kernels are instantiated in dense_launch.hip, one object per
 // operand-format pair (FMT: bit 0 = LHS in E5M2, bit 1 = RHS in E5M2), with
 // and without an epilogue.
-template <bool EPI>
+template <int MODE>
 int launch_dense_fmt(bool split, int fmt, int kind, const GemmParams& p, int64_t grid, hipStream_t s) {
   switch (fmt) {
-    case 1: return fp8g::host::launch_dense_kind<1, EPI>(split, kind, p, grid, s);
-    case 2: return fp8g::host::launch_dense_kind<2, EPI>(split, kind, p, grid, s);
-    case 3: return fp8g::host::launch_dense_kind<3, EPI>(split, kind, p, grid, s);
-    default: return fp8g::host::launch_dense_kind<0, EPI>(split, kind, p, grid, s);
+    case 1: return fp8g::host::launch_dense_kind<1, MODE>(split, kind, p, grid, s);
+    case 2: return fp8g::host::launch_dense_kind<2, MODE>(split, kind, p, grid, s);
+    case 3: return fp8g::host::launch_dense_kind<3, MODE>(split, kind, p, grid, s);
+    default: return fp8g::host::launch_dense_kind<0, MODE>(split, kind, p, grid, s);
   }
 }
 
@@ -88,11 +88,12 @@ int check_dense_args(const uint8_t* lhs, int lhs_format, const float* lhs_scales
 }
 
 // The dense GEMM of checked arguments (m, n > 0): configuration, split-K
-// workspace layout, launches.  EPI: with the epilogue that p holds.
-template <bool EPI = false>
+// workspace layout, launches.  MODE kDenseEpilogue: with the epilogue that p
+// holds.
+template <int MODE = kDense>
 int run_dense_gemm(const uint8_t* lhs, int fmt, const float* lhs_scales, int64_t lhs_scales_ld, const uint8_t* rhs,
                    const float* rhs_scales, uint16_t* out, int m, int n, int k, void* workspace,
-                   size_t workspace_bytes, void* stream, GemmParams p = GemmParams{}) {
+                   size_t workspace_bytes, void* stream, GemmParams p = {}) {
   DenseConfig c = dense_config(m, n, k, true);
   if (c.splits > 1 && (!workspace || workspace_bytes < dense_workspace(c, m, n)))
     c = dense_config(m, n, k, false);
@@ -113,7 +114,7 @@ int run_dense_gemm(const uint8_t* lhs, int fmt, const float* lhs_scales, int64_t
     std::fprintf(stderr, "[fp8gemm] dense m=%d n=%d k=%d kind=%d tiles=%dx%d splits=%d grid=%lld\n", m, n, k,
                  c.kind, c.tiles_m, c.tiles_n, c.splits, (long long)grid);
   return launch_units(p, grid, [&](int64_t g) {
-    if (const int st = launch_dense_fmt<EPI>(c.splits > 1, fmt, c.kind, p, g, s)) return st;  // before any launch
+    if (const int st = launch_dense_fmt<MODE>(c.splits > 1, fmt, c.kind, p, g, s)) return st;  // before any launch
     return launched("gemm");
   });
 }
@@ -334,7 +335,7 @@ int fp8_gemm_nt_epilogue(const uint8_t* lhs, int lhs_format, const float* lhs_sc
   GemmParams p{};
   p.bias = bias; p.bias_bf16 = bias_dtype == FP8G_BF16; p.activation = activation;
   p.residual = residual; p.preact = preact;
-  return run_dense_gemm<true>(lhs, fmt, lhs_scales, lhs_scales_ld, rhs, rhs_scales, out, m, n, k, workspace,
+  return run_dense_gemm<fp8g::kDenseEpilogue>(lhs, fmt, lhs_scales, lhs_scales_ld, rhs, rhs_scales, out, m, n, k, workspace,
                               workspace_bytes, stream, p);
 }
 

@@ -30,7 +30,7 @@
 
 namespace fp8g {
 
-enum GemmMode { kDense = 0, kContiguous = 1, kMasked = 2 };
+enum GemmMode { kDense = 0, kContiguous = 1, kMasked = 2, kDenseEpilogue = 3 };
 
 constexpr int kXcds = 8;    // XCDs of an MI355X; workgroups are dealt to them round-robin
 constexpr int kGroupM = 4;  // M-tiles walked together in the dense tile order
@@ -54,18 +54,17 @@ struct GemmParams {
   int splits, groups_per_split;
   int units;                 // work units of the call (tiles, or tiles x splits)
   int unit_offset;           // first unit of this launch (launches under a CU limit take slices)
-  // read by kernels with an epilogue only (dense)
+  // read in mode kDenseEpilogue only
   const void* bias;          // [n] FP32, or BF16 with bias_bf16; or null
   const uint16_t* residual;  // [m][n] BF16, or null
   uint16_t* preact;          // [m][n] BF16, or null
   int bias_bf16, activation;
 };
 
-// What happens to the FP32 sums of a dense tile: nothing (they are rounded to
-// BF16), or what a type of Epilogue's form does with them.
-struct NoEpilogue {
-  static constexpr bool kActive = false;
-};
+// What mode kDenseEpilogue does with the FP32 sums, which the others round to
+// BF16 (epilogue_kernel.hpp defines it where that mode is built).
+template <int MODE>
+struct EpilogueOf;
 
 // Loads this lane's 32-byte K slice of one 16-row MFMA fragment from an LDS
 // tile laid out by tile_byte().  Lane l supplies row (l & 15) and K bytes
@@ -422,7 +421,7 @@ constexpr int epilogue_lds(bool split) {
   return split ? BM * (BN + 4) * 4 : BM * (BN + 8) * 2;
 }
 
-template <int BM, int BN, int TM, int TN, bool SPLIT, typename EPI = NoEpilogue>
+template <int BM, int BN, int TM, int TN, bool SPLIT, int MODE>
 __device__ __forceinline__ void write_tile(const GemmParams& p, const v4f (&acc)[TN][TM], uint8_t* smem, bool holder,
                                            int wrow_m, int wrow_n, int m0, int n0, int rows, int shape_n, int split,
                                            int m_tile, int n_tile, uint16_t* OUT) {
@@ -528,8 +527,8 @@ __device__ __forceinline__ void write_tile(const GemmParams& p, const v4f (&acc)
           v4f sum = t[g * S];
 #pragma unroll
           for (int sp = 1; sp < S; ++sp) sum += t[g * S + sp];
-          if constexpr (EPI::kActive) {
-            EPI::store4(p, sum, at[g], n0 + 4 * ((c0 + g * int(blockDim.x)) % (BN / 4)));
+          if constexpr (MODE == kDenseEpilogue) {
+            EpilogueOf<MODE>::store4(p, sum, at[g], n0 + 4 * ((c0 + g * int(blockDim.x)) % (BN / 4)));
           } else {
             uint2 v;
             v.x = pack_bf16x2(sum[0], sum[1]);
@@ -591,10 +590,10 @@ __device__ __forceinline__ void write_tile(const GemmParams& p, const v4f (&acc)
 // FMT selects the operand formats (bit 0: LHS E5M2, bit 1: RHS E5M2).
 // NSPEC / KSPEC > 0 make n / k compile-time constants (the runtime
 // specialisation builds them per shape); 0 takes them from the parameters.
-// EPI: what happens to the sums (dense only).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int MODE, bool SPLIT, int KU = 1, int WK = 1,
-          int FMT = 0, int NSPEC = 0, int KSPEC = 0, typename EPI = NoEpilogue>
-__device__ __forceinline__ void gemm_body(const GemmParams& p) {
+          int FMT = 0, int NSPEC = 0, int KSPEC = 0>
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N * WK, 1) gemm_kernel(const GemmParams p) {
+  constexpr bool DENSE = MODE == kDense || MODE == kDenseEpilogue;
   constexpr int NW = WAVES_M * WAVES_N * WK;  // 4 waves: one per SIMD; 8 waves: two per SIMD
   static_assert(NW == 4 || NW == 8, "four or eight waves per workgroup");
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -625,8 +624,8 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   // (rows padded by 8 elements so that neither the fragment-ordered writes
   // nor the row-ordered reads pile onto a few banks).
   // A split's FP32 partial tile is staged the same way (rows padded by 4).
-  constexpr int STAGED = epilogue_lds<BM, BN>(SPLIT);
-  constexpr int SMEM = RING > STAGED ? RING : STAGED;
+  constexpr int EPI = epilogue_lds<BM, BN>(SPLIT);
+  constexpr int SMEM = RING > EPI ? RING : EPI;
   static_assert(SMEM + SB_BLOCKS * kMaxGroups * 4 <= 160 * 1024, "LDS with the output staging");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
   __shared__ float sb_cache[SB_BLOCKS][kMaxGroups];
@@ -658,7 +657,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     tiles_m = cs.tiles;
     if (bid >= tiles_m * p.tiles_n) return;
   }
-  if constexpr (MODE == kDense) {
+  if constexpr (DENSE) {
     // Each launch deals its own units [unit_offset, unit_offset + gridDim.x)
     // to the XCDs (all of them when there is no CU limit), so that every
     // slice of a CU-limited call also keeps the tiles that run together on
@@ -781,7 +780,7 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
   // one-block contiguous tiles) skips the products (its copies still run:
   // the ring is shared); in the masked layout a live wave also skips its
   // 16-row sub-tiles that lie wholly past the count.
-  const bool wave_live = MODE == kDense || m0 + wrow_m < rows;
+  const bool wave_live = DENSE || m0 + wrow_m < rows;
   const int live_tm = MODE == kMasked ? uniform(min(TM, max(0, (rows - m0 - wrow_m + 15) / 16))) : TM;
 
   // Fragment pointers of ring slot wk (wave and fragment row offsets are
@@ -856,18 +855,12 @@ __device__ __forceinline__ void gemm_body(const GemmParams& p) {
     }
   }
   const bool holder = wk == 0;  // the waves that now hold the tile's sums
-  static_assert(MODE == kDense || !EPI::kActive, "only the dense GEMM takes an epilogue");
-  if constexpr (EPI::kActive && !SPLIT)
-    EPI::template store_tile<BM, BN, TM, TN, SMEM>(p, acc, smem, holder, wrow_m, wrow_n, m0, n0, rows, shape_n);
+  if constexpr (MODE == kDenseEpilogue && !SPLIT)
+    EpilogueOf<MODE>::template store_tile<BM, BN, TM, TN, SMEM>(p, acc, smem, holder, wrow_m, wrow_n, m0, n0, rows,
+                                                                shape_n);
   else
-    write_tile<BM, BN, TM, TN, SPLIT, EPI>(p, acc, smem, holder, wrow_m, wrow_n, m0, n0, rows, shape_n, split, m_tile,
-                                           n_tile, OUT);
-}
-
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int MODE, bool SPLIT, int KU = 1, int WK = 1,
-          int FMT = 0, int NSPEC = 0, int KSPEC = 0>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N * WK, 1) gemm_kernel(const GemmParams p) {
-  gemm_body<BM, BN, WAVES_M, WAVES_N, STAGES, MODE, SPLIT, KU, WK, FMT, NSPEC, KSPEC>(p);
+    write_tile<BM, BN, TM, TN, SPLIT, MODE>(p, acc, smem, holder, wrow_m, wrow_n, m0, n0, rows, shape_n, split, m_tile,
+                                            n_tile, OUT);
 }
 
 }  // namespace fp8g
