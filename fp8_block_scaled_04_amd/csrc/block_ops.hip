@@ -59,12 +59,20 @@ int launch_norm(const NormArgs& a, hipStream_t s) {
   return launched();
 }
 
-template <typename X, typename R, bool LAYER, int C, int MAX_THREADS>
+template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
 int launch_norm_backward(const NormGradArgs& a, int slices, hipStream_t s) {
   const int threads = int(cdiv(cdiv(a.n / 8, C), 64) * 64);
-  hipLaunchKernelGGL((fp8g::norm_residual_backward_kernel<X, R, LAYER, C, MAX_THREADS>), dim3(unsigned(slices)),
-                     dim3(unsigned(threads)), 0, s, a);
+  const int lds = fp8g::norm_param_lds(a.n, a.params_bf16, a.rows_per_slice);
+  hipLaunchKernelGGL((fp8g::norm_residual_backward_kernel<X, R, LAYER, ROW_GATE, C, MAX_THREADS>),
+                     dim3(unsigned(slices)), dim3(unsigned(threads)), lds, s, a);
   return launched();
+}
+
+template <typename X, typename R, bool LAYER, bool ROW_GATE>
+int launch_norm_backward(const NormGradArgs& a, int slices, hipStream_t s) {
+  if (a.n > 8192) return launch_norm_backward<X, R, LAYER, ROW_GATE, 2, 1024>(a, slices, s);
+  if (a.n > 4096) return launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 1024>(a, slices, s);
+  return launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 512>(a, slices, s);
 }
 
 // Rows of a slice and slices of a gradient's pass.
@@ -190,10 +198,9 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
     return FP8G_EINVAL;
   NormGradArgs a{};
   a.grad_h = grad_h; a.grad_y = grad_y; a.x = post_norm || gate ? x : nullptr; a.h = h;
-  a.post_weight = post_weight; a.gate = gate; a.pre_weight = pre_weight;
+  a.post_weight = post_norm ? post_weight : nullptr; a.gate = gate; a.pre_weight = pre_weight;
   a.grad_x = grad_x; a.grad_residual = grad_residual;
-  a.gate_per_row = gate && gate_rows != 1;
-  a.grad_gate = a.gate_per_row ? grad_gate : nullptr;
+  a.grad_gate = gate && gate_rows != 1 ? grad_gate : nullptr;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
   a.x_ld = x_ld;
   a.rows = num_rows; a.n = n; a.rows_per_slice = slice_rows(num_rows, kGradSlices);
@@ -204,9 +211,8 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
     using X = decltype(x_);
     using R = decltype(r_);
     constexpr bool L = decltype(layer)::value;
-    if (n > 8192) return launch_norm_backward<X, R, L, 2, 1024>(a, slices, s);
-    if (n > 4096) return launch_norm_backward<X, R, L, 1, 1024>(a, slices, s);
-    return launch_norm_backward<X, R, L, 1, 512>(a, slices, s);
+    return gate && gate_rows != 1 ? launch_norm_backward<X, R, L, true>(a, slices, s)
+                                  : launch_norm_backward<X, R, L, false>(a, slices, s);
   });
   if (st || !sums) return st;
   launch_column_sums(a.partial, slices, 3, n, grad_pre_weight, grad_post_weight, shared_gate, s);

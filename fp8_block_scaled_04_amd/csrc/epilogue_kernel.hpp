@@ -37,35 +37,50 @@ struct EpilogueOf<kDenseEpilogue> {
 #pragma unroll
     for (int i = 0; i < N; ++i) b[i] = 0.f;
     if (!p.bias) return;
+    if (p.bias_bf16) {
+      const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + col);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      b[i] = p.bias_bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p.bias)[col + i]) << 16)
-                         : static_cast<const float*>(p.bias)[col + i];
+      for (int i = 0; i < N; i += 4) {
+        const uint2 w = q[i / 4];
+        b[i] = __uint_as_float(w.x << 16), b[i + 1] = __uint_as_float(w.x & 0xffff0000u);
+        b[i + 2] = __uint_as_float(w.y << 16), b[i + 3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+    } else {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + col);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 w = q[i / 4];
+        b[i] = w.x, b[i + 1] = w.y, b[i + 2] = w.z, b[i + 3] = w.w;
+      }
+    }
   }
 
-  // Four sums of the split-K fix-up, at out[at] in column `col`.
-  static __device__ __forceinline__ void store4(const GemmParams& p, const v4f& sum, int64_t at, int col) {
+  // Four sums of the split-K fix-up, at out[at] in column `col`.  What they meet is loaded with the partial sums, which
+  // are waited for all together.
+  struct Four {
     float b[4];
-    load_bias(p, col, b);
-    uint2 r = make_uint2(0, 0), v;
-    if (p.residual) r = *reinterpret_cast<const uint2*>(p.residual + at);
-    float z[4], y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = sum[i] + b[i];
-    if (p.preact) {
-      v.x = pack_bf16x2(z[0], z[1]);
-      v.y = pack_bf16x2(z[2], z[3]);
-      *reinterpret_cast<uint2*>(p.preact + at) = v;
+    uint2 r;
+    __device__ __forceinline__ void load(const GemmParams& p, int64_t at, int col) {
+      load_bias(p, col, b);
+      r = make_uint2(0, 0);
+      if (p.residual) r = *reinterpret_cast<const uint2*>(p.residual + at);
     }
+    __device__ __forceinline__ void store(const GemmParams& p, const v4f& sum, int64_t at) const {
+      float z[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? r.x : r.y;
-      y[i] = activate(p.activation, z[i]) + __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+      for (int i = 0; i < 4; ++i) z[i] = sum[i] + b[i];
+      if (p.preact)
+        *reinterpret_cast<uint2*>(p.preact + at) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+      by_activation(p.activation, [&](auto tag) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = i < 2 ? r.x : r.y;
+          y[i] = activate<decltype(tag)::value>(z[i]) + __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+        }
+      });
+      *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     }
-    v.x = pack_bf16x2(y[0], y[1]);
-    v.y = pack_bf16x2(y[2], y[3]);
-    *reinterpret_cast<uint2*>(p.out + at) = v;
-  }
+  };
 
   // A whole tile from the accumulators (write_tile's arguments; SMEM bytes of LDS, free once the K loop is done).
   template <int BM, int BN, int TM, int TN, int SMEM>
@@ -85,6 +100,15 @@ struct EpilogueOf<kDenseEpilogue> {
     if (in) load_bias(p, col, b);
     for (int pass = 0; pass < PASSES; ++pass) {
       const int first = pass * PR, last = min(PR, rows - m0 - first);  // rows of this pass
+      const int64_t at0 = int64_t(m0 + first) * shape_n + col;
+      const bool work = in && r0 < last;
+      uint4 next[AHEAD] = {};
+      auto load = [&](int r) {  // of the residual; rows past the end: the last one again
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+          next[u] = *reinterpret_cast<const uint4*>(p.residual + at0 + int64_t(min(r + u * step, last - 1)) * shape_n);
+      };
+      if (work && p.residual) load(r0);
       __syncthreads();  // the ring, or the rows staged before, are read
       if (holder && wrow_m / PR == pass) {
 #pragma unroll
@@ -95,37 +119,37 @@ struct EpilogueOf<kDenseEpilogue> {
                                     4 * (lane >> 4)) = acc[i][j];
       }
       __syncthreads();
-      if (!in) continue;
-      const int64_t at0 = int64_t(m0 + first) * shape_n + col;
+      if (!work) continue;
       by_activation(p.activation, [&](auto tag) __attribute__((always_inline)) {
-      constexpr int ACT = decltype(tag)::value;
-      for (int r = r0; r < last; r += AHEAD * step) {
-        uint4 res[AHEAD] = {};
-        if (p.residual) {
+        constexpr int ACT = decltype(tag)::value;
+        for (int r = r0; r < last; r += AHEAD * step) {
+          uint4 res[AHEAD];
 #pragma unroll
-          for (int u = 0; u < AHEAD; ++u)  // rows past the end: the last one again
-            res[u] = *reinterpret_cast<const uint4*>(p.residual + at0 + int64_t(min(r + u * step, last - 1)) * shape_n);
+          for (int u = 0; u < AHEAD; ++u) res[u] = next[u];
+          if (p.residual && r + AHEAD * step < last) load(r + AHEAD * step);
+#pragma unroll
+          for (int u = 0; u < AHEAD; ++u) {
+            const int row = r + u * step;
+            if (row >= last) break;
+            const v4f lo = *reinterpret_cast<const v4f*>(stage + row * LDT + c8);
+            const v4f hi = *reinterpret_cast<const v4f*>(stage + row * LDT + c8 + 4);
+            float z[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = (i < 4 ? lo[i] : hi[i - 4]) + b[i];
+            const int64_t at = at0 + int64_t(row) * shape_n;
+            if (p.preact) *reinterpret_cast<uint4*>(p.preact + at) = pack_bf16x8(z);
+            unpack_bf16x8(res[u], y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += activate<ACT>(z[i]);
+            *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(y);
+          }
         }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int row = r + u * step;
-          if (row >= last) break;
-          const v4f lo = *reinterpret_cast<const v4f*>(stage + row * LDT + c8);
-          const v4f hi = *reinterpret_cast<const v4f*>(stage + row * LDT + c8 + 4);
-          float z[8], y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = (i < 4 ? lo[i] : hi[i - 4]) + b[i];
-          const int64_t at = at0 + int64_t(row) * shape_n;
-          if (p.preact) *reinterpret_cast<uint4*>(p.preact + at) = pack_bf16x8(z);
-          unpack_bf16x8(res[u], y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] += activate<ACT>(z[i]);
-          *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(y);
-        }
-      }
       });
     }
   }
 };
+
+template <>
+struct EpilogueFour<kDenseEpilogue> { using type = EpilogueOf<kDenseEpilogue>::Four; };
 
 }  // namespace fp8g

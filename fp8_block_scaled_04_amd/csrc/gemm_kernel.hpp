@@ -65,6 +65,10 @@ struct GemmParams {
 // BF16 (epilogue_kernel.hpp defines it where that mode is built).
 template <int MODE>
 struct EpilogueOf;
+template <int MODE>
+struct EpilogueFour { using type = char; };
+template <>
+struct EpilogueFour<kDenseEpilogue>;
 
 // Loads this lane's 32-byte K slice of one 16-row MFMA fragment from an LDS
 // tile laid out by tile_byte().  Lane l supplies row (l & 15) and K bytes
@@ -520,6 +524,14 @@ __device__ __forceinline__ void write_tile(const GemmParams& p, const v4f (&acc)
           for (int sp = 0; sp < S; ++sp) q[g * S + sp] = p.partial + at[g] + sp * mn;
         }
         v4f t[G * S];
+        [[maybe_unused]] typename EpilogueFour<MODE>::type four[G];
+        if constexpr (MODE == kDenseEpilogue) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const int c4 = 4 * ((c0 + g * int(blockDim.x)) % (BN / 4));
+            four[g].load(p, at[g], n0 + min(c4, min(BN, shape_n - n0) - 4));
+          }
+        }
         load16_coherent<G * S>(q, t);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -528,7 +540,7 @@ __device__ __forceinline__ void write_tile(const GemmParams& p, const v4f (&acc)
 #pragma unroll
           for (int sp = 1; sp < S; ++sp) sum += t[g * S + sp];
           if constexpr (MODE == kDenseEpilogue) {
-            EpilogueOf<MODE>::store4(p, sum, at[g], n0 + 4 * ((c0 + g * int(blockDim.x)) % (BN / 4)));
+            four[g].store(p, sum, at[g]);
           } else {
             uint2 v;
             v.x = pack_bf16x2(sum[0], sum[1]);

@@ -46,15 +46,15 @@ Layout layout(int num_tokens, int topk, int hidden, int inter) {
   return l;
 }
 
-// The second kernel, cut into slices where that leaves every workgroup 48 KB or more to stream (30 tokens, 40 experts of
-// 768 x 384: 24.1 us, uncut 34.4; 64 tokens, 64 experts of 2048 x 768: 85 and 122; but 20 tokens, 8 experts of 256 x
-// 128, 32 KB in all: 14.3 cut into eight, uncut 13.2).
+// The second kernel, cut into slices where that leaves every workgroup 56 KB or more to stream (30 tokens, 40 experts of
+// 768 x 384: 24.1 us, uncut 34.4; 64 tokens, 64 experts of 2048 x 768: 85 and 122; but one token, 8 experts of 2048 x
+// 768, 98 KB in all: 18.2 cut in two, uncut 17.6).
 template <int TX, int R, int WAVES, typename Plan>
 int launch_down(const MoeFewArgs& a, int64_t tiles, hipStream_t s) {
   const int row_tiles = a.hidden / (16 * R);
   const int64_t bytes = tiles * 16 * R * a.inter;  // of a workgroup
   int slices = max_slices(row_tiles);
-  while (slices > 1 && bytes / slices < 48 * 1024) slices /= 2;
+  while (slices > 1 && bytes / slices < 56 * 1024) slices /= 2;
   hipLaunchKernelGGL((fp8g::moe_few_down_kernel<TX, R, WAVES, Plan>), dim3(unsigned(row_tiles), unsigned(slices)),
                      dim3(WAVES * fp8g::kWave), 0, s, a);
   return launched("moe few down");

@@ -38,7 +38,7 @@ struct NormGradArgs {
   float* partial;    // [slices][3][n]: pre_weight, post_weight, gate; null: no sums
   int64_t x_ld;
   int rows, n, rows_per_slice;
-  bool post_norm, gate_per_row, params_bf16;
+  bool post_norm, params_bf16;
   float eps, residual_scale;
 };
 
@@ -294,12 +294,46 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 }
 
 // Grid: slices of rows, which a workgroup takes one after the other, each thread with its C pieces of 8 columns, whose
-// sums over the rows stay in its registers.  The next row is read while this one is worked on.  What a row needs of
-// itself takes two rounds of sums (three for layer norms, whose squares are of centred values):
+// sums over the rows stay in its registers.  What a row needs of itself takes two rounds of sums (three for layer norms,
+// whose squares are of centred values):
 //   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
-template <typename X, typename R, bool LAYER, int C, int MAX_THREADS>
+// The next row is read while this one is worked on, which works because nothing else is read meanwhile: memory answers
+// in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS (8192 x 4096
+// with its sums 100.7 us, 107 without), but for single rows, and FP32 ones of rows so long that they do not fit.
+constexpr int kNormParamBytes = 144 * 1024;
+__host__ __device__ inline int norm_param_lds(int n, bool params_bf16, int rows_per_slice) {
+  const int bytes = 3 * n * (params_bf16 ? 2 : 4);
+  return rows_per_slice > 1 && bytes <= kNormParamBytes ? bytes : 0;
+}
+template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
   __shared__ NormPart parts[2][3];
+  extern __shared__ __attribute__((aligned(16))) char params[];  // pre_weight, post_weight, gate, as they are stored
+  const int row_bytes = a.n * (a.params_bf16 ? 2 : 4);
+  const bool in_lds = norm_param_lds(a.n, a.params_bf16, a.rows_per_slice) != 0;
+  const void* const shared[3] = {a.pre_weight, a.post_weight, ROW_GATE ? nullptr : a.gate};
+  if (in_lds) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (shared[k])
+        for (int i = threadIdx.x * 16; i < row_bytes; i += blockDim.x * 16)
+          *reinterpret_cast<uint4*>(params + k * row_bytes + i) =
+              *reinterpret_cast<const uint4*>(static_cast<const char*>(shared[k]) + i);
+    __syncthreads();
+  }
+  auto param = [&](int k, int c, float v[8]) {
+    if (in_lds) {
+      const char* at = params + k * row_bytes + c * (a.params_bf16 ? 2 : 4);
+      RawParam r;
+      if (shared[k]) {
+        r.w[0] = *reinterpret_cast<const uint4*>(at);
+        if (!a.params_bf16) r.w[1] = *reinterpret_cast<const uint4*>(at + 16);
+      }
+      r.get(shared[k], a.params_bf16, v);
+    } else {
+      param8(shared[k], a.params_bf16, c, v);
+    }
+  };
   const int waves = blockDim.x >> 6, n = a.n;
   const float inv_n = 1.f / n;
   int col[C];
@@ -359,7 +393,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       for (int c = 0; c < C; ++c) {
         if (!in[c]) continue;
         float w[8];
-        param8(a.pre_weight, a.params_bf16, col[c], w);
+        param(0, col[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float b = gy[c][i] * w[i];
@@ -379,7 +413,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       for (int c = 0; c < C; ++c) {
         if (!in[c]) continue;
         float w[8];
-        param8(a.pre_weight, a.params_bf16, col[c], w);
+        param(0, col[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s_pre[c][i] = fmaf(gy[c][i], h[c][i] * r, s_pre[c][i]);
@@ -398,15 +432,16 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
         store8<R>(a.grad_residual, at0 + col[c], g);
       }
       float w[8];
-      param8(a.post_norm ? a.post_weight : nullptr, a.params_bf16, col[c], w);
+      param(1, col[c], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[c][i] *= rx;
       if (a.gate) {
         float u[8], g[8];
-        param8(a.gate, a.params_bf16, (a.gate_per_row ? at0 : 0) + col[c], g);
+        if constexpr (ROW_GATE) param8(a.gate, a.params_bf16, at0 + col[c], g);
+        else param(2, col[c], g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (x[c][i] * w[i]);
-        if (a.gate_per_row) {
+        if constexpr (ROW_GATE) {
           if (a.grad_gate) store8<float>(a.grad_gate, at0 + col[c], u);
         } else {
 #pragma unroll
