@@ -293,34 +293,29 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
   }
 }
 
-// Grid: slices of rows, which a workgroup takes one after the other, each thread with its C pieces of 8 columns, whose
-// sums over the rows stay in its registers.  What a row needs of itself takes two rounds of sums (three for layer norms,
+// Grid: slices of rows, which a workgroup takes blockDim.y at a time, each thread with its C pieces of 8 columns, whose
+// sums over the rows stay in its registers and are added through LDS at the end where there are several rows at a time.  What a row needs of itself takes two rounds of sums (three for layer norms,
 // whose squares are of centred values):
 //   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
 // The next row is read while this one is worked on, which works because nothing else is read meanwhile: memory answers
 // in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS (8192 x 4096
-// with its sums 100.7 us, 107 without), but for single rows, and FP32 ones of rows so long that they do not fit.
-constexpr int kNormParamBytes = 144 * 1024;
-__host__ __device__ inline int norm_param_lds(int n, bool params_bf16, int rows_per_slice) {
+// with its sums 99 us, 107 without), but for a workgroup that has no next row (257 x 2048: 11.7 us, 12.5 with them there),
+// and FP32 ones of rows so long that they do not fit.
+constexpr int kNormParamBytes = 144 * 1024, kNormGradRows = 8;  // rows at a time, at most
+__host__ __device__ inline int norm_param_lds(int n, bool params_bf16, bool one_round) {
   const int bytes = 3 * n * (params_bf16 ? 2 : 4);
-  return rows_per_slice > 1 && bytes <= kNormParamBytes ? bytes : 0;
+  return !one_round && bytes <= kNormParamBytes ? bytes : 0;
 }
 template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
-  __shared__ NormPart parts[2][3];
+  constexpr bool SEVERAL = MAX_THREADS == 512;  // rows at a time, perhaps
+  __shared__ NormPart parts[2][3][SEVERAL ? kNormGradRows : 1];
+  const int ty = SEVERAL ? threadIdx.y : 0, at_once = SEVERAL ? blockDim.y : 1;
   extern __shared__ __attribute__((aligned(16))) char params[];  // pre_weight, post_weight, gate, as they are stored
+  const int tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * at_once;
   const int row_bytes = a.n * (a.params_bf16 ? 2 : 4);
-  const bool in_lds = norm_param_lds(a.n, a.params_bf16, a.rows_per_slice) != 0;
+  const bool in_lds = norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= at_once) != 0;
   const void* const shared[3] = {a.pre_weight, a.post_weight, ROW_GATE ? nullptr : a.gate};
-  if (in_lds) {
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (shared[k])
-        for (int i = threadIdx.x * 16; i < row_bytes; i += blockDim.x * 16)
-          *reinterpret_cast<uint4*>(params + k * row_bytes + i) =
-              *reinterpret_cast<const uint4*>(static_cast<const char*>(shared[k]) + i);
-    __syncthreads();
-  }
   auto param = [&](int k, int c, float v[8]) {
     if (in_lds) {
       const char* at = params + k * row_bytes + c * (a.params_bf16 ? 2 : 4);
@@ -362,21 +357,33 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
   };
 #pragma unroll
   for (int c = 0; c < C; ++c) xs[c].clear(), gys[c].clear(), hs[c].clear(), ghs[c].clear();
-  if (first < last) load(first);
-  for (int row = first; row < last; ++row) {
+  if (first + ty < last) load(first + ty);
+  if (in_lds) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (shared[k])
+        for (int i = tid * 16; i < row_bytes; i += threads * 16)
+          *reinterpret_cast<uint4*>(params + k * row_bytes + i) =
+              *reinterpret_cast<const uint4*>(static_cast<const char*>(shared[k]) + i);
+    __syncthreads();
+  }
+  int turn = 0;
+  for (int round = first; round < last; round += at_once, turn ^= 1) {  // every wave takes every round
+    const int row = round + ty;
+    const bool live = !SEVERAL || row < last;
     const int64_t at0 = int64_t(row) * n;
-    NormPart* part = parts[row & 1];
+    auto& part = parts[turn];
     float x[C][8], h[C][8], gy[C][8], d[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) xs[c].get(x[c]), hs[c].get(h[c]), gys[c].get(gy[c]), ghs[c].get(d[c]);
-    if (row + 1 < last) load(row + 1);
+    if (row + at_once < last) load(row + at_once);
     if constexpr (LAYER) {
       float m[2] = {0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[0] += h[c][i], m[1] += x[c][i];
-      row_sums(m, waves, part[0]);
+      row_sums(m, waves, part[0][ty]);
       if (!a.post_norm) m[1] = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
           m[3] += b;
         }
       }
-      row_sums(m, waves, part[1]);
+      row_sums(m, waves, part[1][ty]);
       if (a.post_norm) rx = 1.f / sqrtf(fmaf(m[1], inv_n, a.eps));
     }
     if (a.grad_y) {
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       const float along = m[2] * inv_n * r * r, mean = LAYER ? m[3] * inv_n : 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (!in[c]) continue;
+        if (!in[c] || !live) continue;
         float w[8];
         param(0, col[c], w);
 #pragma unroll
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
     float b[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x; x becomes norm(x)
-      if (!in[c]) continue;
+      if (!in[c] || !live) continue;
       if (a.grad_residual) {
         float g[8];
 #pragma unroll
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       }
     }
     if (a.post_norm) {
-      row_sums(b, waves, part[2]);
+      row_sums(b, waves, part[2][ty]);
       const float along = b[0] * inv_n, mean = LAYER ? b[1] * inv_n : 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -471,18 +478,33 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
     if (a.grad_x) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (in[c]) store8<X>(a.grad_x, at0 + col[c], d[c]);
+        if (in[c] && live) store8<X>(a.grad_x, at0 + col[c], d[c]);
     }
   }
   if (!a.partial) return;
+  float* const out = a.partial + int64_t(blockIdx.x) * 3 * n;
+  auto put = [&](float (&sum)[C][8], int64_t at) {
+    if (SEVERAL && at_once > 1) {  // the rows' sums in order
+      float* const mine = reinterpret_cast<float*>(params) + threadIdx.x * 8;
+      static_assert(C == 1 || !SEVERAL, "several rows at a time have a piece a thread");
+      __syncthreads();
+      store8<float>(mine + ty * blockDim.x * 8, 0, sum[0]);
+      __syncthreads();
+      if (ty > 0) return;
+      for (int y = 1; y < at_once; ++y) {
+        float v[8];
+        load8(mine + y * blockDim.x * 8, v);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    if (!in[c]) continue;
-    float* p = a.partial + int64_t(blockIdx.x) * 3 * n + col[c];
-    store8<float>(p, 0, s_pre[c]);
-    store8<float>(p, n, s_post[c]);
-    store8<float>(p, 2 * int64_t(n), s_gate[c]);
-  }
+        for (int i = 0; i < 8; ++i) sum[0][i] += v[i];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (in[c]) store8<float>(out, at + col[c], sum[c]);
+  };
+  put(s_pre, 0);
+  put(s_post, n);
+  put(s_gate, 2 * int64_t(n));
 }
 
 }  // namespace fp8g
