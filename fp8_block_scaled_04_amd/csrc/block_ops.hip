@@ -19,6 +19,7 @@ constexpr int kNormMaxColumns = 16384;  // 8 columns x 4 pieces x 512 threads
 // Workgroups of a gradient's pass, at most: what 256 CUs hold at once, by their registers 1024 threads each.
 constexpr int grad_slices(int n) { return n > 4096 ? 256 : 512; }
 constexpr int64_t kMaxBlocks = 0xffffffff / 1024;  // workgroups of up to 1024 threads: their number is 32 bits
+constexpr int kMaxRows = 1 << 30;  // the kernels' row numbers are 32 bits, with room for a slice behind the last
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -36,7 +37,7 @@ int check_norm(int num_rows, int n, int kind, int x_dtype, int stream_dtype, int
   if (!float_type(x_dtype) || !float_type(stream_dtype) || !float_type(param_dtype) || !(eps >= 0.f))
     return FP8G_EINVAL;
   if (gate && gate_rows != 1 && gate_rows != num_rows) return FP8G_EINVAL;
-  if (n % 8 != 0 || n > kNormMaxColumns) return FP8G_EUNSUPPORTED;
+  if (n % 8 != 0 || n > kNormMaxColumns || num_rows > kMaxRows) return FP8G_EUNSUPPORTED;
   return FP8G_OK;
 }
 
@@ -117,7 +118,7 @@ int fp8_epilogue_backward(const uint16_t* grad_out, const uint16_t* preact, int 
                           uint16_t* grad_preact, float* grad_bias, void* workspace, size_t workspace_bytes,
                           void* stream) {
   if (m < 0 || n < 0 || activation < FP8G_ACT_NONE || activation > FP8G_ACT_SILU) return FP8G_EINVAL;
-  if (n % 8 != 0) return FP8G_EUNSUPPORTED;
+  if (n % 8 != 0 || m > kMaxRows || cdiv(n, 64) > kMaxBlocks) return FP8G_EUNSUPPORTED;
   if (n == 0) return FP8G_OK;
   auto s = static_cast<hipStream_t>(stream);
   if (grad_bias && !aligned16(grad_bias)) return FP8G_EINVAL;
@@ -189,8 +190,8 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
                                void* grad_residual, float* grad_pre_weight, float* grad_post_weight, float* grad_gate,
                                void* workspace, size_t workspace_bytes, void* stream) {
   if (int st = check_norm(num_rows, n, kind, x_dtype, stream_dtype, param_dtype, gate_rows, gate, eps)) return st;
-  if (x_ld < n) return FP8G_EINVAL;
-  if (x_ld % 8 != 0) return FP8G_EUNSUPPORTED;
+  if (x && x_ld < n) return FP8G_EINVAL;
+  if (x && x_ld % 8 != 0) return FP8G_EUNSUPPORTED;
   if ((grad_post_weight && !post_norm) || (grad_gate && !gate)) return FP8G_EINVAL;
   if (n == 0) return FP8G_OK;
   if (!all_aligned16(grad_h, grad_y, x, h, post_weight, gate, pre_weight, grad_x, grad_residual, grad_pre_weight,

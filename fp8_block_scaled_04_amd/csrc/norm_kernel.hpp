@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 }
 
 // Grid: slices of rows, which a workgroup takes blockDim.y at a time, each thread with its C pieces of 8 columns, whose
-// sums over the rows stay in its registers and are added through LDS at the end where there are several rows at a time.  What a row needs of itself takes two rounds of sums (three for layer norms,
-// whose squares are of centred values):
+// sums over the rows stay in its registers and are added through LDS at the end where there are several rows at a time.
+// What a row needs of itself takes two rounds of sums (three for layer norms, whose squares are of centred values):
 //   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
 // The next row is read while this one is worked on, which works because nothing else is read meanwhile: memory answers
 // in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS (8192 x 4096

@@ -517,8 +517,8 @@ int fp8_gemm_nt_epilogue(const uint8_t* lhs, int lhs_format, const float* lhs_sc
  *               preact itself
  *   grad_bias   [n] FP32 = sum over rows of grad_out * act'(preact) (FP32, before
  *               that rounding), or NULL: not computed
- * ReLU's derivative at 0 is 0.  n % 8 == 0 (FP8G_EUNSUPPORTED otherwise);
- * tensors 16-byte aligned.  With grad_bias the call needs a workspace of
+ * ReLU's derivative at 0 is 0.  n % 8 == 0, n < 2^28, m <= 2^30
+ * (FP8G_EUNSUPPORTED otherwise); tensors 16-byte aligned.  With grad_bias the call needs a workspace of
  * fp8_epilogue_backward_workspace_bytes() bytes (0: none), uninitialised, not
  * shared by concurrent calls; FP8G_EINVAL without it.  Sums have a fixed order:
  * equal calls give equal bits.  m = 0 gives a grad_bias of zeros. */
@@ -549,8 +549,9 @@ enum { FP8G_NORM_RMS = 0, FP8G_NORM_LAYER = 1 };
  *             [ceil(n / 128)][q_scales_ld >= num_rows]: what
  *             fp8_cast_per_token_group makes of y in FP32
  * At least one of h, y and q.  Strides are multiples of 8, n % 8 == 0 and n <=
- * 16384 (FP8G_EUNSUPPORTED otherwise); tensors 16-byte aligned.  Sums of
- * squares are FP32: rows of values above 1e18 come out as zeros. */
+ * 16384, num_rows < 2^22 (n <= 512: four times that), FP8G_EUNSUPPORTED
+ * otherwise; tensors 16-byte aligned.  Sums of squares are FP32: rows of values
+ * above 1e18 come out as zeros. */
 int fp8_norm_residual(const void* x, int x_dtype, int64_t x_ld, const void* residual, int64_t residual_ld,
                       int stream_dtype, int num_rows, int n, int kind, float eps, int post_norm,
                       const void* post_weight, const void* gate, int gate_rows, float residual_scale,
@@ -573,7 +574,7 @@ int fp8_norm_residual(const void* x, int x_dtype, int64_t x_ld, const void* resi
  * not) is asked for, the call needs a workspace of
  * fp8_norm_residual_backward_workspace_bytes() bytes, uninitialised, not shared
  * by concurrent calls; FP8G_EINVAL without it.  Sums have a fixed order: equal
- * calls give equal bits.  num_rows = 0 gives sums of zero. */
+ * calls give equal bits.  num_rows = 0 gives sums of zero; num_rows <= 2^30. */
 size_t fp8_norm_residual_backward_workspace_bytes(int num_rows, int n);
 int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const void* x, int x_dtype, int64_t x_ld,
                                const void* h, int stream_dtype, int num_rows, int n, int kind, float eps,
@@ -593,7 +594,7 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
  *              zeros; an expert may be named twice
  *   weights    [num_tokens][topk] FP32, or NULL (1)
  *   up         [num_experts][2 inter][hidden]: G, then U;
- *              up_scales [num_experts][2 inter / 128][hidden / 128]
+ *              up_scales [num_experts][2 inter / 128][hidden / 128], below 5e33
  *   down       [num_experts][hidden][inter];
  *              down_scales [num_experts][hidden / 128][inter / 128]
  *   out        [num_tokens][hidden] BF16 (written in full)

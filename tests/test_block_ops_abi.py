@@ -109,3 +109,22 @@ def test_workspace_sizes(lib):
     assert lib.fp8_norm_residual_backward_workspace_bytes(0, 8) == 0
     # 512 slices at most
     assert lib.fp8_norm_residual_backward_workspace_bytes(1 << 20, 1024) == 512 * 3 * 1024 * 4
+
+
+def test_sizes_past_32_bit_rows_and_grids_are_refused(lib):
+    """Row numbers and grids are 32 bits: nothing near their end reaches a kernel."""
+    past = (1 << 30) + 1
+    assert lib.fp8_epilogue_backward(P, P, 4, past, 64, P, None, None, 0, None) == EUNSUPPORTED
+    assert lib.fp8_epilogue_backward(P, P, 4, 1, 1 << 28, P, None, None, 0, None) == EUNSUPPORTED
+    for rows, n in ((past, 8), (2 ** 31 - 1, 8), (1 << 22, 1024), (1 << 24, 512)):
+        assert lib.fp8_norm_residual(P, 1, n, None, n, 1, rows, n, 0, 1e-6, 0, None, None, 1, 1.0, None, 0, P, None, None,
+                                     0, None, rows, None) == EUNSUPPORTED, (rows, n)
+    for rows in (past, 2 ** 31 - 1):
+        assert lib.fp8_norm_residual_backward(P, None, None, 1, 8, None, 1, rows, 8, 0, 1e-6, 0, None, None, 1, 1.0, None,
+                                              0, P, None, None, None, None, None, 0, None) == EUNSUPPORTED
+
+
+def test_norm_backward_asks_nothing_of_an_absent_x(lib):
+    """Without x its row stride is not looked at (no rows: nothing is launched)."""
+    args = (P, P, None, 1, 0, P, 1, 0, 64, 0, 1e-6, 0, None, None, 1, 1.0, None, 0, P, P, None, None, None, None, 0, None)
+    assert lib.fp8_norm_residual_backward(*args) == OK
