@@ -66,9 +66,9 @@ int grad_rows(int n) { return n > 4096 ? 1 : std::min<int>(fp8g::kNormGradRows, 
 
 template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
 int launch_norm_backward(const NormGradArgs& a, int slices, hipStream_t s) {
-  const int threads = int(cdiv(cdiv(a.n / 8, C), 64) * 64), rows = MAX_THREADS == 512 ? grad_rows(a.n) : 1;
-  const int lds = std::max(fp8g::norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= rows),
-                           rows > 1 ? rows * threads * 8 * int(sizeof(float)) : 0);
+  const int threads = int(cdiv(cdiv(a.n / 8, C), 64) * 64), rows = grad_rows(a.n);
+  const int of_rows = rows > 1 ? rows * threads * 8 : C > 1 ? 2 * a.n : 0;  // floats: sums of rows, or over them
+  const int lds = std::max(fp8g::norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= rows), 4 * of_rows);
   hipLaunchKernelGGL((fp8g::norm_residual_backward_kernel<X, R, LAYER, ROW_GATE, C, MAX_THREADS>),
                      dim3(unsigned(slices)), dim3(unsigned(threads), unsigned(rows)), lds, s, a);
   return launched();

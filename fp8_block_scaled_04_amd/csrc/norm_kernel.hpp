@@ -56,6 +56,11 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
+  // What was made of the values is not to be kept: the compiler takes them to be new.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i].x), "+v"(w[i].y), "+v"(w[i].z), "+v"(w[i].w));
+  }
   __device__ __forceinline__ void get(float v[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -299,24 +304,28 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 //   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
 // The next row is read while this one is worked on, which works because nothing else is read meanwhile: memory answers
 // in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS (8192 x 4096
-// with its sums 99 us, 107 without), but for a workgroup that has no next row (257 x 2048: 11.7 us, 12.5 with them there),
-// and FP32 ones of rows so long that they do not fit.
-constexpr int kNormParamBytes = 144 * 1024, kNormGradRows = 8;  // rows at a time, at most
+// with its sums 99 us, 107 without), but for a workgroup that has no next row (257 x 2048: 11.7 us, 12.5 with them there).
+// Rows of more than 8192 columns (two pieces a thread) leave no registers for the next row: their threads keep only
+// what is packed, d and one of the three sums, the other two lie in LDS, and the parameters come from the cache
+// (2048 x 12288: 106 us; all in registers, which spilled, 219).
+//
+// Bound by memory: six tensors a row, 8192 x 4096 at 4.0 TB/s, 16 waves a CU and the sums of 256 or 512 slices.
+constexpr int kNormGradRows = 8;  // rows at a time, at most
 __host__ __device__ inline int norm_param_lds(int n, bool params_bf16, bool one_round) {
-  const int bytes = 3 * n * (params_bf16 ? 2 : 4);
-  return !one_round && bytes <= kNormParamBytes ? bytes : 0;
+  return n <= 8192 && !one_round ? 3 * n * (params_bf16 ? 2 : 4) : 0;
 }
 template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
-  constexpr bool SEVERAL = MAX_THREADS == 512;  // rows at a time, perhaps
+  constexpr bool SEVERAL = C == 1 && MAX_THREADS == 512;  // rows at a time, perhaps
   __shared__ NormPart parts[2][3][SEVERAL ? kNormGradRows : 1];
-  const int ty = SEVERAL ? threadIdx.y : 0, at_once = SEVERAL ? blockDim.y : 1;
+  const int ty = SEVERAL ? uniform(threadIdx.y) : 0, at_once = SEVERAL ? blockDim.y : 1;
   extern __shared__ __attribute__((aligned(16))) char params[];  // pre_weight, post_weight, gate, as they are stored
   const int tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * at_once;
+  constexpr bool KEEP = C == 1;  // what is unpacked, and the sums, stay in registers
   const int row_bytes = a.n * (a.params_bf16 ? 2 : 4);
-  const bool in_lds = norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= at_once) != 0;
+  const bool in_lds = KEEP && norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= at_once) != 0;
   const void* const shared[3] = {a.pre_weight, a.post_weight, ROW_GATE ? nullptr : a.gate};
-  auto param = [&](int k, int c, float v[8]) {
+  auto param = [&](int k, unsigned c, float v[8]) {
     if (in_lds) {
       const char* at = params + k * row_bytes + c * (a.params_bf16 ? 2 : 4);
       RawParam r;
@@ -331,14 +340,20 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
   };
   const int waves = blockDim.x >> 6, n = a.n;
   const float inv_n = 1.f / n;
-  int col[C];
+  unsigned col[C];  // beside addresses that are a wave's
   bool in[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    col[c] = 8 * int(threadIdx.x + c * blockDim.x);
-    in[c] = col[c] < n;
+    col[c] = 8 * (threadIdx.x + c * blockDim.x);
+    in[c] = int(col[c]) < n;
   }
-  float s_pre[C][8] = {}, s_post[C][8] = {}, s_gate[C][8] = {};
+  float s_pre[C][8] = {}, s_post[KEEP ? C : 1][8] = {}, s_gate[KEEP ? C : 1][8] = {};
+  float* const long_sums = reinterpret_cast<float*>(params);  // !KEEP: post_weight's, gate's
+  if constexpr (!KEEP) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (in[c]) store8<float>(long_sums, col[c], s_post[0]), store8<float>(long_sums, n + col[c], s_post[0]);
+  }
   const int first = blockIdx.x * a.rows_per_slice, last = min(a.rows, first + a.rows_per_slice);
   Raw8<X> xs[C], gys[C];
   Raw8<R> hs[C], ghs[C];
@@ -347,12 +362,12 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (!in[c]) continue;
-      if (a.x) xs[c].load(a.x, row * a.x_ld + col[c]);
+      if (a.x) xs[c].load(static_cast<const X*>(a.x) + row * a.x_ld, col[c]);
       if (a.grad_y) {
-        gys[c].load(a.grad_y, at0 + col[c]);
-        hs[c].load(a.h, at0 + col[c]);
+        gys[c].load(static_cast<const X*>(a.grad_y) + at0, col[c]);
+        hs[c].load(static_cast<const R*>(a.h) + at0, col[c]);
       }
-      if (a.grad_h) ghs[c].load(a.grad_h, at0 + col[c]);
+      if (a.grad_h) ghs[c].load(static_cast<const R*>(a.grad_h) + at0, col[c]);
     }
   };
 #pragma unroll
@@ -371,27 +386,64 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
   for (int round = first; round < last; round += at_once, turn ^= 1) {  // every wave takes every round
     const int row = round + ty;
     const bool live = !SEVERAL || row < last;
+    // A column that may be new every time keeps every tensor's address in scalar registers: kept per lane and advanced
+    // from row to row, they spilled.
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(col[c]));
     const int64_t at0 = int64_t(row) * n;
     auto& part = parts[turn];
-    float x[C][8], h[C][8], gy[C][8], d[C][8];
+    float x_[C][8], h_[C][8], gy_[C][8], d[C][8], mean_h = 0.f, mean_x = 0.f;
+    if constexpr (KEEP) xs[0].get(x_[0]), hs[0].get(h_[0]), gys[0].get(gy_[0]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) xs[c].get(x[c]), hs[c].get(h[c]), gys[c].get(gy[c]), ghs[c].get(d[c]);
-    if (row + at_once < last) load(row + at_once);
+    for (int c = 0; c < C; ++c) ghs[c].get(d[c]);
+    if (KEEP && row + at_once < last) load(row + at_once);
+    auto get_x = [&](int c, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8 && KEEP; ++i) v[i] = x_[c][i];
+      if constexpr (!KEEP) {
+        xs[c].get(v);
+#pragma unroll
+        for (int i = 0; i < 8 && LAYER; ++i) v[i] -= mean_x;
+      }
+    };
+    auto get_h = [&](int c, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8 && KEEP; ++i) v[i] = h_[c][i];
+      if constexpr (!KEEP) {
+        hs[c].get(v);
+#pragma unroll
+        for (int i = 0; i < 8 && LAYER; ++i) v[i] -= mean_h;
+      }
+    };
+    auto get_gy = [&](int c, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8 && KEEP; ++i) v[i] = gy_[c][i];
+      if constexpr (!KEEP) gys[c].get(v);
+    };
+    auto next_piece = [&](int c) {
+      if constexpr (!KEEP) {
+        __builtin_amdgcn_sched_barrier(0);
+        xs[c].renew(), hs[c].renew(), gys[c].renew();
+      }
+    };
     if constexpr (LAYER) {
       float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        float x[8], h[8];
+        get_x(c, x), get_h(c, h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[0] += h[c][i], m[1] += x[c][i];
+        for (int i = 0; i < 8; ++i) m[0] += h[i], m[1] += x[i];
+        next_piece(c);
+      }
       row_sums(m, waves, part[0][ty]);
-      if (!a.post_norm) m[1] = 0.f;
+      mean_h = m[0] * inv_n;
+      if (a.post_norm) mean_x = m[1] * inv_n;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[c][i] = in[c] ? fmaf(-inv_n, m[0], h[c][i]) : 0.f;
-          x[c][i] = in[c] ? fmaf(-inv_n, m[1], x[c][i]) : 0.f;
-        }
+      for (int i = 0; i < 8 && KEEP; ++i) {
+        h_[0][i] = in[0] ? h_[0][i] - mean_h : 0.f;
+        x_[0][i] = in[0] ? x_[0][i] - mean_x : 0.f;
+      }
     }
     float m[4] = {0.f, 0.f, 0.f, 0.f};  // of h^2, x^2, a h, a
     float rx = 1.f;
@@ -399,16 +451,18 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (!in[c]) continue;
-        float w[8];
+        float w[8], x[8], h[8], gy[8];
         param(0, col[c], w);
+        get_x(c, x), get_h(c, h), get_gy(c, gy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float b = gy[c][i] * w[i];
-          m[0] = fmaf(h[c][i], h[c][i], m[0]);
-          m[1] = fmaf(x[c][i], x[c][i], m[1]);
-          m[2] = fmaf(b, h[c][i], m[2]);
+          const float b = gy[i] * w[i];
+          m[0] = fmaf(h[i], h[i], m[0]);
+          m[1] = fmaf(x[i], x[i], m[1]);
+          m[2] = fmaf(b, h[i], m[2]);
           m[3] += b;
         }
+        next_piece(c);
       }
       row_sums(m, waves, part[1][ty]);
       if (a.post_norm) rx = 1.f / sqrtf(fmaf(m[1], inv_n, a.eps));
@@ -419,67 +473,87 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (!in[c] || !live) continue;
-        float w[8];
+        float w[8], h[8], gy[8];
         param(0, col[c], w);
+        get_h(c, h), get_gy(c, gy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s_pre[c][i] = fmaf(gy[c][i], h[c][i] * r, s_pre[c][i]);
-          d[c][i] = fmaf(r, fmaf(-along, h[c][i], gy[c][i] * w[i]) - mean, d[c][i]);
+          s_pre[c][i] = fmaf(gy[i], h[i] * r, s_pre[c][i]);
+          d[c][i] = fmaf(r, fmaf(-along, h[i], gy[i] * w[i]) - mean, d[c][i]);
         }
+        next_piece(c);
       }
     }
     float b[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x; x becomes norm(x)
+    for (int c = 0; c < C; ++c) {  // d becomes the gradient of norm(x), or of x
       if (!in[c] || !live) continue;
       if (a.grad_residual) {
         float g[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = a.residual_scale * d[c][i];
-        store8<R>(a.grad_residual, at0 + col[c], g);
+        store8<R>(static_cast<R*>(a.grad_residual) + at0, col[c], g);
       }
-      float w[8];
+      float w[8], x[8];
       param(1, col[c], w);
+      get_x(c, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[c][i] *= rx;
+      for (int i = 0; i < 8; ++i) x[i] *= rx;
       if (a.gate) {
         float u[8], g[8];
         if constexpr (ROW_GATE) param8(a.gate, a.params_bf16, at0 + col[c], g);
         else param(2, col[c], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (x[c][i] * w[i]);
+        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (x[i] * w[i]);
         if constexpr (ROW_GATE) {
-          if (a.grad_gate) store8<float>(a.grad_gate, at0 + col[c], u);
+          if (a.grad_gate) store8<float>(a.grad_gate + at0, col[c], u);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s_gate[c][i] += u[i];
+          for (int i = 0; i < 8 && KEEP; ++i) s_gate[c][i] += u[i];
+          if constexpr (!KEEP) {
+            float t[8];
+            load8(long_sums + n + col[c], t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] += u[i];
+            store8<float>(long_sums, n + col[c], t);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[c][i] *= g[i];
       }
       if (a.post_norm) {
+        float t[8];
+        if constexpr (!KEEP) load8(long_sums + col[c], t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s_post[c][i] = fmaf(d[c][i], x[c][i], s_post[c][i]);
+          float& sum = KEEP ? s_post[c][i] : t[i];
+          sum = fmaf(d[c][i], x[i], sum);
           d[c][i] *= w[i];
-          b[0] = fmaf(d[c][i], x[c][i], b[0]);
+          b[0] = fmaf(d[c][i], x[i], b[0]);
           b[1] += d[c][i];
         }
+        if constexpr (!KEEP) store8<float>(long_sums, col[c], t);
       }
+      next_piece(c);
     }
     if (a.post_norm) {
       row_sums(b, waves, part[2][ty]);
       const float along = b[0] * inv_n, mean = LAYER ? b[1] * inv_n : 0.f;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        float x[8];
+        get_x(c, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] = rx * (fmaf(-along, x[c][i], d[c][i]) - mean);
+        for (int i = 0; i < 8; ++i) d[c][i] = rx * (fmaf(-along, x[i] * rx, d[c][i]) - mean);
+        next_piece(c);
+      }
     }
     if (a.grad_x) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (in[c] && live) store8<X>(a.grad_x, at0 + col[c], d[c]);
+        if (in[c] && live) store8<X>(static_cast<X*>(a.grad_x) + at0, col[c], d[c]);
     }
+    if (!KEEP && row + at_once < last) load(row + at_once);
   }
   if (!a.partial) return;
   float* const out = a.partial + int64_t(blockIdx.x) * 3 * n;
@@ -503,8 +577,21 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
       if (in[c]) store8<float>(out, at + col[c], sum[c]);
   };
   put(s_pre, 0);
-  put(s_post, n);
-  put(s_gate, 2 * int64_t(n));
+  if constexpr (KEEP) {
+    put(s_post, n);
+    put(s_gate, 2 * int64_t(n));
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (!in[c]) continue;
+      float t[8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        load8(long_sums + k * n + col[c], t);
+        store8<float>(out, (k + 1) * int64_t(n) + col[c], t);
+      }
+    }
+  }
 }
 
 }  // namespace fp8g
