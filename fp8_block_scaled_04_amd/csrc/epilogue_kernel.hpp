@@ -10,6 +10,13 @@
 // of rows, and the activation is chosen once per piece in a loop instead of in
 // an unrolled copy for every accumulator.  The 256 x 256 tile, whose FP32 form
 // is twice the ring, goes in two halves.
+//
+// What it adds to the product: the tile's way through LDS and the activation,
+// which no matrix instruction of the workgroup overlaps, and the residual's and
+// the pre-activations' bytes (4096 x 4096 x 7168, GELU_TANH and
+// pre-activations 115 us, the product alone 100; 4001 x 7168 x 16384 with a
+// residual 430 and 415; 64 x 2112 x 7168 split over k, SiLU and a residual 10.4
+// and 9.6).  The residual of the next rows is read while these are written.
 #pragma once
 
 #include "activation.hpp"

@@ -23,7 +23,11 @@
 // 1.41 times that of their own rounding, with this it is 1.01.  The block's
 // scale and the largest exponent go onto the FP32 sum.
 //
-// What bounds it: the matrices are read once, a byte a weight.
+// What bounds it: the matrices are read once, a byte a weight.  64 tokens, 128
+// experts of 7168 x 2048: 626 us for the first kernel (6.0 TB/s) and 278 for the
+// second (6.8); 7 tokens, 16 of 4096 x 2048: 37 and 20.  One token, 8 experts of
+// 2048 x 768: 8.4 and 7.0, of which a launch and the chain of loads up to the
+// first block (the indices, then what they name) are 2.8 and 3.6.
 #pragma once
 
 #include <type_traits>

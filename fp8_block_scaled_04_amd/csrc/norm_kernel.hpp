@@ -204,6 +204,10 @@ __device__ __forceinline__ float normalise(float (&v)[C][8], const bool (&in)[C]
 
 // A thread holds C pieces of 8 columns, blockDim.x threads a row, blockDim.y rows a workgroup (more than one only
 // where a row is one wave's).  Consecutive rows run on one XCD, so that its L2 gathers the lines of the scales.
+//
+// A row is read once and stays in registers.  Many rows are bound by memory: 16384 x 7168 with its codes 172 us, 4.8
+// TB/s; 5003 x 2120 layer norms with an FP32 stream 34 us, 3.7 TB/s (four rounds of sums a row, whose waits the six rows
+// of a CU do not cover quite).  One row of 7168 takes 4.4 us, a launch and the chain of two loads and two sums.
 template <typename X, typename R, bool LAYER, int C>
 __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(const NormArgs a) {
   __shared__ NormPart parts[4];
