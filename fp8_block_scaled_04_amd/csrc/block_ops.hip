@@ -64,21 +64,25 @@ int launch_norm(const NormArgs& a, hipStream_t s) {
 // Rows that a workgroup of the gradients takes at a time: what 512 threads hold, a piece of 8 columns each.
 int grad_rows(int n) { return n > 4096 ? 1 : std::min<int>(fp8g::kNormGradRows, int(512 / (cdiv(n, 512) * 64))); }
 
-template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
+template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS, bool IN_LDS>
 int launch_norm_backward(const NormGradArgs& a, int slices, hipStream_t s) {
   const int threads = int(cdiv(cdiv(a.n / 8, C), 64) * 64), rows = grad_rows(a.n);
   const int of_rows = rows > 1 ? rows * threads * 8 : C > 1 ? 2 * a.n : 0;  // floats: sums of rows, or over them
-  const int lds = std::max(fp8g::norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= rows), 4 * of_rows);
-  hipLaunchKernelGGL((fp8g::norm_residual_backward_kernel<X, R, LAYER, ROW_GATE, C, MAX_THREADS>),
+  const int lds = std::max(IN_LDS ? 3 * a.n : 0, of_rows) * int(sizeof(float));
+  hipLaunchKernelGGL((fp8g::norm_residual_backward_kernel<X, R, LAYER, ROW_GATE, C, MAX_THREADS, IN_LDS>),
                      dim3(unsigned(slices)), dim3(unsigned(threads), unsigned(rows)), lds, s, a);
   return launched();
 }
 
 template <typename X, typename R, bool LAYER, bool ROW_GATE>
 int launch_norm_backward(const NormGradArgs& a, int slices, hipStream_t s) {
-  if (a.n > 8192) return launch_norm_backward<X, R, LAYER, ROW_GATE, 2, 1024>(a, slices, s);
-  if (grad_rows(a.n) == 1) return launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 1024>(a, slices, s);
-  return launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 512>(a, slices, s);
+  if (a.n > 8192) return launch_norm_backward<X, R, LAYER, ROW_GATE, 2, 1024, false>(a, slices, s);
+  const bool again = a.rows_per_slice > grad_rows(a.n);  // more than one round: the parameters are read again
+  if (grad_rows(a.n) == 1)
+    return again ? launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 1024, true>(a, slices, s)
+                 : launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 1024, false>(a, slices, s);
+  return again ? launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 512, true>(a, slices, s)
+               : launch_norm_backward<X, R, LAYER, ROW_GATE, 1, 512, false>(a, slices, s);
 }
 
 // Rows of a slice and slices of a gradient's pass.

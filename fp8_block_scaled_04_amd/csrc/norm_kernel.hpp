@@ -315,32 +315,18 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 //
 // Bound by memory: six tensors a row, 8192 x 4096 at 4.0 TB/s, 16 waves a CU and the sums of 256 or 512 slices.
 constexpr int kNormGradRows = 8;  // rows at a time, at most
-__host__ __device__ inline int norm_param_lds(int n, bool params_bf16, bool one_round) {
-  return n <= 8192 && !one_round ? 3 * n * (params_bf16 ? 2 : 4) : 0;
-}
-template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS>
+template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS, bool IN_LDS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
   constexpr bool SEVERAL = C == 1 && MAX_THREADS == 512;  // rows at a time, perhaps
   __shared__ NormPart parts[2][3][SEVERAL ? kNormGradRows : 1];
   const int ty = SEVERAL ? uniform(threadIdx.y) : 0, at_once = SEVERAL ? blockDim.y : 1;
-  extern __shared__ __attribute__((aligned(16))) char params[];  // pre_weight, post_weight, gate, as they are stored
+  extern __shared__ __attribute__((aligned(16))) float params[];  // IN_LDS: pre_weight, post_weight, gate
   const int tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * at_once;
   constexpr bool KEEP = C == 1;  // what is unpacked, and the sums, stay in registers
-  const int row_bytes = a.n * (a.params_bf16 ? 2 : 4);
-  const bool in_lds = KEEP && norm_param_lds(a.n, a.params_bf16, a.rows_per_slice <= at_once) != 0;
   const void* const shared[3] = {a.pre_weight, a.post_weight, ROW_GATE ? nullptr : a.gate};
-  auto param = [&](int k, unsigned c, float v[8]) {
-    if (in_lds) {
-      const char* at = params + k * row_bytes + c * (a.params_bf16 ? 2 : 4);
-      RawParam r;
-      if (shared[k]) {
-        r.w[0] = *reinterpret_cast<const uint4*>(at);
-        if (!a.params_bf16) r.w[1] = *reinterpret_cast<const uint4*>(at + 16);
-      }
-      r.get(shared[k], a.params_bf16, v);
-    } else {
-      param8(shared[k], a.params_bf16, c, v);
-    }
+  auto param = [&](int k, unsigned c, float (&v)[8]) {
+    if constexpr (IN_LDS) load8(params + k * a.n + c, v);
+    else param8(shared[k], a.params_bf16, c, v);
   };
   const int waves = blockDim.x >> 6, n = a.n;
   const float inv_n = 1.f / n;
@@ -352,7 +338,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
     in[c] = int(col[c]) < n;
   }
   float s_pre[C][8] = {}, s_post[KEEP ? C : 1][8] = {}, s_gate[KEEP ? C : 1][8] = {};
-  float* const long_sums = reinterpret_cast<float*>(params);  // !KEEP: post_weight's, gate's
+  float* const long_sums = params;  // !KEEP: post_weight's, gate's
   if constexpr (!KEEP) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -377,13 +363,14 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
 #pragma unroll
   for (int c = 0; c < C; ++c) xs[c].clear(), gys[c].clear(), hs[c].clear(), ghs[c].clear();
   if (first + ty < last) load(first + ty);
-  if (in_lds) {
+  if constexpr (IN_LDS) {
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (shared[k])
-        for (int i = tid * 16; i < row_bytes; i += threads * 16)
-          *reinterpret_cast<uint4*>(params + k * row_bytes + i) =
-              *reinterpret_cast<const uint4*>(static_cast<const char*>(shared[k]) + i);
+      for (int i = tid * 8; i < n; i += threads * 8) {
+        float v[8];
+        param8(shared[k], a.params_bf16, i, v);
+        store8<float>(params, k * n + i, v);
+      }
     __syncthreads();
   }
   int turn = 0;
@@ -563,7 +550,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
   float* const out = a.partial + int64_t(blockIdx.x) * 3 * n;
   auto put = [&](float (&sum)[C][8], int64_t at) {
     if (SEVERAL && at_once > 1) {  // the rows' sums in order
-      float* const mine = reinterpret_cast<float*>(params) + threadIdx.x * 8;
+      float* const mine = params + threadIdx.x * 8;
       static_assert(C == 1 || !SEVERAL, "several rows at a time have a piece a thread");
       __syncthreads();
       store8<float>(mine + ty * blockDim.x * 8, 0, sum[0]);
