@@ -307,13 +307,15 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_residual_kernel(cons
 // What a row needs of itself takes two rounds of sums (three for layer norms, whose squares are of centred values):
 //   sum h^2, sum a h, sum x^2  ->  dh  ->  sum b x,  b = du post_weight
 // The next row is read while this one is worked on, which works because nothing else is read meanwhile: memory answers
-// in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS (8192 x 4096
-// with its sums 99 us, 107 without), but for a workgroup that has no next row (257 x 2048: 11.7 us, 12.5 with them there).
+// in order, so a wait for a parameter would be one for the next row.  The parameters therefore lie in LDS, as FP32
+// (8192 x 4096 with its sums 95 us; 101 as they are stored, chosen and unpacked at every use; 107 from memory), but for a
+// workgroup that has no next row (257 x 2048: 11.7 us, 12.5 with them there).
 // Rows of more than 8192 columns (two pieces a thread) leave no registers for the next row: their threads keep only
 // what is packed, d and one of the three sums, the other two lie in LDS, and the parameters come from the cache
 // (2048 x 12288: 106 us; all in registers, which spilled, 219).
 //
-// Bound by memory: six tensors a row, 8192 x 4096 at 4.0 TB/s, 16 waves a CU and the sums of 256 or 512 slices.
+// Bound by memory, and nearly by vector instructions (some 300 for a thread's 8 columns): 8192 x 4096 at 4.5 TB/s in 90
+// us, 16 waves a CU, and 5 for the sums of 256 or 512 slices.
 constexpr int kNormGradRows = 8;  // rows at a time, at most
 template <typename X, typename R, bool LAYER, bool ROW_GATE, int C, int MAX_THREADS, bool IN_LDS>
 __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(const NormGradArgs a) {
@@ -387,6 +389,9 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_residual_backward_kernel(con
     if constexpr (KEEP) xs[0].get(x_[0]), hs[0].get(h_[0]), gys[0].get(gy_[0]);
 #pragma unroll
     for (int c = 0; c < C; ++c) ghs[c].get(d[c]);
+    if constexpr (KEEP)  // unpacked here: put off past the next row's loads, it takes a copy of what is packed
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(x_[0][i]), "+v"(h_[0][i]), "+v"(gy_[0][i]), "+v"(d[0][i]));
     if (KEEP && row + at_once < last) load(row + at_once);
     auto get_x = [&](int c, float (&v)[8]) {
 #pragma unroll
