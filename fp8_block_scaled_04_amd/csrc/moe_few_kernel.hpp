@@ -17,11 +17,14 @@
 // are BF16, as x is, times 2^-16: then no sum of a block's 128 products passes
 // FP32's range where its scaled value does not.  The second's are FP16: mid is
 // kept as FP16 values with an exponent for each 16 of a pair's columns, which
-// the first kernel finds where it forms them.  So mid is off by 2^-12 of its
-// value (2^-24 of the largest of 128 neighbours where that is more), an eighth
-// of what BF16 would cost in the same bytes: with BF16 the outputs' error was
-// 1.41 times that of their own rounding, with this it is 1.01.  The block's
-// scale and the largest exponent go onto the FP32 sum.
+// the first kernel finds where it forms them, and brought to the largest exponent
+// of a block where it is read.  So mid is off by 2^-11 of its value, an eighth of
+// what BF16 would cost in the same bytes, and by 2^-37 of the largest of 128
+// neighbours where that is more: a single large channel, as gated feed-forward
+// networks have them, leaves its neighbours as they are even where the second
+// matrix has nothing for it.  With BF16 the outputs' error was 1.41 times that of
+// their own rounding, with this it is 1.01.  The block's scale and the largest
+// exponent go onto the FP32 sum.
 //
 // What bounds it: the matrices are read once, a byte a weight.  64 tokens, 128
 // experts of 7168 x 2048: 626 us for the first kernel (6.0 TB/s) and 278 for the
@@ -80,6 +83,12 @@ __device__ __forceinline__ v4i few_decode(int lo, int hi) {
     f[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(hi), s, true));
   }
   return f;
+}
+
+// 2^d for d <= 0 as FP16: below 2^-14 one of its subnormal numbers, below 2^-24 0.
+__device__ __forceinline__ _Float16 few_power(int d) {
+  const int bits = d >= -14 ? (d + 15) << 10 : d >= -24 ? 1 << (d + 24) : 0;
+  return __builtin_bit_cast(_Float16, uint16_t(bits));
 }
 
 // Workgroup barrier after this wave's LDS accesses; copies to LDS stay in flight.
@@ -485,18 +494,22 @@ struct FewStream {
     b.exponent = 0;
     if constexpr (MID) {
       // The lane's activations, 32 columns from 32 q on, are of the groups 2 q and 2 q + 1: brought to the token's
-      // largest exponent.  (Under 2^-14 of it: 0.)
+      // largest exponent.  One power of two takes a group down by 2^-14 and, where a lane has one farther down, another by
+      // 2^-24 more (under that: 0).  (Both for every block: 64 tokens, 128 experts of 7168 x 2048 965 us, 918 so.)
       int top = -128, own[2];
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, int(exponents[i / 4] << (24 - 8 * (i & 3))) >> 24);
       const int word = q & 2 ? exponents[1] : exponents[0], half = q & 1 ? word >> 16 : word;
       own[0] = int(unsigned(half) << 24) >> 24, own[1] = int(unsigned(half) << 16) >> 24;
       b.exponent = top;
+      auto times = [&](int j, _Float16 by) {
+        x[j] = __builtin_bit_cast(v4i, __builtin_bit_cast(v8f16_t, x[j]) * by);
+      };
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = own[j / 2] - top;
-        const uint16_t by = d < -14 ? 0 : uint16_t((d + 15) << 10);  // 2^d
-        x[j] = __builtin_bit_cast(v4i, __builtin_bit_cast(v8f16_t, x[j]) * __builtin_bit_cast(_Float16, by));
+      for (int j = 0; j < 4; ++j) times(j, few_power(max(own[j / 2] - top, -14)));
+      if (__any(min(own[0], own[1]) - top < -14)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) times(j, few_power(min(own[j / 2] - top + 14, 0)));
       }
     }
 #pragma unroll

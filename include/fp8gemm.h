@@ -584,10 +584,13 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
                                float* grad_gate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* A mixture-of-experts layer for a few tokens (a decoding step), in two kernels:
- *   mid[p] = bf16(act(G x_t) * (U x_t)),  out[t] = bf16(sum over j of weights[p] * (D mid[p]))
+ *   mid[p] = act(G x_t) * (U x_t),  out[t] = bf16(sum over j of weights[p] * (D mid[p]))
  * for pair p = t * topk + j with the matrices of expert expert_idx[p], FP8 E4M3
  * codes and block scales as fp8_grouped_gemm_contiguous takes them (so a layer's
- * prefill and decode share one copy); the activations stay BF16.
+ * prefill and decode share one copy).  x stays BF16; mid is formed in FP32 and
+ * kept as FP16 values with an exponent for each 16 columns: a value is off by
+ * 2^-11 of itself, or by 2^-37 of the largest of its block of 128 columns (from
+ * a multiple of 128 on) where that is more.
  *   x          [num_tokens][hidden] BF16, row stride x_ld >= hidden, x_ld % 8 == 0
  *   expert_idx [num_tokens][topk] int32; a pair with an index outside [0,
  *              num_experts) adds nothing, and a token without any other has a row of
