@@ -38,11 +38,16 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float v[8]) {
 
 template <>
 struct EpilogueOf<kDenseEpilogue> {
+  // What stands for a bias or residual that is not there: -0, to which any sum adds without a change (0 would make of a
+  // sum of -0 a 0).
+  static constexpr float kNone = -0.f;
+  static constexpr uint32_t kNone2 = 0x80008000u;  // two of BF16
+
   // N (4 or 8) consecutive values of the bias, from column `col` on.
   template <int N>
   static __device__ __forceinline__ void load_bias(const GemmParams& p, int col, float (&b)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = 0.f;
+    for (int i = 0; i < N; ++i) b[i] = kNone;
     if (!p.bias) return;
     if (p.bias_bf16) {
       const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + col);
@@ -69,7 +74,7 @@ struct EpilogueOf<kDenseEpilogue> {
     uint2 r;
     __device__ __forceinline__ void load(const GemmParams& p, int64_t at, int col) {
       load_bias(p, col, b);
-      r = make_uint2(0, 0);
+      r = make_uint2(kNone2, kNone2);
       if (p.residual) r = *reinterpret_cast<const uint2*>(p.residual + at);
     }
     __device__ __forceinline__ void store(const GemmParams& p, const v4f& sum, int64_t at) const {
@@ -109,7 +114,9 @@ struct EpilogueOf<kDenseEpilogue> {
       const int first = pass * PR, last = min(PR, rows - m0 - first);  // rows of this pass
       const int64_t at0 = int64_t(m0 + first) * shape_n + col;
       const bool work = in && r0 < last;
-      uint4 next[AHEAD] = {};
+      uint4 next[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) next[u] = make_uint4(kNone2, kNone2, kNone2, kNone2);
       auto load = [&](int r) {  // of the residual; rows past the end: the last one again
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
