@@ -943,7 +943,9 @@ def fp8_w4_matvec_experts(x, expert_idx, w, scales, out, w_format=FP8G_INT4, zer
 
 # ---- the feed-forward block around the products ------------------------------------------
 def _ws(workspace, needed, device):
-    """(address, bytes) of a workspace of the given device, allocated where none is given and one is needed."""
+    """(address, bytes, the tensor) of a workspace of the given device, allocated where none is given and one is needed.
+    A call that has to be given one and is not does not go through _direct: with the allocation it takes 14 to 20 us
+    on the host instead of 8 to 9."""
     if workspace is None:
         if not needed:
             return None, 0, None
@@ -1046,8 +1048,8 @@ def fp8_norm_residual(x, residual=None, h=None, y=None, q=None, q_scales=None, *
     residual_scale * residual + gate * u, y = norm(h) * pre_weight.  x, y
     [T][n] float32 or bfloat16; residual, h [T][n] float32 or bfloat16; q
     [T][n] the FP8 codes of y with q_scales [KG][ld >= T]; gate [n], [1][n] or
-    [T][n]; x and residual rows may be strided.  Outputs not given are not
-    computed.  Returns (h, y, q, q_scales)."""
+    [T][n]; x and residual rows may be strided.  Layer norms have no shift.
+    Outputs not given are not computed.  Returns (h, y, q, q_scales)."""
     if _direct and stream is None:
         st = _direct.norm_residual(x, residual, h, y, q, q_scales, pre_weight, post_norm, post_weight, gate,
                                    residual_scale, kind, eps, q_format)

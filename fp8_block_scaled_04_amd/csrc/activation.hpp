@@ -4,9 +4,9 @@
 //   GELU      z Phi(z), Phi the normal distribution's function
 //   GELU_TANH z (1 + tanh a) / 2 = z s(2 a),       a = sqrt(2 / pi) (z + 0.044715 z^3)
 // Nothing here cancels, so the left tails keep their relative precision (what
-// 1 + erf or 1 + tanh would lose there).  The logistic function is the
-// reciprocal of 1 + e^-v as it stands: e^-v past FP32's range gives 0, which is
-// what the function is there.  Phi(-z) for z >= 0 is e^(-z^2 / 2) R(t), t = 1 /
+// 1 + erf or 1 + tanh would lose there) down to values of 1e-36; what is smaller
+// may come out as 0, since the logistic function is the reciprocal of 1 + e^-v as
+// it stands and the hardware's reciprocal has no subnormal results.  Phi(-z) for z >= 0 is e^(-z^2 / 2) R(t), t = 1 /
 // (1 + 0.3 z), R a polynomial fitted to e^(z^2 / 2) erfc(z / sqrt 2) / 2 for the
 // least relative error (1.6e-7 on 0 <= z <= 14.5, 5e-7 as FP32 forms it).  An
 // infinity gives the limit (0 or itself) because what is multiplied is cut off

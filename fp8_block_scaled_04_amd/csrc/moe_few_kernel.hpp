@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(WAVES* kWave) moe_few_down_kernel(const MoeFew
     for (int i = lane; i < a.tokens * kRows; i += kWave) sums.v[wave][i / kRows][i % kRows] = 0.f;
   few_plan<TX, WAVES>(a, lds.plan, *reinterpret_cast<FewPlanScratch<Plan::kPairs>*>(lds.ring));
   const int row0 = blockIdx.x * kRows, kg = a.inter / kGroupK, sets = a.inter / kFewGroup;
-  const int all = uniform(plan.tiles) * kg;  // (at most 1024 tiles of 512 blocks)
+  const int all = uniform(plan.tiles) * kg;  // (at most 512 tiles of 512 blocks)
   const int slices = gridDim.y, run = blockIdx.y * WAVES + wave;
   const int f0 = int(int64_t(all) * run / (slices * WAVES)), f1 = int(int64_t(all) * (run + 1) / (slices * WAVES));
   struct Units {

@@ -536,7 +536,8 @@ enum { FP8G_NORM_RMS = 0, FP8G_NORM_LAYER = 1 };
  *   norm(v) = v / sqrt(mean(v^2) + eps)            (FP8G_NORM_RMS)
  *             (v - mean(v)) / sqrt(var(v) + eps)   (FP8G_NORM_LAYER)
  * in FP32, every output rounded once (y and the codes from h before it is
- * rounded).
+ * rounded).  Layer norms have a weight and no shift: y plus a shift is the
+ * caller's to form, and its codes the cast's (fp8_cast_per_token_group).
  *   x         [num_rows][n] FP32 or BF16 (x_dtype), row stride x_ld >= n
  *   residual  [num_rows][n] FP32 or BF16 (stream_dtype), row stride residual_ld
  *             >= n, or NULL (h = gate * u; residual_scale is then not used)
@@ -551,7 +552,8 @@ enum { FP8G_NORM_RMS = 0, FP8G_NORM_LAYER = 1 };
  * At least one of h, y and q.  Strides are multiples of 8, n % 8 == 0 and n <=
  * 16384, num_rows < 2^22 (n <= 512: four times that), FP8G_EUNSUPPORTED
  * otherwise; tensors 16-byte aligned.  Sums of squares are FP32: rows of values
- * above 1e18 come out as zeros. */
+ * above 1e18 come out as zeros, and with eps 0 rows of values below 1e-19 lose
+ * precision (below 1e-23 they come out infinite). */
 int fp8_norm_residual(const void* x, int x_dtype, int64_t x_ld, const void* residual, int64_t residual_ld,
                       int stream_dtype, int num_rows, int n, int kind, float eps, int post_norm,
                       const void* post_weight, const void* gate, int gate_rows, float residual_scale,
@@ -603,12 +605,14 @@ int fp8_norm_residual_backward(const void* grad_h, const void* grad_y, const voi
  *   out        [num_tokens][hidden] BF16 (written in full)
  *   workspace  fp8_moe_few_tokens_workspace_bytes() bytes, uninitialised, not shared
  *              by concurrent calls; FP8G_EINVAL without it
- * Any number of tokens, min(64, 512 / topk) at a time: an expert's matrices are
- * read once for up to 16 of its pairs, so beyond a few hundred pairs the grouped
- * GEMMs are the way.  hidden % 128 == 0 and inter % 128 == 0, both <= 65536, inter
- * > 0, topk <= 32, num_experts <= 4096 (FP8G_EUNSUPPORTED otherwise).  Tensors
- * 16-byte aligned (expert_idx, weights 4).  A token's sum goes over its experts in a
- * fixed order: equal calls give equal bits. */
+ * Any number of tokens, min(64, 512 / topk) at a time, each time reading the
+ * matrices anew (and once more for every 16 of an expert's pairs): one such pass
+ * takes 0.4 to 0.7 of the time of the grouped GEMMs with the steps around them
+ * (casts, layout, activation, combine), two passes 0.9 to 1.3, and from three on
+ * the grouped GEMMs are faster.  hidden % 128 == 0 and inter % 128 == 0, both <=
+ * 65536, inter > 0, topk <= 32, num_experts <= 4096 (FP8G_EUNSUPPORTED otherwise).
+ * Tensors 16-byte aligned (expert_idx, weights 4).  A token's sum goes over its
+ * experts in a fixed order: equal calls give equal bits. */
 size_t fp8_moe_few_tokens_workspace_bytes(int num_tokens, int topk, int hidden, int inter);
 int fp8_moe_few_tokens(const uint16_t* x, int64_t x_ld, const int32_t* expert_idx, const float* weights,
                        int num_tokens, int topk, const uint8_t* up, const float* up_scales, const uint8_t* down,
